@@ -267,6 +267,61 @@ lora_status lora_fwd_static_scratch(const lora_bf16* X, const lora_bf16* W, cons
                                     float alpha, float p, uint64_t seed, int64_t m, int64_t k, int64_t n, int32_t r,
                                     lora_bf16* Y, lora_bf16* S_saved, uint8_t* mask_bits, void* stream);
 
+/* Causal softmax attention over packed sequences with grouped heads: what stands between the q, k and v projections
+ * and the o projection of a layer (the packed batches of lora_pack_greedy and the multi-adapter calls).
+ *
+ *   S = scale Q K^T,  query i of a sequence sees its keys j <= i + (k_rows - q_rows),
+ *   lse_i = log sum_j exp(S_ij),   O_i = sum_j exp(S_ij - lse_i) V_j
+ *
+ * Q is q_rows x q_heads x head_dim, K and V are k_rows x kv_heads x head_dim, bf16; query head h uses key/value head
+ * h / (q_heads / kv_heads).  A sequence may have fewer queries than keys (the last q_rows tokens of a longer prompt,
+ * down to a single token) or more (its first rows see no key).  A row that sees no key gets O = 0 and lse = -inf, and
+ * its gradients are zero.
+ *  - Strides are in elements and multiples of 8, the features of a head are contiguous, and no element may have two
+ *    places (rows of heads or heads of rows, with any padding: a slice of a fused projection's output is fine).
+ *  - head_dim is a multiple of 8 up to 128, q_heads <= 1024 and a multiple of kv_heads, at most 262144 rows.
+ *  - seqs is a HOST array, read before the call returns: q_start and k_start do not decrease and no two sequences
+ *    share a row (LORA_ETABLE).  Rows of no sequence are never read; they get O = 0, lse = -inf, dQ = dK = dV = 0.
+ *  - A sequence's results depend on its own rows only, whatever lies beside it.  Within a sequence a K, V or dO that
+ *    is infinite or NaN may reach rows that do not see it.
+ *  - P and dS are rounded to bf16 for their products with V, K, Q and dO; everything else is fp32 until the outputs.
+ *    Every sum has a fixed order: results are bit-identical from call to call in both reduction modes.
+ *  - workspace: attn_workspace_size() bytes for attn_bwd, 256 for attn_fwd; 256-byte aligned.  Its first 256 bytes
+ *    (the device status word) are zero before the first use and stay so; the rest is scratch whose contents do not
+ *    matter, so it is no workspace for the calls above. */
+enum { LORA_ATTN_MAX_SEQS = 1024, LORA_ATTN_MAX_HEADS = 1024, LORA_ATTN_MAX_HEAD_DIM = 128 };
+
+typedef struct {
+    int64_t q_start, q_rows;
+    int64_t k_start, k_rows;
+} lora_attn_seq;
+
+typedef struct {
+    int64_t row, head; /* elements from one row to the next, from one head to the next */
+} lora_attn_strides;
+
+typedef struct {
+    int64_t q_rows, k_rows;
+    int32_t q_heads, kv_heads, head_dim;
+    float scale; /* positive and finite */
+    lora_attn_strides q, k, v, o;
+    lora_attn_strides d_o, d_q, d_k, d_v; /* attn_bwd only */
+} lora_attn_shape;
+
+size_t attn_workspace_size(int64_t q_rows, int32_t q_heads);
+
+/* Forward: writes O (strides shape->o) and lse (q_rows x q_heads, fp32, contiguous). */
+lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const lora_attn_shape* shape,
+                     const lora_attn_seq* seqs, int32_t n_seqs, lora_bf16* O, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Backward: from dO and the forward's Q, K, V, O and lse the gradients dQ, dK, dV (overwritten; dK and dV summed over
+ * the query heads that share them). */
+lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
+                     const lora_bf16* O, const float* lse, const lora_attn_shape* shape, const lora_attn_seq* seqs,
+                     int32_t n_seqs, lora_bf16* dQ, lora_bf16* dK, lora_bf16* dV, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
 /* Host only, no GPU needed: the routing table.  tile_adapter[i] (i < ceil(m/128))
  * receives the adapter of tile i, -1 where no segment covers it. */
 lora_status lora_tile_table(const lora_segment* segments, int32_t n_segments, int32_t n_adapters, int64_t m,
@@ -334,11 +389,13 @@ const char* lora_status_string(lora_status s);
  * time in ms and the number of launches.  Kinds: 0 down-projection,
  * 1 finalize S, 2 forward GEMM, 3 dS/dB, 4 finalize dS/dB, 5 backward GEMM,
  * 6 dA, 7 finalize dA, 8 memset (gradients of adapters that own no rows),
- * 9-12 DoRA (U, norm, dZ, dmag).  When kind 6 runs on the library's side
+ * 9-12 DoRA (U, norm, dZ, dmag), 13-18 attention
+ * (forward, joining of split rows, delta, dQ, dK and dV, unused rows),
+ * 19-22 losses (rows, pairs, gradient, sum), 23 AdamW.  When kind 6 runs on the library's side
  * stream beside the backward GEMM, its event pair spans from the fork to its
  * end.
  * Host-side cost: two event records per launch. */
-enum { LORA_KERNEL_KINDS = 13 };
+enum { LORA_KERNEL_KINDS = 24 };
 lora_status lora_timing_begin(void);
 lora_status lora_timing_end(float* total_ms, int32_t* launches, int32_t n_kinds);
 const char* lora_kernel_name(int32_t kind);

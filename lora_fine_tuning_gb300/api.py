@@ -274,6 +274,142 @@ def dora_bwd(dY, X, W, A, B, S_saved, Y, mag, g_saved, alpha: float, p: float, s
     return dX, dA, dB, dmag
 
 
+# ---------------------------------------------------------------------------------------------------------------
+# packed causal attention
+# ---------------------------------------------------------------------------------------------------------------
+
+_STREAM_WS: dict = {}
+
+
+class _On:
+    """Allocates on the device of `t` and for the stream the call runs on: the caching allocator then hands the
+    memory to nobody else before that stream is done with it."""
+
+    def __init__(self, t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.device = t.device
+        self.stream = stream
+        self.handle = _stream(stream)
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, kind: str, size: int) -> torch.Tensor:
+        """A cached workspace of this stream (calls on different streams may overlap), zeroed when it is made."""
+        key = (kind, self.device.index, self.handle)
+        ws = _STREAM_WS.get(key)
+        if ws is None or ws.numel() < size:
+            size = max(256, 1 << (size - 1).bit_length())
+            if self.stream is None:
+                ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(self.stream):
+                    ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
+            _STREAM_WS[key] = ws
+        return ws
+
+
+class AttnSeqs:
+    """The sequences of a packed batch: (q_start, q_rows, k_start, k_rows) each, in row order.  Made once and used by
+    every layer's attention."""
+
+    def __init__(self, seqs):
+        self.seqs = [tuple(int(x) for x in s) for s in seqs]
+        if any(len(s) != 4 for s in self.seqs):
+            raise ValueError("each sequence is (q_start, q_rows, k_start, k_rows)")
+        self.array = native.attn_seqs_array(self.seqs)
+
+    def __len__(self):
+        return len(self.seqs)
+
+
+def attn_seqs(seqs) -> AttnSeqs:
+    """A table of packed sequences from (q_start, q_rows, k_start, k_rows) tuples; (start, rows) pairs stand for
+    sequences whose queries and keys are the same rows."""
+    if isinstance(seqs, AttnSeqs):
+        return seqs
+    return AttnSeqs([(s[0], s[1], s[0], s[1]) if len(s) == 2 else s for s in seqs])
+
+
+def _check_heads(name: str, t: torch.Tensor, shape) -> None:
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"the features of a head of {name} must be contiguous")
+
+
+def _attn_shape(Q, K, V, O, scale):
+    if Q.dim() != 3 or K.dim() != 3 or V.dim() != 3:
+        raise ValueError("Q, K and V are rows x heads x head_dim")
+    (q_rows, q_heads, d), (k_rows, kv_heads, _) = Q.shape, K.shape
+    _check_heads("Q", Q, (q_rows, q_heads, d))
+    _check_heads("K", K, (k_rows, kv_heads, d))
+    _check_heads("V", V, (k_rows, kv_heads, d))
+    _check_heads("O", O, (q_rows, q_heads, d))
+    s = native.AttnShape(q_rows, k_rows, q_heads, kv_heads, d, d ** -0.5 if scale is None else float(scale))
+    for field, t in (("q", Q), ("k", K), ("v", V), ("o", O)):
+        _set_strides(s, field, t)
+    return s
+
+
+def _set_strides(shape, field: str, t: torch.Tensor) -> None:
+    m = getattr(shape, field)   # the stride of an extent of one is never used, and torch lets it be anything
+    m.row, m.head = (t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+
+
+def _check_lse(lse, q_rows: int, q_heads: int) -> None:
+    if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or tuple(lse.shape) != (q_rows, q_heads):
+        raise ValueError(f"lse must be a contiguous CUDA float32 tensor of shape {(q_rows, q_heads)}")
+
+
+def attn_fwd(Q, K, V, seqs, *, scale: Optional[float] = None, O=None, lse=None, ws=None, stream=None):
+    """Causal attention of packed sequences with grouped heads.  Q: rows x q_heads x head_dim, K and V: rows x
+    kv_heads x head_dim (strided slices of a fused projection are fine); seqs: attn_seqs(...) or what it takes; scale:
+    1/sqrt(head_dim) if not given.  Returns (O, lse), lse the fp32 log-sum-exp of each row and head."""
+    seqs = attn_seqs(seqs)
+    on = _On(Q, stream)
+    O = O if O is not None else on.empty(Q.shape, torch.bfloat16)
+    shape = _attn_shape(Q, K, V, O, scale)
+    lse = lse if lse is not None else on.empty(Q.shape[:2], torch.float32)
+    _check_lse(lse, Q.shape[0], Q.shape[1])
+    ws = ws if ws is not None else on.workspace("attn", 256)
+    st = native.lib().attn_fwd(_ptr(Q), _ptr(K), _ptr(V), ctypes.byref(shape), seqs.array, len(seqs), _ptr(O),
+                               _ptr(lse), _ptr(ws), ws.numel(), on.handle)
+    native.check("attn_fwd", st)
+    return O, lse
+
+
+def attn_bwd(dO, Q, K, V, O, lse, seqs, *, scale: Optional[float] = None, dQ=None, dK=None, dV=None, ws=None,
+             stream=None):
+    """Gradients of attn_fwd from dO and its O and lse.  Returns (dQ, dK, dV); dK and dV are summed over the query
+    heads that share them."""
+    seqs = attn_seqs(seqs)
+    on = _On(Q, stream)
+    dQ = dQ if dQ is not None else on.empty(Q.shape, torch.bfloat16)
+    dK = dK if dK is not None else on.empty(K.shape, torch.bfloat16)
+    dV = dV if dV is not None else on.empty(V.shape, torch.bfloat16)
+    shape = _attn_shape(Q, K, V, O, scale)
+    for name, field, t, like in (("dO", "d_o", dO, Q), ("dQ", "d_q", dQ, Q), ("dK", "d_k", dK, K), ("dV", "d_v", dV, V)):
+        _check_heads(name, t, like.shape)
+        _set_strides(shape, field, t)
+    _check_lse(lse, Q.shape[0], Q.shape[1])
+    ws = ws if ws is not None else on.workspace("attn", attn_workspace_size(Q.shape[0], Q.shape[1]))
+    st = native.lib().attn_bwd(_ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), ctypes.byref(shape),
+                               seqs.array, len(seqs), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), on.handle)
+    native.check("attn_bwd", st)
+    return dQ, dK, dV
+
+
+def attn_workspace_size(q_rows: int, q_heads: int) -> int:
+    return int(native.lib().attn_workspace_size(q_rows, q_heads))
+
+
 def lora_device_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream; returns the raw device status code of the workspace (0 = fine) and clears it."""
     code = ctypes.c_int32(0)

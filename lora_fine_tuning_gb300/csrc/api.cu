@@ -10,8 +10,11 @@
 #include <mutex>
 #include <vector>
 
+#include "attn.h"
+#include "host.h"
 #include "kernels.h"
 #include "lora.h"
+#include "optim.h"
 #include "plan.h"
 
 namespace lora {
@@ -42,11 +45,16 @@ struct SideStream {
 std::mutex g_mu;
 thread_local const char* g_last_error = "no error";
 
+}  // namespace
+
 bool cuda_ok(cudaError_t e) {
     if (e == cudaSuccess) return true;
     g_last_error = cudaGetErrorString(e);
     return false;
 }
+
+namespace {
+
 DeviceState g_dev[64];
 uint64_t g_wait_ns = 2000000000ull;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -55,13 +63,11 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 // optional per-kernel timing (measurement tools): events around each launch
 // ---------------------------------------------------------------------------
 
-enum Kind : int {
-    kDownProj = 0, kFinalizeS, kGemmFwd, kDsDb, kFinalize, kGemmBwd, kDa, kFinalizeDa, kMemset,
-    kDoraU, kDoraNorm, kDoraDz, kDoraDmag, kKinds
-};
 const char* const kKindNames[kKinds] = {"down_proj", "finalize_s", "gemm_fwd", "ds_db", "finalize_ds_db",
                                         "gemm_bwd", "da", "finalize_da", "memset",
-                                        "dora_u", "dora_norm", "dora_dz", "dora_dmag"};
+                                        "dora_u", "dora_norm", "dora_dz", "dora_dmag",
+                                        "attn_fwd", "attn_join", "attn_delta", "attn_dq", "attn_dkdv", "attn_fill",
+                                        "loss_rows", "loss_pairs", "loss_grad", "loss_sum", "adamw"};
 
 struct TimingRec {
     int kind;
@@ -82,18 +88,20 @@ cudaEvent_t pool_event() {
     return g_event_pool[g_pool_next++];
 }
 
-// Runs `launch` (which enqueues work on `s`); when timing is on, brackets it with events.
-template <class F>
-cudaError_t timed(int kind, cudaStream_t s, F&& launch) {
-    if (!g_timing_on) return launch();
+}  // namespace
+
+cudaError_t timed_call(int kind, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx) {
+    if (!g_timing_on) return launch(ctx);
     std::lock_guard<std::mutex> lock(g_timing_mu);
     cudaEvent_t a = pool_event(), b = pool_event();
     if (a) cudaEventRecord(a, s);
-    const cudaError_t e = launch();
+    const cudaError_t e = launch(ctx);
     if (b) cudaEventRecord(b, s);
     if (a && b) g_timing.push_back(TimingRec{kind, a, b});
     return e;
 }
+
+uint64_t wait_limit_ns() { return g_wait_ns; }
 
 lora_status device_setup(int* sms_out) {
     int dev = 0;
@@ -113,7 +121,8 @@ lora_status device_setup(int* sms_out) {
             d.sms = sms;
             if (!cuda_ok(down_configure()) || !cuda_ok(gemm2_configure()) ||
                 !cuda_ok(dsdb_configure()) ||
-                !cuda_ok(da_configure()) || !cuda_ok(dora_configure()))
+                !cuda_ok(da_configure()) || !cuda_ok(dora_configure()) || !cuda_ok(attn_fwd_configure()) ||
+                !cuda_ok(attn_bwd_configure()))
                 d.status = LORA_ECUDA;
         }
         if (d.status == LORA_OK && g_encode == nullptr) {
@@ -132,6 +141,24 @@ lora_status device_setup(int* sms_out) {
     *sms_out = d.sms;
     return LORA_OK;
 }
+
+bool make_map_heads(CUtensorMap* map, const void* base, int d, int heads, int64_t rows, int64_t head_stride,
+                    int64_t row_stride, int box_heads, int box_rows) {
+    // a stride of an extent of one is never used, but the encoder wants it to be a legal one
+    const int64_t hs = heads > 1 ? head_stride : (d + 7) / 8 * 8;
+    const int64_t rs = rows > 1 ? row_stride : (d + 7) / 8 * 8;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(rs) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) g_last_error = "cuTensorMapEncodeTiled rejected a tensor map";
+    return r == CUDA_SUCCESS;
+}
+
+namespace {
 
 std::vector<SideStream> g_side;   // guarded by g_mu
 
@@ -196,8 +223,6 @@ CUtensorMapSwizzle rank_swizzle_host(int rpad) {
 // ---------------------------------------------------------------------------
 // validation helpers
 // ---------------------------------------------------------------------------
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int rank_pad(int r) {
     int p = 16;
@@ -429,11 +454,6 @@ GemmSched gemm_plan(const Call& c, GemmParams& g, bool bwd, int bn) {
     g.sk_part = reinterpret_cast<float*>(c.ws + c.L.sk + sk_flag_bytes(c.L.sk_pairs));
     return sc;
 }
-
-#define LORA_CUDA(expr)                          \
-    do {                                         \
-        if (!cuda_ok(expr)) return LORA_ECUDA;   \
-    } while (0)
 
 // DoRA's extra inputs and scratch for one forward (single adapter).
 struct DoraFwd {

@@ -1,0 +1,94 @@
+// Launch plans of the packed attention (k_attn_fwd.cu, k_attn_bwd.cu), filled by attn_api.cu.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "plan.h"
+
+namespace lora {
+
+constexpr int kAttnMaxSeqs = 1024;
+constexpr int kAttnTile = 128;        // rows of a query tile and of a key tile
+
+// One sequence of the batch.  A kernel's work items are numbered sequence by sequence; item0 is the first of this
+// one's (the table is in order of falling work, not of rows).
+struct AttnSeq {
+    int32_t q0, k0;      // first row of the queries, of the keys
+    int32_t ql, kl;      // rows
+    int32_t item0;
+};
+
+// The table travels as a kernel parameter (no device table, no copy); a small batch passes a small one.
+template <int N>
+struct AttnSeqs {
+    AttnSeq s[N];
+};
+constexpr int kAttnFewSeqs = 32;
+
+// A matrix of rows x heads x d in global memory, strides in elements.
+struct AttnMat {
+    uint16_t* p;
+    int64_t row, head;
+};
+
+// Query rows of one key/value head are tiled with the heads of its group: a 128-row tile holds 128 / hp tokens x hp
+// query heads, row = token * hp + head, hp the largest power of two (at most 128) that divides the group.  The g / hp
+// packs of a group are separate tiles.
+struct AttnShape {
+    int32_t n_seqs;
+    int32_t items;
+    int32_t hq, hkv, group;
+    int32_t hp, hp_log2;     // query heads in a tile
+    int32_t packs;           // hq / hp: packs of the whole layer
+    int32_t d, d16;          // head width, rounded up to 16
+    float scale;             // softmax scale
+    float scale_log2;        // scale * log2(e)
+};
+
+struct AttnFwdParams {
+    CUtensorMap mapQ, mapK, mapV;
+    AttnShape sh;
+    AttnMat O;
+    float* lse;              // rows x hq
+    DevCtl ctl;
+};
+
+struct AttnBwdParams {
+    CUtensorMap mapQ, mapK, mapV, mapDO;
+    AttnShape sh;
+    const float* lse;        // rows x hq
+    float* delta;            // rows x hq
+    AttnMat dQ, dK, dV;
+    DevCtl ctl;
+};
+
+struct AttnDeltaParams {
+    const uint16_t *O, *dO;
+    int64_t o_row, o_head, do_row, do_head;
+    int64_t rows;
+    int32_t hq, d;
+    float* delta;
+};
+
+// Rows of the outputs that belong to no sequence: rows [from, to) of up to three matrices get zeros, lse -inf.
+struct AttnGaps {
+    int32_t from[kAttnMaxSeqs + 1], to[kAttnMaxSeqs + 1];
+};
+struct AttnFillParams {
+    AttnMat a, b;            // b.p may be null
+    int32_t heads, d;
+    float* lse;              // may be null
+    int32_t n;
+};
+
+cudaError_t attn_fwd_configure();
+cudaError_t attn_bwd_configure();
+cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+cudaError_t launch_attn_delta(const AttnDeltaParams& p, cudaStream_t stream);
+cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream);
+
+}  // namespace lora

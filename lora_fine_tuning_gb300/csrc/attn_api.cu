@@ -1,0 +1,235 @@
+// C ABI of the packed attention: validation, work items and launches.  See include/lora.h for the contract.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "attn.h"
+#include "host.h"
+
+namespace lora {
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+
+struct Prepared {
+    AttnShape sh;
+    AttnSeqs<kAttnMaxSeqs> order;   // sequences with rows, most keys first
+    int n = 0;
+    AttnGaps q_gaps, k_gaps;
+    int nq_gaps = 0, nk_gaps = 0;
+};
+
+lora_status check_mat(const void* p, const lora_attn_strides& s, int64_t rows, int heads, int d) {
+    if (rows > 0 && !p) return LORA_EINVAL;
+    if (!aligned16(p)) return LORA_EALIGN;
+    if (s.row % 8 || s.head % 8) return LORA_EALIGN;
+    if (s.row < 0 || s.head < 0 || s.row >= (int64_t{1} << 38) || s.head >= (int64_t{1} << 38)) return LORA_ESHAPE;
+    // rows of heads, or heads of rows; either way no element twice
+    const bool by_row = (heads == 1 || s.head >= d) && (rows <= 1 || s.row >= (heads - 1) * (heads == 1 ? 0 : s.head) + d);
+    const bool by_head = (rows <= 1 || s.row >= d) && (heads == 1 || s.head >= (rows - 1) * s.row + d);
+    return by_row || by_head ? LORA_OK : LORA_ESHAPE;
+}
+
+lora_status check_seqs(const lora_attn_seq* seqs, int32_t n, int64_t q_rows, int64_t k_rows, Prepared& c) {
+    if (n < 0 || n > LORA_ATTN_MAX_SEQS) return LORA_ETABLE;
+    if (n > 0 && !seqs) return LORA_EINVAL;
+    int64_t q_end = 0, k_end = 0;
+    c.n = c.nq_gaps = c.nk_gaps = 0;
+    const auto gap = [](AttnGaps& g, int& count, int64_t from, int64_t to) {
+        if (to > from) {
+            g.from[count] = static_cast<int32_t>(from);
+            g.to[count++] = static_cast<int32_t>(to);
+        }
+    };
+    for (int32_t i = 0; i < n; ++i) {
+        const lora_attn_seq& s = seqs[i];
+        if (s.q_rows < 0 || s.k_rows < 0 || s.q_start < q_end || s.k_start < k_end) return LORA_ETABLE;
+        // starts first: the sums below then stay inside 64 bits
+        if (s.q_start > q_rows || s.k_start > k_rows || s.q_rows > q_rows - s.q_start || s.k_rows > k_rows - s.k_start)
+            return LORA_ETABLE;
+        gap(c.q_gaps, c.nq_gaps, q_end, s.q_start);
+        gap(c.k_gaps, c.nk_gaps, k_end, s.k_start);
+        q_end = s.q_start + s.q_rows;
+        k_end = s.k_start + s.k_rows;
+        if (s.q_rows > 0 || s.k_rows > 0)
+            c.order.s[c.n++] = AttnSeq{static_cast<int32_t>(s.q_start), static_cast<int32_t>(s.k_start),
+                                       static_cast<int32_t>(s.q_rows), static_cast<int32_t>(s.k_rows), 0};
+    }
+    gap(c.q_gaps, c.nq_gaps, q_end, q_rows);
+    gap(c.k_gaps, c.nk_gaps, k_end, k_rows);
+    return LORA_OK;
+}
+
+lora_status check_shape(const lora_attn_shape& a, Prepared& c) {
+    if (a.q_rows < 0 || a.k_rows < 0 || a.q_rows > LORA_MAX_ROWS || a.k_rows > LORA_MAX_ROWS) return LORA_ESHAPE;
+    if (a.q_heads < 1 || a.kv_heads < 1 || a.q_heads > LORA_ATTN_MAX_HEADS || a.q_heads % a.kv_heads) return LORA_ESHAPE;
+    if (a.head_dim < 8 || a.head_dim > LORA_ATTN_MAX_HEAD_DIM || a.head_dim % 8) return LORA_ESHAPE;
+    if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return LORA_EINVAL;
+    AttnShape& s = c.sh;
+    std::memset(&s, 0, sizeof(s));
+    s.hq = a.q_heads;
+    s.hkv = a.kv_heads;
+    s.group = a.q_heads / a.kv_heads;
+    s.hp = 1;
+    while (s.hp < kAttnTile && s.group % (2 * s.hp) == 0) {
+        s.hp *= 2;
+        ++s.hp_log2;
+    }
+    s.packs = s.hq / s.hp;
+    s.d = a.head_dim;
+    s.d16 = (a.head_dim + 15) / 16 * 16;
+    s.scale = a.scale;
+    s.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    return LORA_OK;
+}
+
+lora_status check_workspace(void* ws, size_t have, size_t need) {
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || have < need) return LORA_EWORKSPACE;
+    return LORA_OK;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int64_t tiles_of(int64_t rows, int per) { return (rows + per - 1) / per; }
+
+// Numbers the items (tiles of `per` rows, times `wide`) of every sequence, in the table's order.
+template <class Tiles>
+lora_status number_items(Prepared& c, Tiles tiles, int64_t wide) {
+    int64_t items = 0;
+    for (int i = 0; i < c.n; ++i) {
+        c.order.s[i].item0 = static_cast<int32_t>(items);
+        items += tiles(c.order.s[i]) * wide;
+        if (items > 0x7FFFFFFF) return LORA_ESHAPE;
+    }
+    c.sh.n_seqs = c.n;
+    c.sh.items = static_cast<int32_t>(items);
+    return LORA_OK;
+}
+
+void order_by_keys(Prepared& c) {
+    std::stable_sort(c.order.s, c.order.s + c.n, [](const AttnSeq& a, const AttnSeq& b) { return a.kl > b.kl; });
+}
+
+AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
+
+lora_status fill(const AttnGaps& gaps, int n, AttnMat a, AttnMat b, int heads, int d, float* lse, cudaStream_t s) {
+    if (n == 0) return LORA_OK;
+    AttnFillParams f{a, b, heads, d, lse, n};
+    LORA_CUDA(timed(kAttnFill, s, [&] { return launch_attn_fill(f, gaps, s); }));
+    return LORA_OK;
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t attn_workspace_size(int64_t q_rows, int32_t q_heads) {
+    if (q_rows < 0 || q_heads < 0) return 0;
+    return kStatusBytes + up256(static_cast<size_t>(q_rows) * static_cast<size_t>(q_heads) * 4);
+}
+
+lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const lora_attn_shape* shape,
+                     const lora_attn_seq* seqs, int32_t n_seqs, lora_bf16* O, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (!shape) return LORA_EINVAL;
+    const lora_attn_shape& a = *shape;
+    thread_local Prepared c;   // large: off the stack, one per calling thread
+    lora_status st = check_shape(a, c);
+    if (st) return st;
+    if (a.q_rows > 0 && !lse) return LORA_EINVAL;
+    if (!aligned16(lse)) return LORA_EALIGN;
+    if ((st = check_mat(Q, a.q, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_mat(K, a.k, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_mat(V, a.v, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_mat(O, a.o, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_seqs(seqs, n_seqs, a.q_rows, a.k_rows, c))) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes))) return st;
+    int sms = 0;
+    if ((st = device_setup(&sms))) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
+    order_by_keys(c);
+    const int tokens = kAttnTile / c.sh.hp;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, 2 * tokens); }, c.sh.packs))) return st;
+    if (c.sh.items == 0) return LORA_OK;
+    thread_local AttnFwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.sh = c.sh;
+    // no keys at all: the maps describe one row that is never read
+    const lora_bf16* k = a.k_rows > 0 ? K : Q;
+    const lora_bf16* v = a.k_rows > 0 ? V : Q;
+    const int64_t kr = std::max<int64_t>(a.k_rows, 1);
+    if (!make_map_heads(&p.mapQ, Q, a.head_dim, a.q_heads, a.q_rows, a.q.head, a.q.row, c.sh.hp, tokens) ||
+        !make_map_heads(&p.mapK, k, a.head_dim, a.kv_heads, kr, a.k.head, a.k.row, 1, kAttnTile) ||
+        !make_map_heads(&p.mapV, v, a.head_dim, a.kv_heads, kr, a.v.head, a.v.row, 1, kAttnTile))
+        return LORA_ECUDA;
+    p.O = mat(O, a.o);
+    p.lse = lse;
+    p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
+    LORA_CUDA(timed(kAttnFwd, s, [&] { return launch_attn_fwd(p, c.order, s); }));
+    return LORA_OK;
+}
+
+lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
+                     const lora_bf16* O, const float* lse, const lora_attn_shape* shape, const lora_attn_seq* seqs,
+                     int32_t n_seqs, lora_bf16* dQ, lora_bf16* dK, lora_bf16* dV, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (!shape) return LORA_EINVAL;
+    const lora_attn_shape& a = *shape;
+    thread_local Prepared c;
+    lora_status st = check_shape(a, c);
+    if (st) return st;
+    if (a.q_rows > 0 && !lse) return LORA_EINVAL;
+    if (!aligned16(lse)) return LORA_EALIGN;
+    if ((st = check_mat(dO, a.d_o, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_mat(Q, a.q, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_mat(K, a.k, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_mat(V, a.v, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_mat(O, a.o, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_mat(dQ, a.d_q, a.q_rows, a.q_heads, a.head_dim))) return st;
+    if ((st = check_mat(dK, a.d_k, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_mat(dV, a.d_v, a.k_rows, a.kv_heads, a.head_dim))) return st;
+    if ((st = check_seqs(seqs, n_seqs, a.q_rows, a.k_rows, c))) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, attn_workspace_size(a.q_rows, a.q_heads)))) return st;
+    int sms = 0;
+    if ((st = device_setup(&sms))) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = fill(c.q_gaps, c.nq_gaps, mat(dQ, a.d_q), AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
+    AttnMat mk = mat(dK, a.d_k), mv = mat(dV, a.d_v);
+    if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
+    if (c.n == 0) return LORA_OK;
+    order_by_keys(c);
+    thread_local AttnBwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    const int tokens = kAttnTile / c.sh.hp;
+    const bool no_q = a.q_rows == 0, no_k = a.k_rows == 0;
+    const int64_t qr = std::max<int64_t>(a.q_rows, 1), kr = std::max<int64_t>(a.k_rows, 1);
+    const lora_bf16* any = no_q ? K : Q;
+    if (!make_map_heads(&p.mapQ, no_q ? any : Q, a.head_dim, a.q_heads, qr, a.q.head, a.q.row, c.sh.hp, tokens) ||
+        !make_map_heads(&p.mapDO, no_q ? any : dO, a.head_dim, a.q_heads, qr, a.d_o.head, a.d_o.row, c.sh.hp, tokens) ||
+        !make_map_heads(&p.mapK, no_k ? any : K, a.head_dim, a.kv_heads, kr, a.k.head, a.k.row, 1, kAttnTile) ||
+        !make_map_heads(&p.mapV, no_k ? any : V, a.head_dim, a.kv_heads, kr, a.v.head, a.v.row, 1, kAttnTile))
+        return LORA_ECUDA;
+    p.lse = lse;
+    p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+    p.dQ = mat(dQ, a.d_q);
+    p.dK = mk;
+    p.dV = mv;
+    p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
+    if (!no_q) {
+        AttnDeltaParams d{O, dO, a.o.row, a.o.head, a.d_o.row, a.d_o.head, a.q_rows, a.q_heads, a.head_dim, p.delta};
+        LORA_CUDA(timed(kAttnDelta, s, [&] { return launch_attn_delta(d, s); }));
+    }
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }, c.sh.packs))) return st;
+    p.sh = c.sh;
+    if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, s); }));
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }, c.sh.hkv))) return st;
+    p.sh = c.sh;
+    if (c.sh.items > 0) LORA_CUDA(timed(kAttnDkDv, s, [&] { return launch_attn_dkdv(p, c.order, s); }));
+    return LORA_OK;
+}
+
+}  // extern "C"

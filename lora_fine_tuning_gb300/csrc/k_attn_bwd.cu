@@ -1,0 +1,714 @@
+// Backward of causal softmax attention over packed sequences with grouped heads.
+//
+//   P = exp(scale Q K^T - lse),  delta_i = sum_d dO_id O_id,  dP = dO V^T,  dS = P (dP - delta)
+//   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,   dK and dV summed over the query heads of a group
+//
+// Three passes: delta; dQ, a CTA a 128-row query tile over its keys; dK and dV, a CTA a 128-key tile over the query
+// tiles of all heads of its group.  Each gradient element is summed by one CTA in a fixed order, in TMEM in fp32:
+// the results are the same from call to call, and no partial sum goes through memory.  The price is that S and dP are
+// formed twice (seven products instead of five).
+#include "attn.cuh"
+#include "kernels.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 320;   // warps 0-7: scores and gradients of scores; warp 8: TMA; warp 9: MMAs
+
+// The two groups of four warps share every 128 x 128 tile: group g takes columns [64 g, 64 g + 64).  A group packs
+// its bf16 results into the first 32 of the TMEM columns that it read itself, so neither group waits for the other:
+// K step ks (16 values, 8 columns) of the tile as an A operand starts at column (ks / 4) * 64 + (ks % 4) * 8.
+__device__ __forceinline__ uint32_t a_col(int ks) { return (ks >> 2) * 64 + (ks & 3) * 8; }
+
+// 64 columns of this thread's row.
+__device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
+    tmem_ld32(taddr, v[0]);
+    tmem_ld32(taddr + 32, v[1]);
+    tmem_ld_wait(v);
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// delta
+// ---------------------------------------------------------------------------------------------------------------
+
+// One (row, head) per group of 16 lanes, 8 features a lane.
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnDeltaParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t n = p.rows * p.hq;
+    const int sub = threadIdx.x & 15;
+    for (int64_t i = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 4; i < (n + 1) / 2 * 2;
+         i += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 4) {
+        float sum = 0.f;
+        const int64_t row = i / p.hq;
+        const int h = static_cast<int>(i - row * p.hq);
+        if (i < n && sub * 8 < p.d) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p.O + row * p.o_row + h * p.o_head + sub * 8);
+            const uint4 b = *reinterpret_cast<const uint4*>(p.dO + row * p.do_row + h * p.do_head + sub * 8);
+            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+            }
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (i < n && sub == 0) p.delta[i] = sum;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------------------------------------------
+
+template <int DP>
+struct CfgQ {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr uint32_t kTileBytes = kBoxes * 16384u;
+    static constexpr int kStages = 2;    // of K, and of V
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * static_cast<size_t>(kTileBytes) + 256;
+};
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    using C = CfgQ<DP>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    uint8_t* sQ = smem;
+    uint8_t* sDO = sQ + C::kTileBytes;
+    uint8_t* sK = sDO + C::kTileBytes;
+    uint8_t* sV = sK + S * C::kTileBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + S * C::kTileBytes);
+    uint64_t* q_full = bars;               // Q and dO
+    uint64_t* k_full = q_full + 1;         // S each
+    uint64_t* k_empty = k_full + S;
+    uint64_t* v_full = k_empty + S;
+    uint64_t* v_empty = v_full + S;
+    uint64_t* s_full = v_empty + S;        // 2 score buffers
+    uint64_t* dp_full = s_full + 2;
+    uint64_t* ds_full = dp_full + 1;
+    uint64_t* dq_full = ds_full + 1;
+    uint64_t* k_fixed = dq_full + 1;
+    uint64_t* drain = k_fixed + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    __shared__ int abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 256);
+        mbar_init(dq_full, 1);
+        mbar_init(k_fixed, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDq << 8};
+
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const int tpt = kAttnTile >> sh.hp_log2;
+    const int tiles = (sq.ql + tpt - 1) / tpt;
+    const int local = blockIdx.x - sq.item0;
+    const int tok0 = (tiles - 1 - local / sh.packs) * tpt;
+    const int head0 = (local % sh.packs) << sh.hp_log2;
+    const int kvh = head0 / sh.group;
+    const int off = sq.kl - sq.ql;
+    const int last = min(tok0 + tpt, sq.ql) - 1 + off;            // last key the tile sees
+    const int n = last >= 0 ? last / kAttnTile + 1 : 0;
+    const bool tail = n * kAttnTile > sq.kl;
+
+    if (warp == 8) {
+        bool ok = true;
+        int issued = 0;
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b) {
+                tma_load_3d(sQ + b * 16384, &p.mapQ, q_full, b * 64, head0, sq.q0 + tok0);
+                tma_load_3d(sDO + b * 16384, &p.mapDO, q_full, b * 64, head0, sq.q0 + tok0);
+            }
+        }
+        for (int j = 0; j < n; ++j) {
+            const int s = j % S;
+            const uint32_t ph = (j / S) & 1;
+            if (lane == 0) {
+                ok = mbar_wait(&k_empty[s], ph ^ 1u, w, 1);
+                if (ok) {
+                    mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(sK + s * C::kTileBytes + b * 16384, &p.mapK, &k_full[s], b * 64, kvh,
+                                    sq.k0 + j * kAttnTile);
+                    ok = mbar_wait(&v_empty[s], ph ^ 1u, w, 2);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
+                        for (int b = 0; b < C::kBoxes; ++b)
+                            tma_load_3d(sV + s * C::kTileBytes + b * 16384, &p.mapV, &v_full[s], b * 64, kvh,
+                                        sq.k0 + j * kAttnTile);
+                    } else {
+                        mbar_wait_drain(&k_full[s], ph, p.ctl.wait_ns);
+                    }
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            ++issued;
+        }
+        if (ok && tail && n > 0) {
+            const int s = (n - 1) % S;
+            ok = mbar_wait(&k_full[s], ((n - 1) / S) & 1, w, 3);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                zero_tile_rows(sK + s * C::kTileBytes, C::kBoxes, sq.kl - (n - 1) * kAttnTile);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k_fixed);
+            }
+        }
+        if (!ok && lane == 0) {
+            if (n > 0) mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
+            for (int j = max(0, issued - S); j < issued; ++j) {
+                mbar_wait_drain(&k_full[j % S], (j / S) & 1, p.ctl.wait_ns);
+                mbar_wait_drain(&v_full[j % S], (j / S) & 1, p.ctl.wait_ns);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
+            const uint32_t idesc_q = make_idesc_bf16(128, sh.d16, false, true);
+            const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
+            const uint64_t dod = make_smem_desc(smem_u32(sDO), 16, 1024, kSw128);
+            const uint64_t kd = make_smem_desc(smem_u32(sK), 16, 1024, kSw128);
+            const uint64_t kmn = make_smem_desc(smem_u32(sK), 16384, 1024, kSw128);
+            const uint64_t vd = make_smem_desc(smem_u32(sV), 16, 1024, kSw128);
+            bool ok = true;
+            if (n > 0) ok = mbar_wait(q_full, 0, w, 4);
+            // turn j: S(j) (its own buffer), dQ += dS(j - 1) K(j - 1), dP(j)
+            for (int j = 0; j <= n && n > 0 && ok; ++j) {
+                const uint64_t cur = static_cast<uint64_t>(j % S) * (C::kTileBytes >> 4);
+                const uint64_t prev = static_cast<uint64_t>((j + S - 1) % S) * (C::kTileBytes >> 4);
+                if (j < n) {
+                    if (!mbar_wait(&k_full[j % S], (j / S) & 1, w, 5)) { ok = false; break; }
+                    if (tail && j == n - 1 && !mbar_wait(k_fixed, 0, w, 6)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP>(t_s + (j & 1) * 128, qd, kd + cur, idesc_s);
+                    umma_commit(&s_full[j & 1]);
+                }
+                if (j > 0) {
+                    if (!mbar_wait(ds_full, (j - 1) & 1, w, 8)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_ta(t_dq, t_s + ((j - 1) & 1) * 128 + a_col(ks), kmn + prev + ks * 128u, idesc_q,
+                                     (j != 1 || ks != 0) ? 1u : 0u);
+                    umma_commit(&k_empty[(j - 1) % S]);
+                }
+                if (j < n) {
+                    if (!mbar_wait(&v_full[j % S], (j / S) & 1, w, 7)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP>(t_dp, dod, vd + cur, idesc_s);
+                    umma_commit(dp_full);
+                    umma_commit(&v_empty[j % S]);
+                }
+            }
+            if (ok) umma_commit(dq_full);
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+        }
+    } else {
+        const int g = warp >> 2;                     // columns [64 g, 64 g + 64) of every tile
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;
+        const int tok = tok0 + (r >> sh.hp_log2);
+        const int head = head0 + (r & (sh.hp - 1));
+        const bool row_ok = tok < sq.ql;
+        const int limit = tok + off;
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const float sl = sh.scale_log2;
+        float lse2 = 0.f, delta = 0.f;
+        if (row_ok) {
+            const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
+            lse2 = p.lse[at] * kLog2e;
+            delta = p.delta[at];
+            if (limit < 0) lse2 = 0.f;               // no visible key: every score is masked below
+        }
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const uint32_t ts = t_s + (j & 1) * 128 + lanes + g * 64;
+            ok = mbar_wait(&s_full[j & 1], (j >> 1) & 1, w, 9);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t v[2][32], x[2][32];
+            ld64(ts, v);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e]), sl, -lse2)));
+            ok = mbar_wait(dp_full, j & 1, w, 10);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            ld64(t_dp + lanes + g * 64, x);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * (__uint_as_float(x[c][e]) - delta));
+            if ((j + 1) * kAttnTile - 1 > tok0 + off) {
+                const int lim = limit - j * kAttnTile - g * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e > lim) x[c][e] = 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[e] = pack_bf16x2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
+                tmem_st16(ts + c * 16, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(ds_full);
+        }
+        if (ok && n > 0) {
+            ok = mbar_wait(dq_full, 0, w, 11);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+        }
+        if (ok) {
+            uint16_t* out = p.dQ.p + (static_cast<int64_t>(sq.q0) + tok) * p.dQ.row + static_cast<int64_t>(head) * p.dQ.head;
+            // group g writes every second 16 features
+#pragma unroll 1
+            for (int c = g * 16; c < sh.d16; c += 32) {
+                uint32_t o[16];
+                if (n > 0) {
+                    tmem_ld16(t_dq + lanes + c, o);
+                    tmem_ld_wait(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                }
+                if (row_ok) store_out16(out, o, sh.scale, c, sh.d);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// dK, dV
+// ---------------------------------------------------------------------------------------------------------------
+
+template <int DP>
+struct CfgKV {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr uint32_t kTileBytes = kBoxes * 16384u;
+    static constexpr int kStages = 2;    // of Q, and of dO
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * static_cast<size_t>(kTileBytes) + 2 * 2 * 512 + 256;
+};
+
+// Barrier among the 256 threads of the score warps.
+__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    using C = CfgKV<DP>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    uint8_t* sK = smem;
+    uint8_t* sV = sK + C::kTileBytes;
+    uint8_t* sQ = sV + C::kTileBytes;
+    uint8_t* sDO = sQ + S * C::kTileBytes;
+    float* sStat = reinterpret_cast<float*>(sDO + S * C::kTileBytes);   // [2][lse2 128, delta 128]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sStat + 2 * 256);
+    uint64_t* k_full = bars;               // K
+    uint64_t* v_full = k_full + 1;         // V
+    uint64_t* q_full = v_full + 1;         // S each
+    uint64_t* q_empty = q_full + S;
+    uint64_t* do_full = q_empty + S;
+    uint64_t* do_empty = do_full + S;
+    uint64_t* s_full = do_empty + S;
+    uint64_t* dp_full = s_full + 1;
+    uint64_t* p_full = dp_full + 1;
+    uint64_t* ds_full = p_full + 1;
+    uint64_t* out_full = ds_full + 1;
+    uint64_t* fixed = out_full + 1;        // S: Q and dO rows past the sequence are zero
+    uint64_t* drain = fixed + S;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    __shared__ int abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(k_full, 1);
+        mbar_init(v_full, 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+            mbar_init(&do_full[s], 1);
+            mbar_init(&do_empty[s], 1);
+            mbar_init(&fixed[s], 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_full, 256);
+        mbar_init(ds_full, 256);
+        mbar_init(out_full, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDkDv << 8};
+
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const int tpt = kAttnTile >> sh.hp_log2;
+    const int local = blockIdx.x - sq.item0;
+    const int kt = local / sh.hkv;                       // the first key tiles have the most queries
+    const int kvh = local - kt * sh.hkv;
+    const int off = sq.kl - sq.ql;
+    const int key0 = kt * kAttnTile;
+    // the first query tile with a row that sees the first key, and the tiles after it, for each pack of the group
+    const int i0 = max(0, key0 - off) / tpt;
+    const int qt = (sq.ql + tpt - 1) / tpt;
+    const int per = max(0, qt - i0);
+    const int packs = sh.group >> sh.hp_log2;
+    const int n = per * packs;
+    const int ragged = sq.ql - (qt - 1) * tpt;           // tokens of the last query tile
+    const bool tail = ragged < tpt;
+
+    if (warp == 8) {
+        bool ok = true;
+        int issued = 0;
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(k_full, C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(sK + b * 16384, &p.mapK, k_full, b * 64, kvh, sq.k0 + key0);
+            mbar_arrive_expect_tx(v_full, C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(sV + b * 16384, &p.mapV, v_full, b * 64, kvh, sq.k0 + key0);
+        }
+        for (int t = 0; t < n; ++t) {
+            const int s = t % S;
+            const uint32_t ph = (t / S) & 1;
+            const int pack = t / per, i = i0 + (t - pack * per);
+            const int head0 = kvh * sh.group + (pack << sh.hp_log2);
+            if (lane == 0) {
+                ok = mbar_wait(&q_empty[s], ph ^ 1u, w, 1) && mbar_wait(&do_empty[s], ph ^ 1u, w, 2);
+                if (ok) {
+                    mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(sQ + s * C::kTileBytes + b * 16384, &p.mapQ, &q_full[s], b * 64, head0,
+                                    sq.q0 + i * tpt);
+                    mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(sDO + s * C::kTileBytes + b * 16384, &p.mapDO, &do_full[s], b * 64, head0,
+                                    sq.q0 + i * tpt);
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            ++issued;
+            if (tail && i == qt - 1) {
+                ok = mbar_wait(&q_full[s], ph, w, 3) && mbar_wait(&do_full[s], ph, w, 4);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                zero_tile_rows(sQ + s * C::kTileBytes, C::kBoxes, ragged << sh.hp_log2);
+                zero_tile_rows(sDO + s * C::kTileBytes, C::kBoxes, ragged << sh.hp_log2);
+                __syncwarp();
+            }
+            // the MMAs of every tile wait here: the rows of this stage are the sequence's own
+            if (lane == 0) mbar_arrive(&fixed[s]);
+        }
+        if (!ok && lane == 0) {
+            if (n > 0) {
+                mbar_wait_drain(k_full, 0, p.ctl.wait_ns);
+                mbar_wait_drain(v_full, 0, p.ctl.wait_ns);
+            }
+            for (int t = max(0, issued - S); t < issued; ++t) {
+                mbar_wait_drain(&q_full[t % S], (t / S) & 1, p.ctl.wait_ns);
+                mbar_wait_drain(&do_full[t % S], (t / S) & 1, p.ctl.wait_ns);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
+            const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
+            const uint64_t kd = make_smem_desc(smem_u32(sK), 16, 1024, kSw128);
+            const uint64_t vd = make_smem_desc(smem_u32(sV), 16, 1024, kSw128);
+            const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
+            const uint64_t dod = make_smem_desc(smem_u32(sDO), 16, 1024, kSw128);
+            const uint64_t qmn = make_smem_desc(smem_u32(sQ), 16384, 1024, kSw128);
+            const uint64_t domn = make_smem_desc(smem_u32(sDO), 16384, 1024, kSw128);
+            bool ok = true;
+            if (n > 0) ok = mbar_wait(k_full, 0, w, 5) && mbar_wait(v_full, 0, w, 8);
+            // turn t: dV += P(t - 1)^T dO(t - 1), S^T(t), dK += dS(t - 1)^T Q(t - 1), dP^T(t)
+            for (int t = 0; t <= n && n > 0 && ok; ++t) {
+                const uint64_t cur = static_cast<uint64_t>(t % S) * (C::kTileBytes >> 4);
+                const uint64_t prev = static_cast<uint64_t>((t + S - 1) % S) * (C::kTileBytes >> 4);
+                if (t > 0) {
+                    if (!mbar_wait(p_full, (t - 1) & 1, w, 10)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_ta(t_dv, t_s + a_col(ks), domn + prev + ks * 128u, idesc_o,
+                                     (t != 1 || ks != 0) ? 1u : 0u);
+                    umma_commit(&do_empty[(t - 1) % S]);
+                }
+                if (t < n) {
+                    if (!mbar_wait(&q_full[t % S], (t / S) & 1, w, 6)) { ok = false; break; }
+                    if (!mbar_wait(&fixed[t % S], (t / S) & 1, w, 7)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP>(t_s, kd, qd + cur, idesc_s);
+                    umma_commit(s_full);
+                }
+                if (t > 0) {
+                    if (!mbar_wait(ds_full, (t - 1) & 1, w, 11)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_ta(t_dk, t_dp + a_col(ks), qmn + prev + ks * 128u, idesc_o,
+                                     (t != 1 || ks != 0) ? 1u : 0u);
+                    umma_commit(&q_empty[(t - 1) % S]);
+                }
+                if (t < n) {
+                    if (!mbar_wait(&do_full[t % S], (t / S) & 1, w, 9)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP>(t_dp, vd, dod + cur, idesc_s);
+                    umma_commit(dp_full);
+                }
+            }
+            if (ok) umma_commit(out_full);
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+        }
+    } else {
+        const int g = warp >> 2;
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;              // key of the tile
+        const int ct = threadIdx.x & 127;            // the query row whose statistics this thread fetches
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t ts = t_s + lanes + g * 64;
+        const uint32_t tdp = t_dp + lanes + g * 64;
+        const float sl = sh.scale_log2;
+        const float* src = g == 0 ? p.lse : p.delta; // group 0 fetches lse, group 1 delta
+        // one tile ahead: lse in the exponent's units (a row that is not there, or sees no key: +inf, P = 0), delta
+        const auto fetch = [&](int t) -> float {
+            const int pack = t / per, i = i0 + (t - pack * per);
+            const int tok = i * tpt + (ct >> sh.hp_log2);
+            const int head = kvh * sh.group + (pack << sh.hp_log2) + (ct & (sh.hp - 1));
+            const bool there = t < n && tok < sq.ql && tok + off >= 0;
+            if (!there) return g == 0 ? -neg_inf() : 0.f;
+            const float x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
+            return g == 0 ? x * kLog2e : x;
+        };
+        bool ok = true;
+        float next = n > 0 ? fetch(0) : 0.f;
+        for (int t = 0; t < n; ++t) {
+            float* stat = sStat + (t & 1) * 256;
+            stat[g * 128 + ct] = next;
+            score_sync();
+            next = fetch(t + 1);
+            const int pack = t / per, i = i0 + (t - pack * per);
+            const uint32_t st = smem_u32(stat) + g * 256;    // this group's 64 columns
+            ok = mbar_wait(s_full, t & 1, w, 12);
+            // after a wait that gave up the loop runs on (each later wait returns at once): the barrier above counts
+            // all 256 threads
+            if (!ok) abort_flag = 1;
+            __syncwarp();
+            tc_fence_after();
+            uint32_t v[2][32], x[2][32];
+            ld64(ts, v);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const uint4 q = lds128(st + (c * 32 + e) * 4);
+                    v[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e]), sl, -__uint_as_float(q.x))));
+                    v[c][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 1]), sl, -__uint_as_float(q.y))));
+                    v[c][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 2]), sl, -__uint_as_float(q.z))));
+                    v[c][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 3]), sl, -__uint_as_float(q.w))));
+                }
+            // keys after a query's limit: key0 + r > tok + off
+            int cmin = 0;
+            if (key0 + kAttnTile - 1 > i * tpt + off) {
+                const int lo = key0 + r - off - i * tpt;     // first token of the tile that sees this key
+                cmin = (max(lo, 0) << sh.hp_log2) - g * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e < cmin) v[c][e] = 0u;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[e] = pack_bf16x2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+                tmem_st16(ts + c * 16, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(p_full);
+            ok = mbar_wait(dp_full, t & 1, w, 13);
+            if (!ok) abort_flag = 1;
+            __syncwarp();
+            tc_fence_after();
+            ld64(tdp, x);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const uint4 q = lds128(st + 512 + (c * 32 + e) * 4);
+                    const float d0 = __uint_as_float(v[c][e]) * (__uint_as_float(x[c][e]) - __uint_as_float(q.x));
+                    const float d1 = __uint_as_float(v[c][e + 1]) * (__uint_as_float(x[c][e + 1]) - __uint_as_float(q.y));
+                    const float d2 = __uint_as_float(v[c][e + 2]) * (__uint_as_float(x[c][e + 2]) - __uint_as_float(q.z));
+                    const float d3 = __uint_as_float(v[c][e + 3]) * (__uint_as_float(x[c][e + 3]) - __uint_as_float(q.w));
+                    o[e / 2] = pack_bf16x2(d0, d1);
+                    o[e / 2 + 1] = pack_bf16x2(d2, d3);
+                }
+                tmem_st16(tdp + c * 16, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(ds_full);
+        }
+        ok = *static_cast<volatile int*>(&abort_flag) == 0;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok && n > 0) {
+            ok = mbar_wait(out_full, 0, w, 14);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+        }
+        if (ok) {
+            const int key = key0 + r;
+            const bool row_ok = key < sq.kl;
+            uint16_t* dk = p.dK.p + (static_cast<int64_t>(sq.k0) + key) * p.dK.row + static_cast<int64_t>(kvh) * p.dK.head;
+            uint16_t* dv = p.dV.p + (static_cast<int64_t>(sq.k0) + key) * p.dV.row + static_cast<int64_t>(kvh) * p.dV.head;
+            // group 0 writes dV, group 1 dK
+            const uint32_t from = (g == 0 ? t_dv : t_dk) + lanes;
+            uint16_t* out = g == 0 ? dv : dk;
+            const float f = g == 0 ? 1.f : sh.scale;
+#pragma unroll 1
+            for (int c = 0; c < sh.d16; c += 16) {
+                uint32_t o[16];
+                if (n > 0) {
+                    tmem_ld16(from + c, o);
+                    tmem_ld_wait(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                }
+                if (row_ok) store_out16(out, o, f, c, sh.d);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DP, int N>
+cudaError_t run_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    return launch_pdl(attn_dq_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), CfgQ<DP>::kSmem, stream, p,
+                      reinterpret_cast<const AttnSeqs<N>&>(seqs));
+}
+
+template <int DP, int N>
+cudaError_t run_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    return launch_pdl(attn_dkdv_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), CfgKV<DP>::kSmem, stream, p,
+                      reinterpret_cast<const AttnSeqs<N>&>(seqs));
+}
+
+template <int DP, int N>
+cudaError_t configure() {
+    const cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(CfgQ<DP>::kSmem));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attn_dkdv_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(CfgKV<DP>::kSmem));
+}
+
+}  // namespace
+
+cudaError_t attn_bwd_configure() {
+    cudaError_t e = configure<64, kAttnFewSeqs>();
+    if (e == cudaSuccess) e = configure<64, kAttnMaxSeqs>();
+    if (e == cudaSuccess) e = configure<128, kAttnFewSeqs>();
+    if (e == cudaSuccess) e = configure<128, kAttnMaxSeqs>();
+    return e;
+}
+
+cudaError_t launch_attn_delta(const AttnDeltaParams& p, cudaStream_t stream) {
+    const int64_t blocks = std::min<int64_t>((p.rows * p.hq + 15) / 16, 152 * 16);
+    return launch_pdl(attn_delta_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
+}
+
+cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    const bool few = p.sh.n_seqs <= kAttnFewSeqs;
+    if (p.sh.d <= 64) return few ? run_dq<64, kAttnFewSeqs>(p, seqs, stream) : run_dq<64, kAttnMaxSeqs>(p, seqs, stream);
+    return few ? run_dq<128, kAttnFewSeqs>(p, seqs, stream) : run_dq<128, kAttnMaxSeqs>(p, seqs, stream);
+}
+
+cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    const bool few = p.sh.n_seqs <= kAttnFewSeqs;
+    if (p.sh.d <= 64)
+        return few ? run_dkdv<64, kAttnFewSeqs>(p, seqs, stream) : run_dkdv<64, kAttnMaxSeqs>(p, seqs, stream);
+    return few ? run_dkdv<128, kAttnFewSeqs>(p, seqs, stream) : run_dkdv<128, kAttnMaxSeqs>(p, seqs, stream);
+}
+
+}  // namespace lora

@@ -1,0 +1,372 @@
+// Forward of causal softmax attention over packed sequences with grouped heads.
+//
+//   S = scale Q K^T,  visible keys j <= i + (k_len - q_len),  lse_i = log sum_j exp S_ij,  O = exp(S - lse) V
+//
+// in one pass over the keys with the running maximum and sum of each row.  A CTA works on two 128-row query tiles
+// (tokens x heads of one group, attn.h) that share every K and V tile: while the softmax of one tile runs, the tensor
+// cores work on the other's products.  Warps 0-3 and 4-7: the softmax of tile 0 and 1, a thread one row; warp 8: TMA
+// (K and V tiles of 128 keys through a ring of stages); warp 9: the MMAs.  S (fp32) lives in TMEM, is read by its
+// row's thread, and P goes back in bf16 over S's columns, from where the second product reads it as its A operand.
+// The rows of O are rescaled in TMEM only when a row's maximum grew by more than 2^8 since the last rescaling (the
+// statistics keep the older maximum until then: P stays below 2^8, far inside bf16's and fp32's ranges).
+#include "attn.cuh"
+#include "kernels.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kStages = 4;
+constexpr float kRescale = 8.f;   // log2 of the growth of a row's maximum that rescales O
+
+template <int DP>
+struct Cfg {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr uint32_t kTileBytes = kBoxes * 16384u;   // 128 rows x DP bf16
+    static constexpr size_t kSmem = 1024 + (2 + kStages) * static_cast<size_t>(kTileBytes) + 256;
+};
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    using C = Cfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_1024(smem_raw);
+    uint8_t* sQ = smem;
+    uint8_t* sKV = smem + 2 * C::kTileBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kStages * C::kTileBytes);
+    uint64_t* q_full = bars;              // 2
+    uint64_t* kv_full = q_full + 2;       // kStages
+    uint64_t* kv_empty = kv_full + kStages;
+    uint64_t* s_full = kv_empty + kStages;   // 2
+    uint64_t* p_full = s_full + 2;           // 2
+    uint64_t* o_full = p_full + 2;           // 2
+    uint64_t* v_fixed = o_full + 2;          // 1: the last V tile's rows past the sequence are zero
+    uint64_t* drain = v_fixed + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    __shared__ int abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        mbar_init(v_fixed, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&p.mapQ);
+        tma_prefetch_desc(&p.mapK);
+        tma_prefetch_desc(&p.mapV);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnFwd << 8};
+
+    // the item: a pair of query tiles of one pack of heads, the pairs with the most keys first
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
+    const int pairs = (sq.ql + 2 * tpt - 1) / (2 * tpt);
+    const int local = blockIdx.x - sq.item0;
+    const int pack = local % sh.packs;
+    const int tok0 = (pairs - 1 - local / sh.packs) * 2 * tpt;      // first token of tile 0
+    const int head0 = pack << sh.hp_log2;
+    const int kvh = head0 / sh.group;
+    const int off = sq.kl - sq.ql;
+    int nk[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int first = tok0 + i * tpt;
+        const int last = min(first + tpt, sq.ql) - 1;               // last token of the tile
+        nk[i] = (first < sq.ql && last + off >= 0) ? (last + off) / kAttnTile + 1 : 0;
+    }
+    const int nkm = max(nk[0], nk[1]);
+    const bool tail = nkm * kAttnTile > sq.kl;                      // the last key tile ends past the sequence
+
+    if (warp == 8) {
+        bool ok = true;
+        int issued = 0;
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i) {
+                if (nk[i] == 0) continue;
+                mbar_arrive_expect_tx(&q_full[i], C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + i * C::kTileBytes + b * 16384, &p.mapQ, &q_full[i], b * 64, head0,
+                                sq.q0 + tok0 + i * tpt);
+            }
+        }
+        for (int t = 0; t < 2 * nkm; ++t) {
+            const int s = t % kStages;
+            const uint32_t ph = (t / kStages) & 1;
+            if (lane == 0) {
+                ok = mbar_wait(&kv_empty[s], ph ^ 1u, w, 1);
+                if (ok) {
+                    mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
+                    const CUtensorMap* map = (t & 1) ? &p.mapV : &p.mapK;
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        tma_load_3d(sKV + s * C::kTileBytes + b * 16384, map, &kv_full[s], b * 64, kvh,
+                                    sq.k0 + (t >> 1) * kAttnTile);
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+            ++issued;
+        }
+        if (ok && tail && nkm > 0) {
+            const int t = 2 * nkm - 1;
+            ok = mbar_wait(&kv_full[t % kStages], (t / kStages) & 1, w, 2);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                zero_tile_rows(sKV + (t % kStages) * C::kTileBytes, C::kBoxes, sq.kl - (nkm - 1) * kAttnTile);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_fixed);
+            }
+        }
+        if (!ok && lane == 0) {
+            // copies in flight land before the CTA exits
+            for (int i = 0; i < 2; ++i)
+                if (nk[i] > 0) mbar_wait_drain(&q_full[i], 0, p.ctl.wait_ns);
+            for (int t = max(0, issued - kStages); t < issued; ++t)
+                mbar_wait_drain(&kv_full[t % kStages], (t / kStages) & 1, p.ctl.wait_ns);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
+            const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
+            const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
+            const uint64_t kd = make_smem_desc(smem_u32(sKV), 16, 1024, kSw128);       // K: rows x features
+            const uint64_t vd = make_smem_desc(smem_u32(sKV), 16384, 1024, kSw128);    // V: features contiguous
+            bool ok = true;
+            // turn j: for each query tile the product of P(j - 1) with V(j - 1), then the scores with K(j).  S(j)
+            // overwrites P(j - 1) in TMEM: the MMAs execute in the order in which they are issued.
+            for (int j = 0; j <= nkm && nkm > 0; ++j) {
+                const int tk = 2 * j, tv = 2 * j - 1;
+                const uint64_t ks_ = kd + static_cast<uint64_t>(tk % kStages) * (C::kTileBytes >> 4);
+                const uint64_t vs_ = vd + static_cast<uint64_t>((tv + kStages) % kStages) * (C::kTileBytes >> 4);
+                if (j > 0) {
+                    if (!mbar_wait(&kv_full[tv % kStages], (tv / kStages) & 1, w, 3)) { ok = false; break; }
+                    if (tail && j == nkm && !mbar_wait(v_fixed, 0, w, 4)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                if (j < nkm) {
+                    if (!mbar_wait(&kv_full[tk % kStages], (tk / kStages) & 1, w, 5)) { ok = false; break; }
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (j > 0 && j <= nk[i]) {
+                        if (!mbar_wait(&p_full[i], (j - 1) & 1, w, 6)) { ok = false; break; }
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            umma_bf16_ta(tmem + 256 + i * DP, tmem + i * 128 + ks * 8, vs_ + ks * 128u, idesc_o,
+                                         (j != 1 || ks != 0) ? 1u : 0u);
+                        if (j == nk[i]) umma_commit(&o_full[i]);
+                    }
+                    if (j < nk[i]) {
+                        if (j == 0) {
+                            if (!mbar_wait(&q_full[i], 0, w, 7)) { ok = false; break; }
+                            tc_fence_after();
+                        }
+                        mma_rows<DP>(tmem + i * 128, qd + i * (C::kTileBytes >> 4), ks_, idesc_s);
+                        umma_commit(&s_full[i]);
+                    }
+                }
+                if (!ok) break;
+                if (j > 0) umma_commit(&kv_empty[tv % kStages]);
+                if (j < nkm) umma_commit(&kv_empty[tk % kStages]);
+            }
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+        }
+    } else {
+        const int i = warp >> 2;                     // query tile
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;              // row of the tile = TMEM lane
+        const int tok = tok0 + i * tpt + (r >> sh.hp_log2);
+        const int head = head0 + (r & (sh.hp - 1));
+        const int limit = tok + off;                 // last visible key (clamped below kl: tok < ql)
+        const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        const uint32_t ts = tmem + lanes + i * 128;
+        const uint32_t to = tmem + lanes + 256 + i * DP;
+        const float sl = sh.scale_log2;
+        const int n = i == 0 ? nk[0] : nk[1];
+        const int first_limit = tok0 + i * tpt + off;   // last key the tile's first row sees
+        float m = neg_inf(), l = 0.f;                // maximum (in the exponent's units) and sum
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            ok = mbar_wait(&s_full[i], j & 1, w, 9);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v[c]);
+            tmem_ld_wait(v);
+            if ((j + 1) * kAttnTile - 1 > first_limit) {
+                // keys past the row's limit (and past the sequence: limit < kl)
+                const int lim = limit - j * kAttnTile;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e > lim) v[c][e] = 0xff800000u;
+            }
+            float top = neg_inf();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[c][e]));
+            top *= sl;
+            if (j == 0) {
+                m = top;
+            } else {
+                const bool grow = top > m + kRescale;
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+                    // s_full of this tile came after the previous product into O
+                    const float mn = grow ? top : m;
+                    const float f = grow ? (m == neg_inf() ? 0.f : ex2(m - mn)) : 1.f;
+                    m = mn;
+                    l *= f;
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + c, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(to + c, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float ms = m == neg_inf() ? 0.f : m;   // a row without a visible key yet: exp2(-inf) = 0 throughout
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float a = ex2(fmaf(__uint_as_float(v[c][2 * e]), sl, -ms));
+                    const float b = ex2(fmaf(__uint_as_float(v[c][2 * e + 1]), sl, -ms));
+                    sum[e & 3] += a + b;
+                    o[e] = pack_bf16x2(a, b);
+                }
+                tmem_st16(ts + c * 16, o);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[i]);
+        }
+        if (ok && n > 0) {
+            ok = mbar_wait(&o_full[i], 0, w, 10);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+        }
+        if (ok) {
+            const bool row_ok = tok < sq.ql;
+            const float f = l == 0.f ? 0.f : 1.f / l;   // no visible key: zeros; a NaN stays one
+            uint16_t* out = p.O.p + (static_cast<int64_t>(sq.q0) + tok) * p.O.row + static_cast<int64_t>(head) * p.O.head;
+#pragma unroll 1
+            for (int c = 0; c < sh.d16; c += 16) {
+                uint32_t o[16];
+                if (n > 0) {
+                    tmem_ld16(to + c, o);
+                    tmem_ld_wait(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                }
+                if (l == 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                }
+                if (row_ok) store_out16(out, o, f, c, sh.d);
+            }
+            if (row_ok)
+                p.lse[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Rows of no sequence: zeros (and lse -inf), so that what reads the whole batch later finds no stale values.
+__global__ void __launch_bounds__(256) attn_fill_kernel(const __grid_constant__ AttnFillParams p,
+                                                        const __grid_constant__ AttnGaps gaps) {
+    pdl_wait();
+    pdl_trigger();
+    const int from = gaps.from[blockIdx.x], to = gaps.to[blockIdx.x];
+    const int chunks = p.heads * (p.d / 8);
+    for (int row = from + blockIdx.y; row < to; row += gridDim.y) {
+        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+            const int h = c / (p.d / 8), x = (c - h * (p.d / 8)) * 8;
+            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+            stg128(p.a.p + static_cast<int64_t>(row) * p.a.row + static_cast<int64_t>(h) * p.a.head + x, z);
+            if (p.b.p) stg128(p.b.p + static_cast<int64_t>(row) * p.b.row + static_cast<int64_t>(h) * p.b.head + x, z);
+        }
+        if (p.lse)
+            for (int h = threadIdx.x; h < p.heads; h += blockDim.x)
+                p.lse[static_cast<int64_t>(row) * p.heads + h] = neg_inf();
+    }
+}
+
+template <int DP, int N>
+cudaError_t run(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    return launch_pdl(attn_fwd_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), Cfg<DP>::kSmem, stream, p,
+                      reinterpret_cast<const AttnSeqs<N>&>(seqs));
+}
+
+template <int DP, int N>
+cudaError_t configure() {
+    return cudaFuncSetAttribute(attn_fwd_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Cfg<DP>::kSmem));
+}
+
+}  // namespace
+
+cudaError_t attn_fwd_configure() {
+    cudaError_t e = configure<64, kAttnFewSeqs>();
+    if (e == cudaSuccess) e = configure<64, kAttnMaxSeqs>();
+    if (e == cudaSuccess) e = configure<128, kAttnFewSeqs>();
+    if (e == cudaSuccess) e = configure<128, kAttnMaxSeqs>();
+    return e;
+}
+
+cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    const bool few = p.sh.n_seqs <= kAttnFewSeqs;
+    if (p.sh.d <= 64) return few ? run<64, kAttnFewSeqs>(p, seqs, stream) : run<64, kAttnMaxSeqs>(p, seqs, stream);
+    return few ? run<128, kAttnFewSeqs>(p, seqs, stream) : run<128, kAttnMaxSeqs>(p, seqs, stream);
+}
+
+cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream) {
+    return launch_pdl(attn_fill_kernel, dim3(p.n, 16), dim3(256), 0, stream, p, gaps);
+}
+
+}  // namespace lora

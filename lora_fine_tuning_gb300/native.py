@@ -19,7 +19,7 @@ STATUS_NAMES = {0: "LORA_OK", 1: "LORA_EINVAL", 2: "LORA_EALIGN", 3: "LORA_ESHAP
 # Symbols include/lora.h declares, in declaration order.
 EXPORTED = ["lora_workspace_size", "lora_set_deterministic", "lora_get_deterministic", "lora_fwd", "lora_bwd", "multi_lora_fwd", "multi_lora_bwd",
             "dora_workspace_size", "dora_weight_norm2", "dora_fwd", "dora_bwd",
-            "lora_fwd_static_scratch", "lora_tile_table",
+            "lora_fwd_static_scratch", "attn_workspace_size", "attn_fwd", "attn_bwd", "lora_tile_table",
             "lora_keep_threshold", "lora_pack_greedy", "lora_device_status", "lora_set_wait_limit_ns", "lora_debug_stuck_wait",
             "lora_debug_gemm_runs",
             "lora_status_string", "lora_timing_begin", "lora_timing_end", "lora_kernel_name",
@@ -34,6 +34,22 @@ class LoraAdapter(ctypes.Structure):
 class LoraSegment(ctypes.Structure):
     _fields_ = [("row_start", ctypes.c_int64), ("rows", ctypes.c_int64), ("adapter", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class AttnSeq(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_int64), ("q_rows", ctypes.c_int64), ("k_start", ctypes.c_int64),
+                ("k_rows", ctypes.c_int64)]
+
+
+class AttnStrides(ctypes.Structure):
+    _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [("q_rows", ctypes.c_int64), ("k_rows", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", AttnStrides), ("k", AttnStrides), ("v", AttnStrides), ("o", AttnStrides),
+                ("d_o", AttnStrides), ("d_q", AttnStrides), ("d_k", AttnStrides), ("d_v", AttnStrides)]
 
 
 class LoraError(RuntimeError):
@@ -78,6 +94,9 @@ def lib() -> ctypes.CDLL:
             "dora_bwd": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, f32, f32, u64, i64, i64, i64, i32, vp, vp,
                                vp, vp, vp, vp, sz, vp]),
             "lora_fwd_static_scratch": (i32, [vp, vp, vp, vp, f32, f32, u64, i64, i64, i64, i32, vp, vp, vp, vp]),
+            "attn_workspace_size": (sz, [i64, i32]),
+            "attn_fwd": (i32, [vp, vp, vp, ctypes.POINTER(AttnShape), vp, i32, vp, vp, vp, sz, vp]),
+            "attn_bwd": (i32, [vp, vp, vp, vp, vp, vp, ctypes.POINTER(AttnShape), vp, i32, vp, vp, vp, vp, sz, vp]),
             "lora_tile_table": (i32, [ctypes.POINTER(LoraSegment), i32, i32, i64, ctypes.POINTER(ctypes.c_int32),
                                       i64]),
             "lora_keep_threshold": (i32, [f32, ctypes.POINTER(ctypes.c_uint32)]),
@@ -120,6 +139,14 @@ def segments_array(segments):
     arr = (LoraSegment * max(1, len(segments)))()
     for i, (s, r, a) in enumerate(segments):
         arr[i].row_start, arr[i].rows, arr[i].adapter, arr[i].reserved = int(s), int(r), int(a), 0
+    return arr
+
+
+def attn_seqs_array(seqs):
+    """(q_start, q_rows, k_start, k_rows) of each sequence -> ctypes array of AttnSeq."""
+    arr = (AttnSeq * max(1, len(seqs)))()
+    for i, s in enumerate(seqs):
+        arr[i].q_start, arr[i].q_rows, arr[i].k_start, arr[i].k_rows = (int(x) for x in s)
     return arr
 
 
@@ -185,7 +212,7 @@ def gemm_runs(M: int, N: int, bn: int, stages: int, max_pairs: int, allow_split:
     return pairs.value, split.value, runs
 
 
-KERNEL_KINDS = 13
+KERNEL_KINDS = 24
 
 
 def timing_begin() -> None:

@@ -1,0 +1,284 @@
+"""Packed causal attention against the formula in 64 bits.
+
+Tolerances (2-norm of the difference over 2-norm of the reference, per tensor): outputs are rounded to bf16 (half a
+unit in the last place, 2^-9 relative at most, about 2^-9 / sqrt(3) = 1.1e-3 in the norm); P and dS are rounded to bf16
+once more before their products, another 1.1e-3 in the norm of each product (independent roundings of the terms, whose
+own norm is at most that of the result where the terms do not cancel, and a few times it where they do).  5e-3 leaves a
+factor of three over the two together.  lse is fp32 throughout: scores of size up to 20 with 2^-24 relative
+roundings in their sums of up to 128 products, and exponents and logarithms of 2^-22: 2e-5 absolute.
+"""
+import math
+
+import pytest
+
+from tests.gpu_helpers import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from lora_fine_tuning_gb300 import api, native  # noqa: E402
+
+TOL = 5e-3
+LSE_TOL = 2e-5
+
+
+def reference(Q, K, V, seqs, scale, dO=None):
+    """Sequence by sequence in 64 bits on the host.  Returns O, lse (and dQ, dK, dV)."""
+    q, k, v = (x.double().cpu() for x in (Q, K, V))
+    g = q.shape[1] // k.shape[1]
+    O, lse = torch.zeros_like(q), torch.full(q.shape[:2], -math.inf, dtype=torch.float64)
+    dQ, dK, dV = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    for qs, ql, ks, kl in seqs:
+        for i in range(0, ql):
+            if i + kl - ql >= 0:
+                break
+        else:
+            continue
+        rows = torch.arange(i, ql)
+        hidden = torch.arange(kl)[None] > (rows + kl - ql)[:, None]
+        for h in range(q.shape[1]):
+            qq, kk, vv = q[qs + rows, h], k[ks:ks + kl, h // g], v[ks:ks + kl, h // g]
+            S = (qq @ kk.T * scale).masked_fill(hidden, -math.inf)
+            L = torch.logsumexp(S, 1)
+            P = torch.exp(S - L[:, None])
+            O[qs + rows, h], lse[qs + rows, h] = P @ vv, L
+            if dO is not None:
+                do = dO.double().cpu()[qs + rows, h]
+                dP = do @ vv.T
+                dS = P * (dP - (P * dP).sum(1, keepdim=True)) * scale
+                dQ[qs + rows, h] = dS @ kk
+                dK[ks:ks + kl, h // g] += dS.T @ qq
+                dV[ks:ks + kl, h // g] += P.T @ do
+    return (O, lse) if dO is None else (O, lse, dQ, dK, dV)
+
+
+def off(got, ref):
+    got, ref = got.double().cpu(), ref
+    assert torch.isfinite(got).all()
+    n = ref.norm()
+    return float((got - ref).norm() / n) if n > 0 else float(got.norm())
+
+
+def check(Q, K, V, seqs, scale, dO, got):
+    O, lse, dQ, dK, dV = got
+    r = reference(Q, K, V, seqs, scale, dO)
+    assert torch.equal(torch.isinf(lse.cpu()), torch.isinf(r[1]))
+    fin = torch.isfinite(r[1])
+    if fin.any():
+        assert float((lse.double().cpu() - r[1])[fin].abs().max()) <= LSE_TOL
+    errs = {n: off(x, y) for n, x, y in zip(("O", "dQ", "dK", "dV"), (O, dQ, dK, dV), (r[0], *r[2:]))}
+    assert all(e <= TOL for e in errs.values()), errs
+
+
+def inputs(tq, tk, hq, hkv, d, layout="rows", seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(t, h):
+        x = torch.randn(max(t, 1) * h * d, device="cuda", generator=g).bfloat16()[:t * h * d]
+        return x.view(h, t, d).transpose(0, 1) if layout == "heads" else x.view(t, h, d)
+
+    if layout == "fused":
+        qkv = rand(tq, hq + 2 * hkv)
+        return qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], rand(tq, hq)
+    return rand(tq, hq), rand(tk, hkv), rand(tk, hkv), rand(tq, hq)
+
+
+def packed(lengths, pad=1):
+    out, at = [], 0
+    for n in lengths:
+        out.append((at, n, at, n))
+        at += -(-n // pad) * pad
+    return out, at
+
+
+def run(Q, K, V, dO, seqs, scale, **kw):
+    O, lse = api.attn_fwd(Q, K, V, seqs, scale=scale, **kw)
+    return (O, lse, *api.attn_bwd(dO, Q, K, V, O, lse, seqs, scale=scale, **kw))
+
+
+@pytest.mark.parametrize("lengths,pad", [
+    ([1], 1), ([2, 1, 3], 1), ([127], 1), ([128], 1), ([129], 1), ([64, 65, 63, 1, 200], 1), ([255, 257], 128),
+    ([700], 1), ([5, 0, 130, 0, 1], 1)])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (4, 2, 128)])
+def test_whole_prompts(lengths, pad, hq, hkv, d):
+    seqs, rows = packed(lengths, pad)
+    Q, K, V, dO = inputs(rows, rows, hq, hkv, d, seed=rows)
+    check(Q, K, V, seqs, d ** -0.5, dO, run(Q, K, V, dO, seqs, None))
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (6, 3), (7, 1), (8, 8), (8, 1), (28, 4), (128, 1), (12, 3)])
+def test_head_groups(hq, hkv):
+    seqs, rows = packed([150, 33], 1)
+    Q, K, V, dO = inputs(rows, rows, hq, hkv, 64, seed=hq)
+    check(Q, K, V, seqs, 0.125, dO, run(Q, K, V, dO, seqs, None))
+
+
+@pytest.mark.parametrize("d", [8, 24, 40, 72, 96, 104, 120])
+def test_head_widths(d):
+    seqs, rows = packed([140, 61], 1)
+    Q, K, V, dO = inputs(rows, rows, 4, 2, d, seed=d)
+    check(Q, K, V, seqs, 0.3, dO, run(Q, K, V, dO, seqs, 0.3))
+
+
+@pytest.mark.parametrize("layout", ["rows", "heads", "fused"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_layouts(layout, d):
+    seqs, rows = packed([200, 100], 128)
+    Q, K, V, dO = inputs(rows, rows, 4, 2, d, layout, seed=3)
+    got = run(Q, K, V, dO, seqs, None)
+    check(Q, K, V, seqs, d ** -0.5, dO, got)
+    # gradients into strided slices of one fused buffer
+    fused = torch.full((rows, 8, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    dQ, dK, dV = fused[:, :4], fused[:, 4:6], fused[:, 6:]
+    api.attn_bwd(dO, Q, K, V, got[0], got[1], seqs, dQ=dQ, dK=dK, dV=dV)
+    assert torch.equal(dQ, got[2]) and torch.equal(dK, got[3]) and torch.equal(dV, got[4])
+
+
+@pytest.mark.parametrize("seqs", [
+    [(0, 1, 0, 500)], [(0, 1, 0, 1), (1, 1, 1, 128), (2, 1, 129, 129), (3, 1, 258, 1000)],
+    [(0, 30, 0, 300), (30, 300, 300, 30), (330, 10, 330, 0), (340, 0, 330, 40), (340, 200, 370, 129)],
+    [(3, 130, 5, 257), (140, 5, 270, 5)], [(0, 300, 0, 1)]])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (4, 2, 128)])
+def test_queries_and_keys_of_different_lengths(seqs, hq, hkv, d):
+    tq, tk = seqs[-1][0] + seqs[-1][1] + 2, seqs[-1][2] + seqs[-1][3] + 3
+    Q, K, V, dO = inputs(tq, tk, hq, hkv, d, seed=tq)
+    check(Q, K, V, seqs, d ** -0.5, dO, run(Q, K, V, dO, seqs, None))
+
+
+def test_no_sequence_and_no_rows():
+    Q, K, V, dO = inputs(40, 50, 4, 2, 64)
+    O, lse, dQ, dK, dV = run(Q, K, V, dO, [], None)
+    assert not any(x.count_nonzero() for x in (O, dQ, dK, dV)) and bool((lse == -math.inf).all())
+    e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = api.attn_fwd(e, K, V, [(0, 0, 0, 50)])
+    assert O.shape == (0, 4, 64) and lse.shape == (0, 4)
+    dQ, dK, dV = api.attn_bwd(e, e, K, V, O, lse, [(0, 0, 0, 50)])
+    assert not dK.count_nonzero() and not dV.count_nonzero()
+    kv = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = api.attn_fwd(Q, kv, kv, [(0, 40, 0, 0)])
+    assert not O.count_nonzero() and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -3e38])
+def test_rows_beside_a_sequence_do_not_reach_it(bad):
+    """Rows of no sequence, and another sequence's rows, hold infinities and NaN."""
+    seqs = [(0, 100, 0, 100), (128, 70, 128, 70), (198, 130, 198, 130)]
+    Q, K, V, dO = inputs(400, 400, 4, 2, 128, seed=5)
+    clean = run(Q, K, V, dO, seqs, None)
+    Q2, K2, V2, dO2 = (x.clone() for x in (Q, K, V, dO))
+    for x in (Q2, K2, V2, dO2):
+        x[100:198] = bad
+        x[328:] = bad
+    dirty = run(Q2, K2, V2, dO2, seqs, None)
+    for a, b in zip(clean, dirty):
+        for s in (slice(0, 100), slice(198, 328)):
+            assert torch.equal(a[s], b[s])
+        assert torch.equal(a[100:128], b[100:128]) and torch.equal(a[328:], b[328:])
+
+
+def test_large_scores_and_growing_maxima():
+    """Scores that grow along the keys (every tile raises the running maximum) and scores of size 1e4."""
+    Q, K, V, dO = inputs(1024, 1024, 2, 1, 64, seed=7)
+    grow = (K.float() * 0.05 + torch.linspace(0, 30, 1024, device="cuda")[:, None, None] / 8).bfloat16()
+    ones = (Q.float() * 0.05 + 1).bfloat16()
+    seqs = [(0, 1024, 0, 1024)]
+    O, lse, dQ, dK, dV = run(ones, grow, V, dO, seqs, None)
+    ref = reference(ones, grow, V, seqs, 0.125, dO)
+    assert float((lse.double().cpu() - ref[1]).abs().max()) <= LSE_TOL
+    errs = {n: off(x, y) for n, x, y in zip(("O", "dK", "dV"), (O, dK, dV), (ref[0], ref[3], ref[4]))}
+    assert all(e <= TOL for e in errs.values()), errs
+    # dQ = dS K: here every feature of K grows alike and dS sums to zero along the keys, so the terms cancel and the
+    # rounding of each to bf16 does not; the tolerance is of the terms' size, |dS| |K|
+    q, k, v, do = (x.double().cpu() for x in (ones, grow, V, dO))
+    hidden = torch.ones(1024, 1024, dtype=torch.bool).triu(1)
+    size = torch.zeros_like(q)
+    for h in range(2):
+        P = torch.softmax((q[:, h] @ k[:, 0].T * 0.125).masked_fill(hidden, -math.inf), 1)
+        dP = do[:, h] @ v[:, 0].T
+        size[:, h] = (P * (dP - (P * dP).sum(1, keepdim=True))).abs() @ k[:, 0].abs() * 0.125
+    assert float((dQ.double().cpu() - ref[2]).norm()) <= TOL * float(size.norm())
+    O, lse = api.attn_fwd((Q.float() * 100).bfloat16(), (K.float() * 100).bfloat16(), V, seqs)
+    assert torch.isfinite(O).all() and torch.isfinite(lse).all()
+
+
+def test_gradients_against_differences():
+    """Central differences of sum(O * dO) computed in 64 bits along random directions, step 1e-3: the truncation
+    error is 1e-6 of the value, so the bound is that of the kernel's bf16 gradients, 5e-3 of |gradient| |direction|
+    (their error is not aligned with the direction: half of that is far more than the expected projection)."""
+    seqs, rows = packed([90, 41], 1)
+    Q, K, V, dO = inputs(rows, rows, 4, 2, 64, seed=11)
+    _, _, dQ, dK, dV = run(Q, K, V, dO, seqs, None)
+    g = torch.Generator().manual_seed(1)
+    base = [x.double().cpu() for x in (Q, K, V)]
+    for i, grad in enumerate((dQ, dK, dV)):
+        direction = torch.randn(base[i].shape, generator=g, dtype=torch.float64)
+        vals = []
+        for s in (1e-3, -1e-3):
+            x = list(base)
+            x[i] = x[i] + s * direction
+            vals.append(float((reference(*x, seqs, 0.125)[0] * dO.double().cpu()).sum()))
+        num = (vals[0] - vals[1]) / 2e-3
+        ana = float((grad.double().cpu() * direction).sum())
+        assert abs(num - ana) <= 5e-3 * float(grad.double().norm()) * 3, (i, num, ana)
+
+
+def test_repeated_calls_and_streams():
+    """Bit-identical from call to call, on the default stream and on another with outputs of its own."""
+    seqs, rows = packed([500, 300, 130], 128)
+    Q, K, V, dO = inputs(rows, rows, 8, 2, 128, seed=13)
+    first = run(Q, K, V, dO, seqs, None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side, None, side):
+        again = run(Q, K, V, dO, seqs, None, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_graph_capture():
+    seqs, rows = packed([300, 77], 1)
+    table = api.attn_seqs(seqs)
+    Q, K, V, dO = inputs(rows, rows, 4, 2, 64, seed=17)
+    want = run(Q, K, V, dO, table, None)
+    O, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    dQ, dK, dV = (torch.empty_like(x) for x in want[2:])
+    ws = torch.zeros(api.attn_workspace_size(rows, 4), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.attn_fwd(Q, K, V, table, O=O, lse=lse, ws=ws)
+        api.attn_bwd(dO, Q, K, V, O, lse, table, dQ=dQ, dK=dK, dV=dV, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, (O, lse, dQ, dK, dV)))
+    assert api.lora_device_status(ws) == 0
+
+
+def test_refusals():
+    Q, K, V, dO = inputs(64, 64, 4, 2, 64)
+
+    def refused(status, seqs=((0, 64, 0, 64),), q=Q, k=K, v=V, **kw):
+        with pytest.raises(native.LoraError) as e:
+            api.attn_fwd(q, k, v, list(seqs), **kw)
+        assert e.value.status == status
+
+    refused(8, [(0, 65, 0, 64)])                                   # past the rows
+    refused(8, [(0, 40, 0, 40), (39, 10, 40, 10)])                 # shared row
+    refused(8, [(32, 10, 0, 10), (0, 10, 10, 10)])                 # not in row order
+    refused(8, [(0, -1, 0, 4)])
+    refused(8, [(i, 0, 0, 0) for i in range(64)] * 17)             # too many, and out of order
+    refused(1, scale=0.0)
+    refused(1, scale=math.inf)
+    refused(3, q=inputs(64, 64, 3, 2, 64)[0])                      # 3 query heads over 2
+    refused(3, *[[(0, 64, 0, 64)]], q=inputs(64, 64, 4, 2, 136)[0], k=inputs(64, 64, 4, 2, 136)[1],
+            v=inputs(64, 64, 4, 2, 136)[2])                        # head too wide
+    refused(2, q=torch.zeros(64 * 256 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(64, 4, 64))   # misaligned
+    refused(6, ws=torch.zeros(128, dtype=torch.uint8, device="cuda"))
+    wide = torch.zeros(64, 4, 66, dtype=torch.bfloat16, device="cuda")[:, :, :64]
+    refused(2, q=wide)                                             # strides not a multiple of 8
+    refused(3, O=torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda").expand(64, 4, 64))
+    with pytest.raises(ValueError):
+        api.attn_fwd(Q, K, V[:32], [(0, 64, 0, 64)])
+    with pytest.raises(TypeError):
+        api.attn_fwd(Q.float(), K, V, [(0, 64, 0, 64)])
