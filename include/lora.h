@@ -322,6 +322,87 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
                      int32_t n_seqs, lora_bf16* dQ, lora_bf16* dK, lora_bf16* dV, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/* Losses on logits, with the gradient of the logits: what an adapter is trained on from preferences or from rewards.
+ *
+ * logits is rows x vocab (bf16 or fp32, row stride ld), one row a token; labels (int64, device) name the token each row
+ * should predict, and a row whose label is outside [0, vocab) (prompt, padding) does not count: its logp is 0, its
+ * dlogits row is zeros, its logits are not read.  logp receives log p of every other row's label (fp32).  dlogits
+ * (optional; same type, row stride dlogits_ld) receives the gradient of *loss; it may be the logits themselves (same
+ * stride): each element is written where it was read.  NULL: the loss and logp only.
+ *  - Pointers need their element's alignment only, rows may start anywhere (odd vocab, sliced logits); vocab up to
+ *    262144, rows up to 262144.  Rows past `vocab` elements (padding up to ld) are neither read nor written.
+ *  - Softmax statistics are fp32 relative to each row's maximum, sums over tokens fp64, in a fixed order: results are
+ *    bit-identical from call to call.  Logits of -inf (a restricted vocabulary) have probability 0.
+ *  - workspace: loss_workspace_size(rows) bytes, 256-byte aligned, scratch whose contents do not matter. */
+enum { LORA_BF16 = 0, LORA_F32 = 1 };
+enum { LORA_MAX_VOCAB = 262144, LORA_MAX_PAIRS = 1024 };
+
+typedef struct {
+    const void* logits;
+    void* dlogits;
+    int64_t rows, vocab, ld, dlogits_ld;
+    const int64_t* labels;
+    float* logp;
+    int32_t dtype; /* LORA_BF16 or LORA_F32, of logits and dlogits */
+    int32_t reserved;
+} lora_logits;
+
+/* Rows [chosen_start, chosen_start + chosen_rows) answer one prompt better than the rejected ones.  Rows of no pair
+ * count for logp only. */
+typedef struct {
+    int64_t chosen_start, rejected_start, chosen_rows, rejected_rows;
+} lora_pref_pair;
+
+size_t loss_workspace_size(int64_t rows);
+
+/* Preference loss of paired log ratios:
+ *   margin_i = sum_{t in chosen_i} (logp_t - ref_t) - sum_{t in rejected_i} (logp_t - ref_t),  h_i = beta margin_i
+ *   *loss = scale * sum_i [ -(1 - label_smoothing) log sigmoid(h_i) - label_smoothing log sigmoid(-h_i) ]
+ * ref_logp (rows, fp32): the reference policy's log p of each label, as this call returns logp when it runs on the
+ * model without its adapters; NULL for none (zeros).  pairs is a HOST array, read before the call returns; no row may
+ * belong to two responses (LORA_ETABLE).  margins receives margin_i (n_pairs, fp32). */
+lora_status pref_loss(const lora_logits* logits, const lora_pref_pair* pairs, int32_t n_pairs, const float* ref_logp,
+                      float beta, float label_smoothing, float scale, float* loss, float* margins, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Clipped policy loss with a KL term:
+ *   r_t = exp(logp_t - old_t),  x_t = ref_t - logp_t
+ *   *loss = scale * sum_t [ -min(r_t A_t, clip(r_t, 1 - clip_low, 1 + clip_high) A_t) + kl_coef (exp(x_t) - x_t - 1) ]
+ * over the rows that count; old_logp and advantages (A) are per row, fp32, ref_logp may be NULL when kl_coef is 0.
+ * Where r_t lies on an end of the clip range the unclipped branch's gradient is taken. */
+lora_status policy_loss(const lora_logits* logits, const float* old_logp, const float* advantages,
+                        const float* ref_logp, float clip_low, float clip_high, float kl_coef, float scale, float* loss,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* One AdamW step over many tensors (adapters, magnitudes, biases) in as few launches as the table allows:
+ *   g = grad * (*grad_scale),  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, with the states and the parameter written back in place.
+ *  - param and grad are bf16 or fp32 each; master (optional, bf16 parameters only) is an fp32 copy that holds the
+ *    parameter: it is updated and param is its rounding.  Without it a bf16 param is read, updated and rounded.
+ *  - state_bits 32: m and v are fp32.  state_bits 8: m and sqrt(v) are e4m3 codes, one byte each, with an fp32 scale for
+ *    every 256 consecutive values (m_scale, v_scale: ceil(n / 256) each; value = code * scale; scale = largest / 448, a
+ *    block whose largest value is below 2^-100 is held as zeros; a positive sqrt(v) gets at least the smallest code).
+ *    States start as zeros (codes and scales) in either form.
+ *  - tensors is a HOST array, read before the call returns; pointers are 16-byte aligned (scales: 4), tensors do not
+ *    overlap.  grad_scale (optional): one fp32 on the device, for example a clipping factor.  step counts from 1. */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    float* master;
+    int64_t n;
+    int32_t param_dtype, grad_dtype; /* LORA_BF16 or LORA_F32 */
+    int32_t state_bits;              /* 8 or 32 */
+    int32_t reserved;
+} lora_adamw_tensor;
+
+lora_status adamw_step(const lora_adamw_tensor* tensors, int32_t n_tensors, double lr, double beta1, double beta2,
+                       double eps, double weight_decay, int64_t step, const float* grad_scale, void* stream);
+
 /* Host only, no GPU needed: the routing table.  tile_adapter[i] (i < ceil(m/128))
  * receives the adapter of tile i, -1 where no segment covers it. */
 lora_status lora_tile_table(const lora_segment* segments, int32_t n_segments, int32_t n_adapters, int64_t m,

@@ -410,6 +410,195 @@ def attn_workspace_size(q_rows: int, q_heads: int) -> int:
     return int(native.lib().attn_workspace_size(q_rows, q_heads))
 
 
+# ---------------------------------------------------------------------------------------------------------------
+# losses on logits
+# ---------------------------------------------------------------------------------------------------------------
+
+class PrefPairs:
+    """Pairs of responses: (chosen_start, rejected_start, chosen_rows, rejected_rows) each.  Made once a batch."""
+
+    def __init__(self, pairs):
+        self.pairs = [tuple(int(x) for x in q) for q in pairs]
+        if any(len(q) != 4 for q in self.pairs):
+            raise ValueError("each pair is (chosen_start, rejected_start, chosen_rows, rejected_rows)")
+        self.array = native.pref_pairs_array(self.pairs)
+
+    def __len__(self):
+        return len(self.pairs)
+
+
+def pref_pairs(pairs) -> PrefPairs:
+    return pairs if isinstance(pairs, PrefPairs) else PrefPairs(pairs)
+
+
+_DTYPES = {torch.bfloat16: native.BF16, torch.float32: native.F32}
+
+
+def _check_rows(name: str, t, rows: int, dtype) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != rows or t.dim() != 1:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} vector of {rows}")
+
+
+def _logits(on, logits, labels, logp, dlogits, want_grad):
+    """Checks the logits and their companions.  Returns (lora_logits, logp, dlogits)."""
+    if logits.dtype not in _DTYPES or not logits.is_cuda or logits.dim() != 2:
+        raise TypeError("logits must be a CUDA bfloat16 or float32 matrix")
+    rows, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    _check_rows("labels", labels, rows, torch.int64)
+    ld = logits.stride(0) if rows > 1 else vocab
+    if logp is None:
+        logp = on.empty((rows,), torch.float32)
+    _check_rows("logp", logp, rows, torch.float32)
+    if dlogits is None and want_grad:
+        # rows as far apart as the logits' own: whole 16-byte vectors are then stored as they were loaded
+        dlogits = on.empty((max(rows, 1) * ld,), logits.dtype).as_strided((rows, vocab), (ld, 1))
+    d_ld = vocab
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype or not dlogits.is_cuda or dlogits.shape != logits.shape or \
+                (vocab > 1 and dlogits.stride(1) != 1):
+            raise ValueError(f"dlogits must be a CUDA {logits.dtype} matrix of shape {tuple(logits.shape)}, rows contiguous")
+        d_ld = dlogits.stride(0) if rows > 1 else ld
+    g = native.Logits(_ptr(logits), _ptr(dlogits), rows, vocab, ld, d_ld, _ptr(labels), _ptr(logp),
+                      _DTYPES[logits.dtype], 0)
+    return g, logp, dlogits
+
+
+def loss_workspace_size(rows: int) -> int:
+    return int(native.lib().loss_workspace_size(rows))
+
+
+def pref_loss(logits, labels, pairs, ref_logp=None, *, beta: float = 0.1, label_smoothing: float = 0.0,
+              scale: float = 1.0, want_grad: bool = True, dlogits=None, logp=None, loss=None, margins=None, ws=None,
+              stream=None):
+    """Preference loss of pairs of responses (include/lora.h): scale * sum over pairs of
+    -(1 - e) log sigmoid(beta margin) - e log sigmoid(-beta margin).  logits: rows x vocab, bf16 or fp32; labels: the
+    token each row should predict (outside [0, vocab): the row does not count); pairs: pref_pairs(...) or what it
+    takes; ref_logp: the reference policy's log p of each label.  Returns (loss, logp, margins, dlogits or None);
+    dlogits=logits writes the gradient in place."""
+    pairs = pref_pairs(pairs)
+    on = _On(logits, stream)
+    g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
+    _check_rows("ref_logp", ref_logp, logits.shape[0], torch.float32)
+    loss = loss if loss is not None else on.empty((), torch.float32)
+    margins = margins if margins is not None else on.empty((len(pairs),), torch.float32)
+    _check_f32("loss", loss, 1)
+    _check_f32("margins", margins, len(pairs))
+    ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
+    st = native.lib().pref_loss(ctypes.byref(g), pairs.array, len(pairs), _ptr(ref_logp), float(beta),
+                                float(label_smoothing), float(scale), _ptr(loss), _ptr(margins), _ptr(ws), ws.numel(),
+                                on.handle)
+    native.check("pref_loss", st)
+    return loss, logp, margins, dlogits
+
+
+def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, *, clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, scale: float = 1.0, want_grad: bool = True, dlogits=None, logp=None, loss=None,
+                ws=None, stream=None):
+    """Clipped policy loss with a KL term (include/lora.h): scale * sum over rows of
+    -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(x) - x - 1), r = exp(logp - old_logp),
+    x = ref_logp - logp.  Returns (loss, logp, dlogits or None); dlogits=logits writes the gradient in place."""
+    on = _On(logits, stream)
+    g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
+    for name, t in (("old_logp", old_logp), ("advantages", advantages), ("ref_logp", ref_logp)):
+        _check_rows(name, t, logits.shape[0], torch.float32)
+    loss = loss if loss is not None else on.empty((), torch.float32)
+    _check_f32("loss", loss, 1)
+    ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
+    st = native.lib().policy_loss(ctypes.byref(g), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp), float(clip_low),
+                                  float(clip_high), float(kl_coef), float(scale), _ptr(loss), _ptr(ws), ws.numel(),
+                                  on.handle)
+    native.check("policy_loss", st)
+    return loss, logp, dlogits
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------------------------------------------
+
+ADAMW_BLOCK = 256   # values that share a scale in 8-bit states
+
+
+@dataclass
+class AdamWTensor:
+    """One parameter with its gradient and states.  fp32 states: m and v like the parameter.  8-bit states: m and v
+    (sqrt(v)) are uint8 or float8_e4m3fn codes, m_scale and v_scale fp32, one for each 256 values.  master: optional
+    fp32 copy of a bf16 parameter."""
+    param: torch.Tensor
+    grad: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    master: Optional[torch.Tensor] = None
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def adamw_tensor(param, grad, *, bits: int = 32, master: bool = False) -> AdamWTensor:
+    """An AdamWTensor with zero states (and, with `master`, an fp32 copy of the parameter)."""
+    n, blocks = param.numel(), -(-param.numel() // ADAMW_BLOCK)
+    copy = param.detach().float().clone() if master else None
+    if bits == 32:
+        m, v = (torch.zeros(param.shape, dtype=torch.float32, device=param.device) for _ in range(2))
+        return AdamWTensor(param, grad, m, v, copy)
+    if bits != 8:
+        raise ValueError("bits is 8 or 32")
+    m, v = (torch.zeros(n, dtype=torch.uint8, device=param.device) for _ in range(2))
+    ms, vs = (torch.zeros(blocks, dtype=torch.float32, device=param.device) for _ in range(2))
+    return AdamWTensor(param, grad, m, v, copy, ms, vs)
+
+
+class AdamWTensors:
+    """The optimiser's list of tensors, checked and laid out once for every step."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.array = (native.AdamWTensor * max(1, len(self.tensors)))()
+        for a, t in zip(self.array, self.tensors):
+            n = t.param.numel()
+            for name in ("param", "grad"):
+                x = getattr(t, name)
+                if x.dtype not in _DTYPES or not x.is_cuda or not x.is_contiguous() or x.numel() != n:
+                    raise ValueError(f"{name} must be a contiguous CUDA bfloat16 or float32 tensor of {n}")
+            eight = t.m.dtype in (torch.uint8, torch.float8_e4m3fn)
+            for name, x in (("m", t.m), ("v", t.v)):
+                if x.dtype != t.m.dtype or not (eight or x.dtype == torch.float32) or not x.is_cuda or \
+                        not x.is_contiguous() or x.numel() != n:
+                    raise ValueError(f"{name} must be a contiguous CUDA tensor of {n}, float32 or 8-bit codes like m")
+            for name, x in (("m_scale", t.m_scale), ("v_scale", t.v_scale)):
+                if eight and x is None:
+                    raise ValueError(f"8-bit states need {name}")
+                if x is not None:
+                    _check_f32(name, x, -(-n // ADAMW_BLOCK))
+            if t.master is not None:
+                _check_f32("master", t.master, n)
+            a.param, a.grad, a.m, a.v = _ptr(t.param), _ptr(t.grad), _ptr(t.m), _ptr(t.v)
+            a.m_scale, a.v_scale, a.master = _ptr(t.m_scale), _ptr(t.v_scale), _ptr(t.master)
+            a.n, a.param_dtype, a.grad_dtype = n, _DTYPES[t.param.dtype], _DTYPES[t.grad.dtype]
+            a.state_bits = 8 if eight else 32
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def adamw_tensors(tensors) -> AdamWTensors:
+    return tensors if isinstance(tensors, AdamWTensors) else AdamWTensors(tensors)
+
+
+def adamw_step(tensors, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.0, step: int, grad_scale=None, stream=None) -> None:
+    """One AdamW step (include/lora.h) over `tensors` (adamw_tensors(...) or a list of AdamWTensor), in place.
+    grad_scale: optional fp32 scalar on the device that multiplies every gradient; step counts from 1."""
+    tensors = adamw_tensors(tensors)
+    if grad_scale is not None:
+        _check_f32("grad_scale", grad_scale, 1)
+    st = native.lib().adamw_step(tensors.array, len(tensors), float(lr), float(beta1), float(beta2), float(eps),
+                                 float(weight_decay), int(step), _ptr(grad_scale), _stream(stream))
+    native.check("adamw_step", st)
+
+
 def lora_device_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises the stream; returns the raw device status code of the workspace (0 = fine) and clears it."""
     code = ctypes.c_int32(0)

@@ -14,7 +14,6 @@
 #include "host.h"
 #include "kernels.h"
 #include "lora.h"
-#include "optim.h"
 #include "plan.h"
 
 namespace lora {

@@ -19,7 +19,8 @@ STATUS_NAMES = {0: "LORA_OK", 1: "LORA_EINVAL", 2: "LORA_EALIGN", 3: "LORA_ESHAP
 # Symbols include/lora.h declares, in declaration order.
 EXPORTED = ["lora_workspace_size", "lora_set_deterministic", "lora_get_deterministic", "lora_fwd", "lora_bwd", "multi_lora_fwd", "multi_lora_bwd",
             "dora_workspace_size", "dora_weight_norm2", "dora_fwd", "dora_bwd",
-            "lora_fwd_static_scratch", "attn_workspace_size", "attn_fwd", "attn_bwd", "lora_tile_table",
+            "lora_fwd_static_scratch", "attn_workspace_size", "attn_fwd", "attn_bwd",
+            "loss_workspace_size", "pref_loss", "policy_loss", "adamw_step", "lora_tile_table",
             "lora_keep_threshold", "lora_pack_greedy", "lora_device_status", "lora_set_wait_limit_ns", "lora_debug_stuck_wait",
             "lora_debug_gemm_runs",
             "lora_status_string", "lora_timing_begin", "lora_timing_end", "lora_kernel_name",
@@ -52,6 +53,28 @@ class AttnShape(ctypes.Structure):
                 ("d_o", AttnStrides), ("d_q", AttnStrides), ("d_k", AttnStrides), ("d_v", AttnStrides)]
 
 
+BF16, F32 = 0, 1
+
+
+class Logits(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64), ("dlogits_ld", ctypes.c_int64),
+                ("labels", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class PrefPair(ctypes.Structure):
+    _fields_ = [("chosen_start", ctypes.c_int64), ("rejected_start", ctypes.c_int64), ("chosen_rows", ctypes.c_int64),
+                ("rejected_rows", ctypes.c_int64)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class LoraError(RuntimeError):
     def __init__(self, fn: str, status: int):
         detail = ""
@@ -75,8 +98,8 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
                                f"g.build()'` (or python -m lora_fine_tuning_gb300.build)")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i32, i64, u64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
-                                      ctypes.c_float, ctypes.c_size_t)
+        vp, i32, i64, u64, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
+                                           ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
         sig = {
             "lora_workspace_size": (sz, [i64, i64, i64, i32, i32]),
             "lora_set_deterministic": (i32, [i32]),
@@ -97,6 +120,10 @@ def lib() -> ctypes.CDLL:
             "attn_workspace_size": (sz, [i64, i32]),
             "attn_fwd": (i32, [vp, vp, vp, ctypes.POINTER(AttnShape), vp, i32, vp, vp, vp, sz, vp]),
             "attn_bwd": (i32, [vp, vp, vp, vp, vp, vp, ctypes.POINTER(AttnShape), vp, i32, vp, vp, vp, vp, sz, vp]),
+            "loss_workspace_size": (sz, [i64]),
+            "pref_loss": (i32, [ctypes.POINTER(Logits), vp, i32, vp, f32, f32, f32, vp, vp, vp, sz, vp]),
+            "policy_loss": (i32, [ctypes.POINTER(Logits), vp, vp, vp, f32, f32, f32, f32, vp, vp, sz, vp]),
+            "adamw_step": (i32, [vp, i32, f64, f64, f64, f64, f64, i64, vp, vp]),
             "lora_tile_table": (i32, [ctypes.POINTER(LoraSegment), i32, i32, i64, ctypes.POINTER(ctypes.c_int32),
                                       i64]),
             "lora_keep_threshold": (i32, [f32, ctypes.POINTER(ctypes.c_uint32)]),
@@ -147,6 +174,14 @@ def attn_seqs_array(seqs):
     arr = (AttnSeq * max(1, len(seqs)))()
     for i, s in enumerate(seqs):
         arr[i].q_start, arr[i].q_rows, arr[i].k_start, arr[i].k_rows = (int(x) for x in s)
+    return arr
+
+
+def pref_pairs_array(pairs):
+    """(chosen_start, rejected_start, chosen_rows, rejected_rows) of each pair -> ctypes array of PrefPair."""
+    arr = (PrefPair * max(1, len(pairs)))()
+    for i, q in enumerate(pairs):
+        arr[i].chosen_start, arr[i].rejected_start, arr[i].chosen_rows, arr[i].rejected_rows = (int(x) for x in q)
     return arr
 
 
