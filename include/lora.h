@@ -385,7 +385,8 @@ lora_status policy_loss(const lora_logits* logits, const float* old_logp, const 
  *    block whose largest value is below 2^-100 is held as zeros; a positive sqrt(v) gets at least the smallest code).
  *    States start as zeros (codes and scales) in either form.
  *  - tensors is a HOST array, read before the call returns; pointers are 16-byte aligned (scales: 4), tensors do not
- *    overlap.  grad_scale (optional): one fp32 on the device, for example a clipping factor.  step counts from 1. */
+ *    overlap.  grad_scale (optional): one fp32 on the device, for example a clipping factor.  step counts from 1, eps is
+ *    at least 1e-30. */
 typedef struct {
     void* param;
     const void* grad;

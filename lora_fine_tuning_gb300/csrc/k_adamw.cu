@@ -4,7 +4,7 @@
 //   p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
 //
 // Bound by memory: every state is read and written once, 16 bytes at a time (22 bytes a bf16 value with fp32 states,
-// 10 with 8-bit states).  A CTA works on 4096 consecutive values of one tensor; the table of tensors is a kernel
+// 10 with 8-bit states).  A CTA works on one chunk of consecutive values of one tensor; the table of tensors is a kernel
 // parameter that the CTA searches for its chunk.
 //
 // 8-bit states: m and sqrt(v) in e4m3, 256 values with one fp32 scale (largest value / 448).  sqrt(v) has half the
@@ -22,42 +22,86 @@ namespace {
 
 constexpr int kT = 256;
 constexpr int kPer = 8;                                // values of a lane: 16 bytes of bf16
-constexpr int kRounds = kAdamChunk / (kT * kPer);
+template <bool B8>
+constexpr int kRounds = (B8 ? kAdamChunk8 : kAdamChunk32) / (kT * kPer);
 static_assert(kPer * 32 == kAdamBlock, "a warp holds one block of the 8-bit states");
 constexpr float kE4m3Max = 448.f;
+constexpr float kSmallest = 0.001953125f;              // 2^-9, e4m3's smallest positive value
 constexpr float kTiny = 7.888609052210118e-31f;        // 2^-100: a block below this is held as zeros
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Two fp32 values in a register pair: one instruction, one IEEE rounding a value.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// Eight values of a lane as they lie in memory, bf16 or fp32 (with `left` < 8 the rest is zero).
+template <bool kF32>
+struct Raw8 {
+    uint4 v[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, int64_t at, int left) {
+        if (left >= 8) {
+#pragma unroll
+            for (int i = 0; i < (kF32 ? 2 : 1); ++i)
+                v[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * (kF32 ? 4 : 2)) + i);
+            return;
+        }
+        uint32_t w[kF32 ? 8 : 4];
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) {
+                if (kF32) w[i] = static_cast<const uint32_t*>(p)[at + i];
+                else w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + i]) << (16 * (i & 1));
+            }
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __device__ __forceinline__ void get(F2 (&x)[4]) const {
+        if (kF32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 q = v[kF32 ? i : 0];
+                x[2 * i] = f2(__uint_as_float(q.x), __uint_as_float(q.y));
+                x[2 * i + 1] = f2(__uint_as_float(q.z), __uint_as_float(q.w));
+            }
+        } else {
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        }
+    }
+};
+
+template <bool f32>
+__device__ __forceinline__ void store8(void* p, int64_t at, int left, const F2 (&pairs)[4]) {
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        const float2 q = parts(pairs[i]);
+        x[2 * i] = q.x;
+        x[2 * i + 1] = q.y;
     }
-}
-
-// `left` values (8 or more: all) from p at `at`, bf16 or fp32.
-__device__ __forceinline__ void load8(const void* p, int64_t at, int left, bool f32, float (&x)[8]) {
-    if (left >= 8) {
-        if (f32) {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-            const float4 a = __ldcs(q), b = __ldcs(q + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-            unpack8(__ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at)), x);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = 0.f;
-        if (i < left)
-            x[i] = f32 ? static_cast<const float*>(p)[at + i]
-                       : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at + i]) << 16);
-    }
-}
-
-__device__ __forceinline__ void store8(void* p, int64_t at, int left, bool f32, const float (&x)[8]) {
     if (left >= 8) {
         if (f32) {
             float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
@@ -78,6 +122,13 @@ __device__ __forceinline__ void store8(void* p, int64_t at, int left, bool f32, 
     }
 }
 
+// 1 / x to 2^-22; x is at least eps, a normal number.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two e4m3 codes -> two floats, and back (round to nearest even, finite values saturate).
 __device__ __forceinline__ float2 from_e4m3(uint32_t codes) {
     uint32_t h;
@@ -92,43 +143,62 @@ __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t at, int left, float scale, float (&x)[8]) {
+__device__ __forceinline__ uint2 load_codes(const void* codes, int64_t at, int left) {
+    const uint8_t* p = static_cast<const uint8_t*>(codes);
+    if (left >= 8) return __ldcs(reinterpret_cast<const uint2*>(p + at));
     uint2 c = make_uint2(0u, 0u);
-    if (left >= 8) {
-        c = __ldcs(reinterpret_cast<const uint2*>(p + at));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) {
-                if (i < 4) c.x |= static_cast<uint32_t>(p[at + i]) << (8 * i);
-                else c.y |= static_cast<uint32_t>(p[at + i]) << (8 * (i - 4));
-            }
-    }
+    for (int i = 0; i < 8; ++i)
+        if (i < left) {
+            if (i < 4) c.x |= static_cast<uint32_t>(p[at + i]) << (8 * i);
+            else c.y |= static_cast<uint32_t>(p[at + i]) << (8 * (i - 4));
+        }
+    return c;
+}
+__device__ __forceinline__ void decode(uint2 c, float scale, F2 (&x)[4]) {
     const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = from_e4m3(w[i]);
-        x[2 * i] = __fmul_rn(f.x, scale);
-        x[2 * i + 1] = __fmul_rn(f.y, scale);
+        x[i] = mul(f2(f.x, f.y), f2(scale, scale));
     }
 }
 
-// One block (this warp's 256 values; x is 0 past the tensor's end) in 8 bits.
+// The largest |x| of two values and a third, a NaN if one is there.
+__device__ __forceinline__ float max_abs(float t, float2 x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(t), "f"(fabsf(x.x)), "f"(fabsf(x.y)));
+    return r;
+}
+
+// One block (this warp's 256 values; x is 0 past the tensor's end) in 8 bits.  kPositive: x is not negative.
 template <bool kPositive>
-__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int64_t at, int left, const float (&x)[8]) {
-    uint32_t top_bits = 0;
+__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int64_t at, int left, const F2 (&x)[4]) {
+    float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top_bits = max(top_bits, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top_bits));   // NaN and infinity order above the rest
+    for (int i = 0; i < 4; ++i) most = max_abs(most, parts(x[i]));
+    // the sign is clear: values order like their bits, infinity and NaN above the rest
+    float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
     if (!(top >= kTiny)) top = 0.f;
     const float f = top > 0.f ? __fmul_rn(__frcp_rn(top), kE4m3Max) : 0.f;
-    float y[8];
+    float2 y[4];
+    float least = kE4m3Max;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = __fmul_rn(x[i], f);
-        if (kPositive && x[i] > 0.f && top > 0.f) y[i] = fmaxf(y[i], 0.001953125f);
+    for (int i = 0; i < 4; ++i) {
+        y[i] = parts(mul(x[i], f2(f, f)));
+        if (kPositive) least = fminf(least, fminf(y[i].x, y[i].y));
     }
-    const uint2 c = make_uint2(to_e4m3(y[0], y[1]) | (to_e4m3(y[2], y[3]) << 16), to_e4m3(y[4], y[5]) | (to_e4m3(y[6], y[7]) << 16));
+    // rare: a value below the smallest code (and the zeros, which stay zeros)
+    if (kPositive && least < kSmallest && top > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 q = parts(x[i]);
+            if (q.x > 0.f) y[i].x = fmaxf(y[i].x, kSmallest);
+            if (q.y > 0.f) y[i].y = fmaxf(y[i].y, kSmallest);
+        }
+    }
+    const uint2 c = make_uint2(to_e4m3(y[0].x, y[0].y) | (to_e4m3(y[1].x, y[1].y) << 16),
+                               to_e4m3(y[2].x, y[2].y) | (to_e4m3(y[3].x, y[3].y) << 16));
     if (left >= 8) {
         __stcs(reinterpret_cast<uint2*>(p + at), c);
     } else {
@@ -139,68 +209,128 @@ __device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int64_t at
     if (lane_id() == 0) *scale = __fmul_rn(top, 1.f / kE4m3Max);
 }
 
-template <int N>
-__global__ void __launch_bounds__(kT) adamw_kernel(const __grid_constant__ AdamStep s, const __grid_constant__ AdamTensors<N> table) {
+// What one round of a lane reads.
+template <bool PF, bool GF, bool B8, bool MA>
+struct Loads {
+    Raw8<GF> g;
+    Raw8<PF || MA> p;
+    Raw8<true> m, v;           // fp32 states
+    uint2 mc, vc;              // 8-bit states
+    float ms, vs;
+    __device__ __forceinline__ void load(const AdamTensor& t, int64_t at, int left) {
+        g.load(t.grad, at, left);
+        p.load(MA ? t.master : t.param, at, left);
+        if (B8) {
+            mc = load_codes(t.m, at, left);
+            vc = load_codes(t.v, at, left);
+            const int64_t block = at / kAdamBlock;   // of the warp's first lane: inside the tensor
+            ms = t.m_scale[block];
+            vs = t.v_scale[block];
+        } else {
+            m.load(t.m, at, left);
+            v.load(t.v, at, left);
+        }
+    }
+};
+
+// The CTA's chunk: the loads of the next round are in flight while this one is worked on.
+template <bool PF, bool GF, bool B8, bool MA>
+__device__ __forceinline__ void chunk_step(const AdamStep& s, const AdamTensor& t, int64_t first, float gs) {
+    Loads<PF, GF, B8, MA> in, next;
+    const int64_t warp_first = first - static_cast<int64_t>(lane_id()) * kPer;
+    const auto left_at = [&](int r) {
+        return static_cast<int>(min(max(t.n - first - static_cast<int64_t>(r) * kT * kPer, int64_t{0}), int64_t{8}));
+    };
+    // whole warps leave together: a block of the 8-bit states is one warp's
+    const auto there = [&](int r) {
+        return r < kRounds<B8> && warp_first + static_cast<int64_t>(r) * kT * kPer < t.n;
+    };
+    if (!there(0)) return;
+    in.load(t, first, left_at(0));
+#pragma unroll
+    for (int r = 0; r < kRounds<B8>; ++r) {
+        const int64_t at = first + static_cast<int64_t>(r) * kT * kPer;
+        const int left = left_at(r);
+        const bool more = there(r + 1);
+        if (more) next.load(t, at + kT * kPer, left_at(r + 1));
+        F2 p[4], g[4], m[4], v[4], root[4];
+        in.g.get(g);
+        in.p.get(p);
+        if (B8) {
+            decode(in.mc, in.ms, m);
+            decode(in.vc, in.vs, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = mul(v[i], v[i]);
+        } else {
+            in.m.get(m);
+            in.v.get(v);
+        }
+        const F2 b1 = f2(s.b1, s.b1), b1c = f2(s.b1c, s.b1c), b2 = f2(s.b2, s.b2), b2c = f2(s.b2c, s.b2c);
+        // sums as x 1 + y: a packed product and a packed sum would be contracted into one rounding
+        const F2 one = f2(s.one, s.one);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            g[i] = mul(g[i], f2(gs, gs));
+            m[i] = fma2(mul(m[i], b1), one, mul(g[i], b1c));
+            v[i] = fma2(mul(v[i], b2), one, mul(mul(g[i], g[i]), b2c));
+            const float2 q = parts(v[i]);
+            root[i] = f2(__fsqrt_rn(q.x), __fsqrt_rn(q.y));
+            const float2 d = parts(fma2(root[i], f2(s.inv_c2, s.inv_c2), f2(s.eps, s.eps)));
+            p[i] = fma2(mul(m[i], f2(s.rate, s.rate)), f2(rcp(d.x), rcp(d.y)), mul(p[i], f2(s.keep, s.keep)));
+        }
+        if (MA) store8<true>(t.master, at, left, p);
+        store8<PF>(t.param, at, left, p);
+        if (B8) {
+            const int64_t block = at / kAdamBlock;
+            store_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + block, at, left, m);
+            store_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + block, at, left, root);
+        } else {
+            store8<true>(t.m, at, left, m);
+            store8<true>(t.v, at, left, v);
+        }
+        if (!more) break;
+        in = next;
+    }
+}
+
+// kB8: the launch's tensors have 8-bit states, else fp32 ones.  Measured on every adapter of a 32-layer model at rank
+// 16 (8-bit) and on 207 M values with an fp32 copy: four CTAs an SM and chunks of 4096 against three and 2048 take
+// 95 against 109 us with 8-bit states (bound by issue slots), 857 against 828 us with fp32 ones (bound by HBM, 7.0 TB/s).
+template <bool kB8, int N>
+__global__ void __launch_bounds__(kT, kB8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamStep s, const __grid_constant__ AdamTensors<N> table) {
     pdl_wait();
     pdl_trigger();
     int lo = 0, hi = s.n;   // the last tensor whose first chunk is not after this one
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (table.t[mid].chunk0 <= static_cast<int>(blockIdx.x)) lo = mid;
+        if (table.chunk0[mid] <= static_cast<int>(blockIdx.x)) lo = mid;
         else hi = mid;
     }
-    const AdamTensor t = table.t[lo];
-    const int64_t first = static_cast<int64_t>(static_cast<int>(blockIdx.x) - t.chunk0) * kAdamChunk + threadIdx.x * kPer;
-    const bool pf32 = t.flags & kAdamParamF32, gf32 = t.flags & kAdamGradF32, bits8 = t.flags & kAdam8Bit;
+    const AdamTensor& t = table.t[lo];
+    const int64_t first = static_cast<int64_t>(static_cast<int>(blockIdx.x) - table.chunk0[lo]) *
+                              (kB8 ? kAdamChunk8 : kAdamChunk32) + threadIdx.x * kPer;
     const float gs = s.grad_scale ? *s.grad_scale : 1.f;
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-        const int64_t at = first + static_cast<int64_t>(r) * kT * kPer;
-        // whole warps leave together: a block of the 8-bit states is one warp's
-        if (at - static_cast<int64_t>(lane_id()) * kPer >= t.n) break;
-        const int left = static_cast<int>(min(max(t.n - at, int64_t{0}), int64_t{8}));
-        float p[8], g[8], m[8], v[8], root[8];
-        load8(t.grad, at, left, gf32, g);
-        if (t.master) load8(t.master, at, left, true, p);
-        else load8(t.param, at, left, pf32, p);
-        const int64_t block = at / kAdamBlock;
-        if (bits8) {
-            load_codes(static_cast<const uint8_t*>(t.m), at, left, t.m_scale[block], m);
-            load_codes(static_cast<const uint8_t*>(t.v), at, left, t.v_scale[block], v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-        } else {
-            load8(t.m, at, left, true, m);
-            load8(t.v, at, left, true, v);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (s.grad_scale) g[i] = __fmul_rn(g[i], gs);
-            m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(g[i], s.b1c));
-            v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(g[i], g[i]), s.b2c));
-            root[i] = __fsqrt_rn(v[i]);
-            const float d = fmaf(root[i], s.inv_c2, s.eps);
-            p[i] = p[i] * s.keep - __fdividef(s.rate * m[i], d);
-        }
-        if (t.master) store8(t.master, at, left, true, p);
-        store8(t.param, at, left, pf32, p);
-        if (bits8) {
-            store_codes<false>(static_cast<uint8_t*>(t.m), t.m_scale + block, at, left, m);
-            store_codes<true>(static_cast<uint8_t*>(t.v), t.v_scale + block, at, left, root);
-        } else {
-            store8(t.m, at, left, true, m);
-            store8(t.v, at, left, true, v);
-        }
+    const bool gf = t.flags & kAdamGradF32;
+    if (t.flags & kAdamParamF32) gf ? chunk_step<true, true, kB8, false>(s, t, first, gs) : chunk_step<true, false, kB8, false>(s, t, first, gs);
+    else if (t.master) gf ? chunk_step<false, true, kB8, true>(s, t, first, gs) : chunk_step<false, false, kB8, true>(s, t, first, gs);
+    else gf ? chunk_step<false, true, kB8, false>(s, t, first, gs) : chunk_step<false, false, kB8, false>(s, t, first, gs);
+}
+
+template <bool kB8>
+cudaError_t run(const AdamStep& p, const AdamTensors<kAdamTensors>& t, int chunks, cudaStream_t stream) {
+    if (p.n > kAdamFew) return launch_pdl(adamw_kernel<kB8, kAdamTensors>, dim3(chunks), dim3(kT), 0, stream, p, t);
+    AdamTensors<kAdamFew> few;
+    for (int i = 0; i < p.n; ++i) {
+        few.t[i] = t.t[i];
+        few.chunk0[i] = t.chunk0[i];
     }
+    return launch_pdl(adamw_kernel<kB8, kAdamFew>, dim3(chunks), dim3(kT), 0, stream, p, few);
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamStep& p, const AdamTensors<kAdamTensors>& t, int chunks, cudaStream_t stream) {
-    if (p.n <= kAdamFew)
-        return launch_pdl(adamw_kernel<kAdamFew>, dim3(chunks), dim3(kT), 0, stream, p,
-                          reinterpret_cast<const AdamTensors<kAdamFew>&>(t));
-    return launch_pdl(adamw_kernel<kAdamTensors>, dim3(chunks), dim3(kT), 0, stream, p, t);
+cudaError_t launch_adamw(const AdamStep& p, const AdamTensors<kAdamTensors>& t, bool bits8, int chunks, cudaStream_t stream) {
+    return bits8 ? run<true>(p, t, chunks, stream) : run<false>(p, t, chunks, stream);
 }
 
 }  // namespace lora
