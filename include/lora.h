@@ -333,7 +333,8 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
  *    262144, rows up to 262144.  Rows past `vocab` elements (padding up to ld) are neither read nor written.
  *  - Softmax statistics are fp32 relative to each row's maximum, sums over tokens fp64, in a fixed order: results are
  *    bit-identical from call to call.  Logits of -inf (a restricted vocabulary) have probability 0.
- *  - workspace: loss_workspace_size(rows) bytes, 256-byte aligned, scratch whose contents do not matter. */
+ *  - workspace: loss_workspace_size(rows) bytes, 256-byte aligned; its first 256 bytes (the device status word and
+ *    a counter) are zero before the first use and stay so, the rest is scratch whose contents do not matter. */
 enum { LORA_BF16 = 0, LORA_F32 = 1 };
 enum { LORA_MAX_VOCAB = 262144, LORA_MAX_PAIRS = 1024 };
 

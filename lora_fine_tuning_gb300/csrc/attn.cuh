@@ -3,11 +3,9 @@
 
 #include "attn.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace lora {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, each 32-bit column holds two consecutive K elements (bf16).
 __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -74,14 +72,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[M][N]) {
 #pragma unroll
     for (int i = 0; i < M; ++i) tmem_landed(r[i]);
 }
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
 // The sequence that holds work item `item`: the last whose first item is not after it.
 template <int N>

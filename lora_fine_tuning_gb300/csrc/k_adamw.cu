@@ -13,7 +13,8 @@
 // the new states before they are rounded.  The states' arithmetic is one IEEE rounding an operation, in the order
 // written, with no contraction: which code a value gets does not depend on the compiler.
 #include "adamw.h"
-#include "attn.cuh"
+#include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 
 namespace lora {
@@ -28,31 +29,6 @@ static_assert(kPer * 32 == kAdamBlock, "a warp holds one block of the 8-bit stat
 constexpr float kE4m3Max = 448.f;
 constexpr float kSmallest = 0.001953125f;              // 2^-9, e4m3's smallest positive value
 constexpr float kTiny = 7.888609052210118e-31f;        // 2^-100: a block below this is held as zeros
-
-// Two fp32 values in a register pair: one instruction, one IEEE rounding a value.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 parts(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 
 // Eight values of a lane as they lie in memory, bf16 or fp32 (with `left` < 8 the rest is zero).
 template <bool kF32>

@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "plan.h"
+
 namespace lora {
 
 constexpr int kLossMaxPairs = 1024;
@@ -30,8 +32,11 @@ struct PrefParams {
     float* coef;           // workspace, rows: d loss / d logp
     float* loss;           // 1
     float* margin;         // pairs
+    float* pair_loss;      // workspace, pairs
+    uint32_t* ticket;      // workspace, zero between calls
     int32_t n_pairs;
     float beta, smoothing, scale;
+    DevCtl ctl;
 };
 
 struct PrefPair {
@@ -50,6 +55,7 @@ struct PolicyParams {
     float* loss;           // 1
     float lo, hi;          // 1 - clip_low, 1 + clip_high
     float kl, scale;
+    DevCtl ctl;
 };
 
 cudaError_t launch_loss_stats(const PrefParams& p, int sms, cudaStream_t stream);

@@ -31,19 +31,19 @@ lora_status check_logits(const lora_logits* g, LossLogits& in) {
 }
 
 struct LossLayout {
-    size_t row, coef, total;
+    size_t row, coef, pairs, total;
 };
 
 LossLayout loss_layout(int64_t rows) {
     LossLayout L;
-    L.row = 0;
-    L.coef = up256(static_cast<size_t>(rows) * sizeof(LossRow));
-    L.total = L.coef + up256(static_cast<size_t>(rows) * 4);
+    L.row = 256;   // after the device status word and the pairs' ticket
+    L.coef = L.row + up256(static_cast<size_t>(rows) * sizeof(LossRow));
+    L.pairs = L.coef + up256(static_cast<size_t>(rows) * 4);
+    L.total = L.pairs + LORA_MAX_PAIRS * 4;
     return L;
 }
 
 lora_status check_workspace(void* ws, size_t have, size_t need) {
-    if (need == 0) return LORA_OK;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || have < need) return LORA_EWORKSPACE;
     return LORA_OK;
 }
@@ -80,7 +80,7 @@ using namespace lora;
 
 extern "C" {
 
-size_t loss_workspace_size(int64_t rows) { return rows > 0 ? loss_layout(rows).total : 0; }
+size_t loss_workspace_size(int64_t rows) { return rows >= 0 ? loss_layout(rows).total : 0; }
 
 lora_status pref_loss(const lora_logits* logits, const lora_pref_pair* pairs, int32_t n_pairs, const float* ref_logp,
                       float beta, float label_smoothing, float scale, float* loss, float* margins, void* workspace,
@@ -106,10 +106,13 @@ lora_status pref_loss(const lora_logits* logits, const lora_pref_pair* pairs, in
     p.coef = reinterpret_cast<float*>(ws + L.coef);
     p.loss = loss;
     p.margin = margins;
+    p.pair_loss = reinterpret_cast<float*>(ws + L.pairs);
+    p.ticket = reinterpret_cast<uint32_t*>(ws + 128);   // beside the status word
     p.n_pairs = n_pairs;
     p.beta = beta;
     p.smoothing = label_smoothing;
     p.scale = scale;
+    p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
     if (p.in.rows > 0) LORA_CUDA(timed(kLossRows, s, [&] { return launch_loss_stats(p, sms, s); }));
     LORA_CUDA(timed(kLossPairs, s, [&] { return launch_loss_pairs(p, table, s); }));
     if (p.in.rows > 0 && p.in.dz) LORA_CUDA(timed(kLossGrad, s, [&] { return launch_loss_grad(p, s); }));
@@ -135,7 +138,8 @@ lora_status policy_loss(const lora_logits* logits, const float* old_logp, const 
     p.old_logp = old_logp;
     p.adv = advantages;
     p.ref = kl_coef != 0.f ? ref_logp : nullptr;
-    p.row_loss = static_cast<float*>(workspace);
+    p.row_loss = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + loss_layout(p.in.rows).row);
+    p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
     p.loss = loss;
     p.lo = static_cast<float>(1.0 - static_cast<double>(clip_low));
     p.hi = static_cast<float>(1.0 + static_cast<double>(clip_high));

@@ -19,7 +19,7 @@ constexpr int kMaxRank = 128;
 
 // Kernel ids for device status codes (code = id << 8 | call site).
 enum KernelId : int { kKDown = 1, kKGemmFwd = 2, kKGemmBwd = 3, kKDsDb = 4, kKDa = 5, kKDebug = 6,
-                      kKAttnFwd = 7, kKAttnDq = 8, kKAttnDkDv = 9 };
+                      kKAttnFwd = 7, kKAttnDq = 8, kKAttnDkDv = 9, kKLoss = 10 };
 
 struct AdapterDev {
     int32_t rank;      // r_i
