@@ -20,6 +20,21 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// True in one lane of a converged warp, the same one every time.  MMAs issued under it take a few cycles each; under
+// `lane == 0`, where the assembler cannot see that one thread of a uniform branch runs, each took about 90 (traced in the
+// forward kernel) and its operands went wrong where a run-time branch stood between two of them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xFFFFFFFF;\n"
+        "selp.b32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // One 128 x 128 product over DP features, both operands K-major 128-row tiles of 64-feature boxes.  Every K step is
 // issued, past the head's width too (the tiles hold zeros there): no branch stands between the steps.
 template <int DP>

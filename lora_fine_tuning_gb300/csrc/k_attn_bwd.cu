@@ -196,7 +196,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
             const uint32_t idesc_q = make_idesc_bf16(128, sh.d16, false, true);
             const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
@@ -238,6 +238,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             umma_commit(drain);
             mbar_wait_drain(drain, 0, p.ctl.wait_ns);
         }
+        __syncwarp();
     } else {
         const int g = warp >> 2;                     // columns [64 g, 64 g + 64) of every tile
         const int quad = warp & 3;
@@ -479,7 +480,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
             const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
             const uint64_t kd = make_smem_desc(smem_u32(sK), 16, 1024, kSw128);
@@ -530,6 +531,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             umma_commit(drain);
             mbar_wait_drain(drain, 0, p.ctl.wait_ns);
         }
+        __syncwarp();
     } else {
         const int g = warp >> 2;
         const int quad = warp & 3;

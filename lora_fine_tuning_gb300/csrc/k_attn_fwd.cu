@@ -17,7 +17,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kStages = 4;
+constexpr int kStages = 5;        // of K or V tiles, which alternate
 constexpr float kRescale = 8.f;   // log2 of the growth of a row's maximum that rescales O
 
 template <int DP>
@@ -40,8 +40,8 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
     uint64_t* kv_full = q_full + 2;       // kStages
     uint64_t* kv_empty = kv_full + kStages;
     uint64_t* s_full = kv_empty + kStages;   // 2
-    uint64_t* p_full = s_full + 2;           // 2
-    uint64_t* o_full = p_full + 2;           // 2
+    uint64_t* p_full = s_full + 2;           // 4: the halves of each tile's P
+    uint64_t* o_full = p_full + 4;           // 2
     uint64_t* v_fixed = o_full + 2;          // 1: the last V tile's rows past the sequence are zero
     uint64_t* drain = v_fixed + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -53,7 +53,8 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+            mbar_init(&p_full[2 * i], 128);
+            mbar_init(&p_full[2 * i + 1], 128);
             mbar_init(&o_full[i], 1);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -150,55 +151,70 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                 mbar_wait_drain(&kv_full[t % kStages], (t / kStages) & 1, p.ctl.wait_ns);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
-            const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
-            const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
-            const uint64_t kd = make_smem_desc(smem_u32(sKV), 16, 1024, kSw128);       // K: rows x features
-            const uint64_t vd = make_smem_desc(smem_u32(sKV), 16384, 1024, kSw128);    // V: features contiguous
-            bool ok = true;
-            // turn j: for each query tile the product of P(j - 1) with V(j - 1), then the scores with K(j).  S(j)
-            // overwrites P(j - 1) in TMEM: the MMAs execute in the order in which they are issued.
-            for (int j = 0; j <= nkm && nkm > 0; ++j) {
-                const int tk = 2 * j, tv = 2 * j - 1;
-                const uint64_t ks_ = kd + static_cast<uint64_t>(tk % kStages) * (C::kTileBytes >> 4);
-                const uint64_t vs_ = vd + static_cast<uint64_t>((tv + kStages) % kStages) * (C::kTileBytes >> 4);
-                if (j > 0) {
-                    if (!mbar_wait(&kv_full[tv % kStages], (tv / kStages) & 1, w, 3)) { ok = false; break; }
-                    if (tail && j == nkm && !mbar_wait(v_fixed, 0, w, 4)) { ok = false; break; }
-                    tc_fence_after();
-                }
-                if (j < nkm) {
-                    if (!mbar_wait(&kv_full[tk % kStages], (tk / kStages) & 1, w, 5)) { ok = false; break; }
-                    tc_fence_after();
-                }
+        // the whole warp waits; one lane issues (elect_one)
+        const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
+        const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
+        const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
+        const uint64_t kd = make_smem_desc(smem_u32(sKV), 16, 1024, kSw128);       // K: rows x features
+        const uint64_t vd = make_smem_desc(smem_u32(sKV), 16384, 1024, kSw128);    // V: features contiguous
+        bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, site));
+            tc_fence_after();
+            return ok;
+        };
+        // turn j: for each query tile the product of P(j - 1) with V(j - 1), then the scores with K(j).  S(j)
+        // overwrites P(j - 1) in TMEM: the MMAs execute in the order in which they are issued.
+        for (int j = 0; j <= nkm && nkm > 0; ++j) {
+            const int tk = 2 * j, tv = 2 * j - 1;
+            const uint64_t ks_ = kd + static_cast<uint64_t>(tk % kStages) * (C::kTileBytes >> 4);
+            const uint64_t vs_ = vd + static_cast<uint64_t>((tv + kStages) % kStages) * (C::kTileBytes >> 4);
+            if (j > 0) {
+                if (!wait(&kv_full[tv % kStages], (tv / kStages) & 1, 3)) break;
+                if (tail && j == nkm && !wait(v_fixed, 0, 4)) break;
+            }
+            if (j < nkm && !wait(&kv_full[tk % kStages], (tk / kStages) & 1, 5)) break;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (j > 0 && j <= nk[i]) {
-                        if (!mbar_wait(&p_full[i], (j - 1) & 1, w, 6)) { ok = false; break; }
-                        tc_fence_after();
+            for (int i = 0; i < 2; ++i) {
+                if (j > 0 && j <= nk[i]) {
+                    if (!wait(&p_full[2 * i], (j - 1) & 1, 6)) break;
+                    if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
+                        for (int ks = 0; ks < 4; ++ks)
                             umma_bf16_ta(tmem + 256 + i * DP, tmem + i * 128 + ks * 8, vs_ + ks * 128u, idesc_o,
                                          (j != 1 || ks != 0) ? 1u : 0u);
+                    }
+                    __syncwarp();
+                    if (!wait(&p_full[2 * i + 1], (j - 1) & 1, 8)) break;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 4; ks < 8; ++ks)
+                            umma_bf16_ta(tmem + 256 + i * DP, tmem + i * 128 + ks * 8, vs_ + ks * 128u, idesc_o, 1u);
                         if (j == nk[i]) umma_commit(&o_full[i]);
                     }
-                    if (j < nk[i]) {
-                        if (j == 0) {
-                            if (!mbar_wait(&q_full[i], 0, w, 7)) { ok = false; break; }
-                            tc_fence_after();
-                        }
+                    __syncwarp();
+                }
+                if (i == 1 && j > 0) {
+                    if (elect_one()) umma_commit(&kv_empty[tv % kStages]);
+                    __syncwarp();
+                }
+                if (j < nk[i]) {
+                    if (j == 0 && !wait(&q_full[i], 0, 7)) break;
+                    if (elect_one()) {
                         mma_rows<DP>(tmem + i * 128, qd + i * (C::kTileBytes >> 4), ks_, idesc_s);
                         umma_commit(&s_full[i]);
                     }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                if (j > 0) umma_commit(&kv_empty[tv % kStages]);
-                if (j < nkm) umma_commit(&kv_empty[tk % kStages]);
             }
-            umma_commit(drain);
-            mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+            if (!ok) break;
+            if (j < nkm && elect_one()) umma_commit(&kv_empty[tk % kStages]);
+            __syncwarp();
         }
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+        __syncwarp();
     } else {
         const int i = warp >> 2;                     // query tile
         const int quad = warp & 3;
@@ -232,12 +248,15 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                     for (int e = 0; e < 32; ++e)
                         if (c * 32 + e > lim) v[c][e] = 0xff800000u;
             }
-            float top = neg_inf();
+            float tops[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+                tops[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[c][e]));
-            top *= sl;
+                for (int e = 2; e < 32; e += 2)
+                    tops[c] = max3(tops[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+            }
+            const float top = sl * fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
             if (j == 0) {
                 m = top;
             } else {
@@ -261,23 +280,29 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                 }
             }
             const float ms = m == neg_inf() ? 0.f : m;   // a row without a visible key yet: exp2(-inf) = 0 throughout
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const F2 sl2 = f2(sl, sl), ms2 = f2(-ms, -ms);
+            F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+            // in halves of 64 keys: the product with V starts on the first while the second is computed
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[16];
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float a = ex2(fmaf(__uint_as_float(v[c][2 * e]), sl, -ms));
-                    const float b = ex2(fmaf(__uint_as_float(v[c][2 * e + 1]), sl, -ms));
-                    sum[e & 3] += a + b;
-                    o[e] = pack_bf16x2(a, b);
+                for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 q = parts(fma2(f2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sl2, ms2));
+                        const float x = ex2(q.x), y = ex2(q.y);
+                        sum[e & 1] = add2(sum[e & 1], f2(x, y));
+                        o[e] = pack_bf16x2(x, y);
+                    }
+                    tmem_st16(ts + c * 16, o);
                 }
-                tmem_st16(ts + c * 16, o);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_full[2 * i + h]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full[i]);
+            const float2 q = parts(add2(sum[0], sum[1]));
+            l += q.x + q.y;
         }
         if (ok && n > 0) {
             ok = mbar_wait(&o_full[i], 0, w, 10);
