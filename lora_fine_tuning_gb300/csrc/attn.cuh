@@ -112,14 +112,76 @@ __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int boxes, int fro
     fence_proxy_async_smem();
 }
 
-// 16 fp32 values -> 8 packed bf16 pairs, times f, to 16 consecutive output elements (8 at a time, features past d
-// are not written; d % 8 == 0).
-__device__ __forceinline__ void store_out16(uint16_t* out, const uint32_t (&v)[16], float f, int c0, int d) {
-    uint32_t w[8];
+// Rows of an output tile that a warp holds in TMEM (row quad * 32 + lane at `taddr`, `have` false: zeros) times f, in bf16,
+// to global memory: tile row r is token r >> hp_log2 of `out`, head r & (hp - 1); rows from `rows` on are not written.
+// They pass through shared memory (`stage`: boxes of 128 rows x 64 features, 16-byte chunks swizzled by the row), so that
+// eight lanes store 128 bytes of a row together.  A row a lane made every store touch 32 lines: 5100 cycles a tile.
+__device__ __forceinline__ void store_tile(uint16_t* out, int64_t row_stride, int64_t head_stride, int hp_log2, int rows,
+                                           int d, int d16, uint32_t stage, uint32_t taddr, int quad, bool have, float f) {
+    const int lane = lane_id();
+    const F2 ff = f2(f, f);
+    if (rows <= quad * 32) return;
+#pragma unroll 1
+    for (int c = 0; c < d16; c += 64) {
+        const uint32_t box = stage + (c >> 6) * 16384 + quad * 4096;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * f, __uint_as_float(v[2 * i + 1]) * f);
-    if (c0 < d) stg128(out + c0, make_uint4(w[0], w[1], w[2], w[3]));
-    if (c0 + 8 < d) stg128(out + c0 + 8, make_uint4(w[4], w[5], w[6], w[7]));
+        for (int x = 0; x < 64; x += 32) {
+            uint32_t o[32];
+            if (have) {
+                tmem_ld32(taddr + c + x, o);
+                tmem_ld_wait(o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 v = parts(mul(f2(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1])), ff));
+                    q[k] = pack_bf16x2(v.x, v.y);
+                }
+                sts128(box + lane * 128 + ((((x + e) >> 3) ^ (lane & 7)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+            }
+        }
+        __syncwarp();
+        if (c + (lane & 7) * 8 < d) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = k * 4 + (lane >> 3), tr = quad * 32 + row;
+                if (tr < rows)
+                    stg128(out + static_cast<int64_t>(tr >> hp_log2) * row_stride +
+                               static_cast<int64_t>(tr & ((1 << hp_log2) - 1)) * head_stride + c + (lane & 7) * 8,
+                           lds128(box + row * 128 + (((lane & 7) ^ (row & 7)) << 4)));
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Unused rows that an item fills: every tiles-th row of the gap after its sequence (from `after`), its share (item
+// `turn` of `turns`) of the rows before the first and after the last sequence; heads [head0, head0 + hp) of a and, if
+// there, b, and lse.  By 256 threads, 16 a row and head.
+static __device__ __noinline__ void fill_rows(const AttnMat& a, const AttnMat* b, float* lse, const AttnShape& sh, int head0,
+                                              int hp_log2, int64_t after, int gap, int tile, int tiles, int turn, int turns,
+                                              int thread) {
+    const int hp = 1 << hp_log2, x = (thread & 15) * 8;
+    const int h = (thread >> 4) & (hp - 1);
+    const int per = 16 >> min(hp_log2, 4), mine = (thread >> 4) >> min(hp_log2, 4);   // rows at a time
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const auto clear = [&](int64_t row) {
+        for (int g = head0 + h; g < head0 + hp; g += 16) {
+            if (x < sh.d) {
+                stg128(a.p + row * a.row + g * a.head + x, zero);
+                if (b) stg128(b->p + row * b->row + g * b->head + x, zero);
+            }
+            if (lse && x == 0) lse[row * sh.hq + g] = neg_inf();
+        }
+    };
+    for (int r = tile * per + mine; r < gap; r += tiles * per) clear(after + r);
+    for (int r = turn * per + mine; r < sh.lead + sh.trail; r += turns * per)
+        clear(r < sh.lead ? r : sh.trail0 + r - sh.lead);
 }
 
 }  // namespace lora

@@ -18,6 +18,7 @@ struct AttnSeq {
     int32_t q0, k0;      // first row of the queries, of the keys
     int32_t ql, kl;      // rows
     int32_t item0;
+    int32_t gap;         // unused rows of the output after this sequence that its items fill
 };
 
 // The table travels as a kernel parameter (no device table, no copy); a small batch passes a small one.
@@ -43,6 +44,8 @@ struct AttnShape {
     int32_t hp, hp_log2;     // query heads in a tile
     int32_t packs;           // hq / hp: packs of the whole layer
     int32_t d, d16;          // head width, rounded up to 16
+    int32_t lead;            // unused rows [0, lead) and [trail0, trail0 + trail) of the output, filled by all items
+    int32_t trail0, trail;
     float scale;             // softmax scale
     float scale_log2;        // scale * log2(e)
 };

@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "attn.h"
 #include "host.h"
@@ -53,7 +54,7 @@ lora_status check_seqs(const lora_attn_seq* seqs, int32_t n, int64_t q_rows, int
         k_end = s.k_start + s.k_rows;
         if (s.q_rows > 0 || s.k_rows > 0)
             c.order.s[c.n++] = AttnSeq{static_cast<int32_t>(s.q_start), static_cast<int32_t>(s.k_start),
-                                       static_cast<int32_t>(s.q_rows), static_cast<int32_t>(s.k_rows), 0};
+                                       static_cast<int32_t>(s.q_rows), static_cast<int32_t>(s.k_rows), 0, 0};
     }
     gap(c.q_gaps, c.nq_gaps, q_end, q_rows);
     gap(c.k_gaps, c.nk_gaps, k_end, k_rows);
@@ -112,6 +113,45 @@ void order_by_keys(Prepared& c) {
 
 AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
 
+// Unused rows that an item of the sequence before them is asked to fill at most; a batch with longer gaps between its
+// sequences gets a kernel of its own for them.
+constexpr int kMaxItemGap = 4096;
+
+// Gives every unused row of an output with `rows` rows to the items of c (numbered already): the rows after a sequence
+// to its own, those before the first and after the last to all.  False if the rows need a launch of their own.  `first`
+// and `len` read a sequence's place.
+template <class First, class Len>
+bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, First first, Len len) {
+    const auto none = [&c] {
+        c.sh.lead = c.sh.trail0 = c.sh.trail = 0;
+        for (int i = 0; i < c.n; ++i) c.order.s[i].gap = 0;
+        return false;
+    };
+    none();
+    if (n_gaps == 0) return true;
+    if (c.sh.items == 0) return false;
+    thread_local std::pair<int32_t, int32_t> ends[kAttnMaxSeqs];   // end row, place in the table
+    int m = 0;
+    for (int i = 0; i < c.n; ++i)
+        if (len(c.order.s[i]) > 0) ends[m++] = {first(c.order.s[i]) + len(c.order.s[i]), i};
+    std::sort(ends, ends + m);
+    for (int g = 0; g < n_gaps; ++g) {
+        const int32_t from = gaps.from[g], to = gaps.to[g];
+        if (from == 0) {
+            c.sh.lead = to;
+        } else if (to == rows) {
+            c.sh.trail0 = from;
+            c.sh.trail = to - from;
+        } else {
+            if (to - from > kMaxItemGap) return none();
+            const auto e = std::lower_bound(ends, ends + m, std::make_pair(from, int32_t{-1}));
+            if (e == ends + m || e->first != from) return none();
+            c.order.s[e->second].gap = to - from;
+        }
+    }
+    return true;
+}
+
 lora_status fill(const AttnGaps& gaps, int n, AttnMat a, AttnMat b, int heads, int d, float* lse, cudaStream_t s) {
     if (n == 0) return LORA_OK;
     AttnFillParams f{a, b, heads, d, lse, n};
@@ -150,10 +190,12 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     int sms = 0;
     if ((st = device_setup(&sms))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
     order_by_keys(c);
     const int tokens = kAttnTile / c.sh.hp;
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, 2 * tokens); }, c.sh.packs))) return st;
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
+        if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
+    }
     if (c.sh.items == 0) return LORA_OK;
     thread_local AttnFwdParams p;
     std::memset(&p, 0, sizeof(p));
@@ -197,10 +239,11 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     int sms = 0;
     if ((st = device_setup(&sms))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = fill(c.q_gaps, c.nq_gaps, mat(dQ, a.d_q), AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
-    AttnMat mk = mat(dK, a.d_k), mv = mat(dV, a.d_v);
-    if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
-    if (c.n == 0) return LORA_OK;
+    const AttnMat mk = mat(dK, a.d_k), mv = mat(dV, a.d_v);
+    if (c.n == 0) {
+        if ((st = fill(c.q_gaps, c.nq_gaps, mat(dQ, a.d_q), AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
+        return fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s);
+    }
     order_by_keys(c);
     thread_local AttnBwdParams p;
     std::memset(&p, 0, sizeof(p));
@@ -224,9 +267,15 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
         LORA_CUDA(timed(kAttnDelta, s, [&] { return launch_attn_delta(d, s); }));
     }
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }, c.sh.packs))) return st;
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
+        if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
+    }
     p.sh = c.sh;
     if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, s); }));
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }, c.sh.hkv))) return st;
+    if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, [](const AttnSeq& q) { return q.k0; }, [](const AttnSeq& q) { return q.kl; })) {
+        if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
+    }
     p.sh = c.sh;
     if (c.sh.items > 0) LORA_CUDA(timed(kAttnDkDv, s, [&] { return launch_attn_dkdv(p, c.order, s); }));
     return LORA_OK;

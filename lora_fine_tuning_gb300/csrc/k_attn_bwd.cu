@@ -67,33 +67,35 @@ template <int DP>
 struct CfgQ {
     static constexpr int kBoxes = DP / 64;
     static constexpr uint32_t kTileBytes = kBoxes * 16384u;
-    static constexpr int kStages = 2;    // of K, and of V
-    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * static_cast<size_t>(kTileBytes) + 256;
+    // a K tile is held from its scores to its gradients, a V tile for one product
+    static constexpr int kStagesK = 3, kStagesV = 2;
+    static constexpr size_t kSmem = 1024 + (2 + kStagesK + kStagesV) * static_cast<size_t>(kTileBytes) + 256;
 };
 
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
     using C = CfgQ<DP>;
-    constexpr int S = C::kStages;
+    constexpr int SK = C::kStagesK, SV = C::kStagesV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_1024(smem_raw);
     uint8_t* sQ = smem;
     uint8_t* sDO = sQ + C::kTileBytes;
     uint8_t* sK = sDO + C::kTileBytes;
-    uint8_t* sV = sK + S * C::kTileBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + S * C::kTileBytes);
+    uint8_t* sV = sK + SK * C::kTileBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + SV * C::kTileBytes);
     uint64_t* q_full = bars;               // Q and dO
-    uint64_t* k_full = q_full + 1;         // S each
-    uint64_t* k_empty = k_full + S;
-    uint64_t* v_full = k_empty + S;
-    uint64_t* v_empty = v_full + S;
-    uint64_t* s_full = v_empty + S;        // 2 score buffers
+    uint64_t* k_full = q_full + 1;         // SK each
+    uint64_t* k_empty = k_full + SK;
+    uint64_t* v_full = k_empty + SK;       // SV each
+    uint64_t* v_empty = v_full + SV;
+    uint64_t* s_full = v_empty + SV;       // 2 score buffers
     uint64_t* dp_full = s_full + 2;
     uint64_t* ds_full = dp_full + 1;
     uint64_t* dq_full = ds_full + 1;
     uint64_t* k_fixed = dq_full + 1;
-    uint64_t* drain = k_fixed + 1;
+    uint64_t* dp_read = k_fixed + 1;
+    uint64_t* drain = dp_read + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     __shared__ int abort_flag;
 
@@ -101,9 +103,11 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < SK; ++s) {
             mbar_init(&k_full[s], 1);
             mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < SV; ++s) {
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
         }
@@ -113,6 +117,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         mbar_init(ds_full, 256);
         mbar_init(dq_full, 1);
         mbar_init(k_fixed, 1);
+        mbar_init(dp_read, 256);
         mbar_init(drain, 1);
         abort_flag = 0;
         fence_barrier_init();
@@ -154,23 +159,22 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             }
         }
         for (int j = 0; j < n; ++j) {
-            const int s = j % S;
-            const uint32_t ph = (j / S) & 1;
+            const int s = j % SK, v = j % SV;
             if (lane == 0) {
-                ok = mbar_wait(&k_empty[s], ph ^ 1u, w, 1);
+                ok = mbar_wait(&k_empty[s], ((j / SK) & 1) ^ 1u, w, 1);
                 if (ok) {
                     mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
                     for (int b = 0; b < C::kBoxes; ++b)
                         tma_load_3d(sK + s * C::kTileBytes + b * 16384, &p.mapK, &k_full[s], b * 64, kvh,
                                     sq.k0 + j * kAttnTile);
-                    ok = mbar_wait(&v_empty[s], ph ^ 1u, w, 2);
+                    ok = mbar_wait(&v_empty[v], ((j / SV) & 1) ^ 1u, w, 2);
                     if (ok) {
-                        mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
+                        mbar_arrive_expect_tx(&v_full[v], C::kTileBytes);
                         for (int b = 0; b < C::kBoxes; ++b)
-                            tma_load_3d(sV + s * C::kTileBytes + b * 16384, &p.mapV, &v_full[s], b * 64, kvh,
+                            tma_load_3d(sV + v * C::kTileBytes + b * 16384, &p.mapV, &v_full[v], b * 64, kvh,
                                         sq.k0 + j * kAttnTile);
                     } else {
-                        mbar_wait_drain(&k_full[s], ph, p.ctl.wait_ns);
+                        mbar_wait_drain(&k_full[s], (j / SK) & 1, p.ctl.wait_ns);
                     }
                 }
             }
@@ -179,8 +183,8 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             ++issued;
         }
         if (ok && tail && n > 0) {
-            const int s = (n - 1) % S;
-            ok = mbar_wait(&k_full[s], ((n - 1) / S) & 1, w, 3);
+            const int s = (n - 1) % SK;
+            ok = mbar_wait(&k_full[s], ((n - 1) / SK) & 1, w, 3);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) {
                 zero_tile_rows(sK + s * C::kTileBytes, C::kBoxes, sq.kl - (n - 1) * kAttnTile);
@@ -190,10 +194,8 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         }
         if (!ok && lane == 0) {
             if (n > 0) mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
-            for (int j = max(0, issued - S); j < issued; ++j) {
-                mbar_wait_drain(&k_full[j % S], (j / S) & 1, p.ctl.wait_ns);
-                mbar_wait_drain(&v_full[j % S], (j / S) & 1, p.ctl.wait_ns);
-            }
+            for (int j = max(0, issued - SK); j < issued; ++j) mbar_wait_drain(&k_full[j % SK], (j / SK) & 1, p.ctl.wait_ns);
+            for (int j = max(0, issued - SV); j < issued; ++j) mbar_wait_drain(&v_full[j % SV], (j / SV) & 1, p.ctl.wait_ns);
         }
     } else if (warp == 9) {
         if (elect_one()) {
@@ -206,32 +208,31 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             const uint64_t vd = make_smem_desc(smem_u32(sV), 16, 1024, kSw128);
             bool ok = true;
             if (n > 0) ok = mbar_wait(q_full, 0, w, 4);
-            // turn j: S(j) (its own buffer), dQ += dS(j - 1) K(j - 1), dP(j)
+            // turn j: S(j) (its own buffer), dP(j) as soon as the score warps hold dP(j - 1) in registers, then
+            // dQ += dS(j - 1) K(j - 1): dP(j) is formed while they work on dS(j - 1)
             for (int j = 0; j <= n && n > 0 && ok; ++j) {
-                const uint64_t cur = static_cast<uint64_t>(j % S) * (C::kTileBytes >> 4);
-                const uint64_t prev = static_cast<uint64_t>((j + S - 1) % S) * (C::kTileBytes >> 4);
                 if (j < n) {
-                    if (!mbar_wait(&k_full[j % S], (j / S) & 1, w, 5)) { ok = false; break; }
+                    if (!mbar_wait(&k_full[j % SK], (j / SK) & 1, w, 5)) { ok = false; break; }
                     if (tail && j == n - 1 && !mbar_wait(k_fixed, 0, w, 6)) { ok = false; break; }
                     tc_fence_after();
-                    mma_rows<DP>(t_s + (j & 1) * 128, qd, kd + cur, idesc_s);
+                    mma_rows<DP>(t_s + (j & 1) * 128, qd, kd + static_cast<uint64_t>(j % SK) * (C::kTileBytes >> 4), idesc_s);
                     umma_commit(&s_full[j & 1]);
+                    if (!mbar_wait(&v_full[j % SV], (j / SV) & 1, w, 7)) { ok = false; break; }
+                    if (j > 0 && !mbar_wait(dp_read, (j - 1) & 1, w, 12)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP>(t_dp, dod, vd + static_cast<uint64_t>(j % SV) * (C::kTileBytes >> 4), idesc_s);
+                    umma_commit(dp_full);
+                    umma_commit(&v_empty[j % SV]);
                 }
                 if (j > 0) {
                     if (!mbar_wait(ds_full, (j - 1) & 1, w, 8)) { ok = false; break; }
                     tc_fence_after();
+                    const uint64_t b = kmn + static_cast<uint64_t>((j - 1) % SK) * (C::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_ta(t_dq, t_s + ((j - 1) & 1) * 128 + a_col(ks), kmn + prev + ks * 128u, idesc_q,
+                        umma_bf16_ta(t_dq, t_s + ((j - 1) & 1) * 128 + a_col(ks), b + ks * 128u, idesc_q,
                                      (j != 1 || ks != 0) ? 1u : 0u);
-                    umma_commit(&k_empty[(j - 1) % S]);
-                }
-                if (j < n) {
-                    if (!mbar_wait(&v_full[j % S], (j / S) & 1, w, 7)) { ok = false; break; }
-                    tc_fence_after();
-                    mma_rows<DP>(t_dp, dod, vd + cur, idesc_s);
-                    umma_commit(dp_full);
-                    umma_commit(&v_empty[j % S]);
+                    umma_commit(&k_empty[(j - 1) % SK]);
                 }
             }
             if (ok) umma_commit(dq_full);
@@ -249,6 +250,10 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         const int limit = tok + off;
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         const float sl = sh.scale_log2;
+        // under the first loads
+        if (sq.gap + sh.lead + sh.trail > 0)
+            fill_rows(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
+                      local / sh.packs, tiles, blockIdx.x / sh.packs, sh.items / sh.packs, threadIdx.x);
         float lse2 = 0.f, delta = 0.f;
         if (row_ok) {
             const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
@@ -275,6 +280,8 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             if (!ok) break;
             tc_fence_after();
             ld64(t_dp + lanes + g * 64, x);
+            tc_fence_before();
+            mbar_arrive(dp_read);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -306,20 +313,10 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             tc_fence_after();
         }
         if (ok) {
-            uint16_t* out = p.dQ.p + (static_cast<int64_t>(sq.q0) + tok) * p.dQ.row + static_cast<int64_t>(head) * p.dQ.head;
-            // group g writes every second 16 features
-#pragma unroll 1
-            for (int c = g * 16; c < sh.d16; c += 32) {
-                uint32_t o[16];
-                if (n > 0) {
-                    tmem_ld16(t_dq + lanes + c, o);
-                    tmem_ld_wait(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
-                }
-                if (row_ok) store_out16(out, o, sh.scale, c, sh.d);
-            }
+            // group g features [64 g, 64 g + 64), through Q's shared memory: all products are done
+            store_tile(p.dQ.p + (static_cast<int64_t>(sq.q0) + tok0) * p.dQ.row + static_cast<int64_t>(head0) * p.dQ.head +
+                               g * 64, p.dQ.row, p.dQ.head, sh.hp_log2, (sq.ql - tok0) << sh.hp_log2, sh.d - g * 64,
+                           min(max(sh.d16 - g * 64, 0), 64), smem_u32(sQ) + g * 16384, t_dq + lanes + g * 64, quad, n > 0, sh.scale);
         }
     }
 
@@ -339,8 +336,9 @@ template <int DP>
 struct CfgKV {
     static constexpr int kBoxes = DP / 64;
     static constexpr uint32_t kTileBytes = kBoxes * 16384u;
-    static constexpr int kStages = 2;    // of Q, and of dO
-    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * static_cast<size_t>(kTileBytes) + 2 * 2 * 512 + 256;
+    // a Q tile is held from its scores to dK, a dO tile from dP to dV
+    static constexpr int kStagesQ = 3, kStagesO = 2;
+    static constexpr size_t kSmem = (2 + kStagesQ + kStagesO) * static_cast<size_t>(kTileBytes) + 2 * 2 * 512 + 256;
 };
 
 // Barrier among the 256 threads of the score warps.
@@ -350,42 +348,51 @@ template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
     using C = CfgKV<DP>;
-    constexpr int S = C::kStages;
+    constexpr int SQ = C::kStagesQ, SO = C::kStagesO;
+    // no other shared memory: the dynamic part starts on a swizzle atom, and there is no room to move it
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align_1024(smem_raw);
+    uint8_t* smem = smem_raw;
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0 && p.ctl.status) atomicCAS(p.ctl.status, 0, (kKAttnDkDv << 8) | 0xFF);
+        return;
+    }
     uint8_t* sK = smem;
     uint8_t* sV = sK + C::kTileBytes;
     uint8_t* sQ = sV + C::kTileBytes;
-    uint8_t* sDO = sQ + S * C::kTileBytes;
-    float* sStat = reinterpret_cast<float*>(sDO + S * C::kTileBytes);   // [2][lse2 128, delta 128]
+    uint8_t* sDO = sQ + SQ * C::kTileBytes;
+    float* sStat = reinterpret_cast<float*>(sDO + SO * C::kTileBytes);   // [2][lse2 128, delta 128]
     uint64_t* bars = reinterpret_cast<uint64_t*>(sStat + 2 * 256);
     uint64_t* k_full = bars;               // K
     uint64_t* v_full = k_full + 1;         // V
-    uint64_t* q_full = v_full + 1;         // S each
-    uint64_t* q_empty = q_full + S;
-    uint64_t* do_full = q_empty + S;
-    uint64_t* do_empty = do_full + S;
-    uint64_t* s_full = do_empty + S;
+    uint64_t* q_full = v_full + 1;         // SQ each
+    uint64_t* q_empty = q_full + SQ;
+    uint64_t* q_fixed = q_empty + SQ;      // Q rows past the sequence are zero
+    uint64_t* do_full = q_fixed + SQ;      // SO each
+    uint64_t* do_empty = do_full + SO;
+    uint64_t* do_fixed = do_empty + SO;
+    uint64_t* s_full = do_fixed + SO;
     uint64_t* dp_full = s_full + 1;
     uint64_t* p_full = dp_full + 1;
     uint64_t* ds_full = p_full + 1;
     uint64_t* out_full = ds_full + 1;
-    uint64_t* fixed = out_full + 1;        // S: Q and dO rows past the sequence are zero
-    uint64_t* drain = fixed + S;
+    uint64_t* drain = out_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    __shared__ int abort_flag;
+    int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(k_full, 1);
         mbar_init(v_full, 1);
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < SQ; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], 1);
+            mbar_init(&q_fixed[s], 1);
+        }
+        for (int s = 0; s < SO; ++s) {
             mbar_init(&do_full[s], 1);
             mbar_init(&do_empty[s], 1);
-            mbar_init(&fixed[s], 1);
+            mbar_init(&do_fixed[s], 1);
         }
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
@@ -437,47 +444,50 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             for (int b = 0; b < C::kBoxes; ++b)
                 tma_load_3d(sV + b * 16384, &p.mapV, v_full, b * 64, kvh, sq.k0 + key0);
         }
-        for (int t = 0; t < n; ++t) {
-            const int s = t % S;
-            const uint32_t ph = (t / S) & 1;
-            const int pack = t / per, i = i0 + (t - pack * per);
-            const int head0 = kvh * sh.group + (pack << sh.hp_log2);
-            if (lane == 0) {
-                ok = mbar_wait(&q_empty[s], ph ^ 1u, w, 1) && mbar_wait(&do_empty[s], ph ^ 1u, w, 2);
-                if (ok) {
-                    mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        tma_load_3d(sQ + s * C::kTileBytes + b * 16384, &p.mapQ, &q_full[s], b * 64, head0,
-                                    sq.q0 + i * tpt);
-                    mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        tma_load_3d(sDO + s * C::kTileBytes + b * 16384, &p.mapDO, &do_full[s], b * 64, head0,
-                                    sq.q0 + i * tpt);
-                }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (!ok) break;
-            ++issued;
-            if (tail && i == qt - 1) {
-                ok = mbar_wait(&q_full[s], ph, w, 3) && mbar_wait(&do_full[s], ph, w, 4);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                zero_tile_rows(sQ + s * C::kTileBytes, C::kBoxes, ragged << sh.hp_log2);
-                zero_tile_rows(sDO + s * C::kTileBytes, C::kBoxes, ragged << sh.hp_log2);
+        const auto fix = [&](uint8_t* tile, uint64_t* full, uint32_t ph, uint64_t* fixed, bool ragged_tile, int site) {
+            if (ragged_tile) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(full, ph, w, site));
+                if (!ok) return;
+                zero_tile_rows(tile, C::kBoxes, ragged << sh.hp_log2);
                 __syncwarp();
             }
-            // the MMAs of every tile wait here: the rows of this stage are the sequence's own
-            if (lane == 0) mbar_arrive(&fixed[s]);
+            // the MMAs of every tile wait here: its rows are the sequence's own
+            if (lane == 0) mbar_arrive(fixed);
+        };
+        int issued_o = 0;
+        for (int t = 0; t < n; ++t) {
+            const int s = t % SQ, o = t % SO;
+            const int pack = t / per, i = i0 + (t - pack * per);
+            const int head0 = kvh * sh.group + (pack << sh.hp_log2);
+            const bool ragged_tile = tail && i == qt - 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_empty[s], ((t / SQ) & 1) ^ 1u, w, 1));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + s * C::kTileBytes + b * 16384, &p.mapQ, &q_full[s], b * 64, head0, sq.q0 + i * tpt);
+            }
+            ++issued;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&do_empty[o], ((t / SO) & 1) ^ 1u, w, 2));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&do_full[o], C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sDO + o * C::kTileBytes + b * 16384, &p.mapDO, &do_full[o], b * 64, head0, sq.q0 + i * tpt);
+            }
+            ++issued_o;
+            fix(sQ + s * C::kTileBytes, &q_full[s], (t / SQ) & 1, &q_fixed[s], ragged_tile, 3);
+            if (!ok) break;
+            fix(sDO + o * C::kTileBytes, &do_full[o], (t / SO) & 1, &do_fixed[o], ragged_tile, 4);
+            if (!ok) break;
         }
         if (!ok && lane == 0) {
             if (n > 0) {
                 mbar_wait_drain(k_full, 0, p.ctl.wait_ns);
                 mbar_wait_drain(v_full, 0, p.ctl.wait_ns);
             }
-            for (int t = max(0, issued - S); t < issued; ++t) {
-                mbar_wait_drain(&q_full[t % S], (t / S) & 1, p.ctl.wait_ns);
-                mbar_wait_drain(&do_full[t % S], (t / S) & 1, p.ctl.wait_ns);
-            }
+            for (int t = max(0, issued - SQ); t < issued; ++t) mbar_wait_drain(&q_full[t % SQ], (t / SQ) & 1, p.ctl.wait_ns);
+            for (int t = max(0, issued_o - SO); t < issued_o; ++t) mbar_wait_drain(&do_full[t % SO], (t / SO) & 1, p.ctl.wait_ns);
         }
     } else if (warp == 9) {
         if (elect_one()) {
@@ -493,37 +503,36 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             if (n > 0) ok = mbar_wait(k_full, 0, w, 5) && mbar_wait(v_full, 0, w, 8);
             // turn t: dV += P(t - 1)^T dO(t - 1), S^T(t), dK += dS(t - 1)^T Q(t - 1), dP^T(t)
             for (int t = 0; t <= n && n > 0 && ok; ++t) {
-                const uint64_t cur = static_cast<uint64_t>(t % S) * (C::kTileBytes >> 4);
-                const uint64_t prev = static_cast<uint64_t>((t + S - 1) % S) * (C::kTileBytes >> 4);
                 if (t > 0) {
                     if (!mbar_wait(p_full, (t - 1) & 1, w, 10)) { ok = false; break; }
                     tc_fence_after();
+                    const uint64_t b = domn + static_cast<uint64_t>((t - 1) % SO) * (C::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_ta(t_dv, t_s + a_col(ks), domn + prev + ks * 128u, idesc_o,
-                                     (t != 1 || ks != 0) ? 1u : 0u);
-                    umma_commit(&do_empty[(t - 1) % S]);
+                        umma_bf16_ta(t_dv, t_s + a_col(ks), b + ks * 128u, idesc_o, (t != 1 || ks != 0) ? 1u : 0u);
+                    umma_commit(&do_empty[(t - 1) % SO]);
                 }
                 if (t < n) {
-                    if (!mbar_wait(&q_full[t % S], (t / S) & 1, w, 6)) { ok = false; break; }
-                    if (!mbar_wait(&fixed[t % S], (t / S) & 1, w, 7)) { ok = false; break; }
+                    if (!mbar_wait(&q_full[t % SQ], (t / SQ) & 1, w, 6)) { ok = false; break; }
+                    if (!mbar_wait(&q_fixed[t % SQ], (t / SQ) & 1, w, 7)) { ok = false; break; }
                     tc_fence_after();
-                    mma_rows<DP>(t_s, kd, qd + cur, idesc_s);
+                    mma_rows<DP>(t_s, kd, qd + static_cast<uint64_t>(t % SQ) * (C::kTileBytes >> 4), idesc_s);
                     umma_commit(s_full);
                 }
                 if (t > 0) {
                     if (!mbar_wait(ds_full, (t - 1) & 1, w, 11)) { ok = false; break; }
                     tc_fence_after();
+                    const uint64_t b = qmn + static_cast<uint64_t>((t - 1) % SQ) * (C::kTileBytes >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_ta(t_dk, t_dp + a_col(ks), qmn + prev + ks * 128u, idesc_o,
-                                     (t != 1 || ks != 0) ? 1u : 0u);
-                    umma_commit(&q_empty[(t - 1) % S]);
+                        umma_bf16_ta(t_dk, t_dp + a_col(ks), b + ks * 128u, idesc_o, (t != 1 || ks != 0) ? 1u : 0u);
+                    umma_commit(&q_empty[(t - 1) % SQ]);
                 }
                 if (t < n) {
-                    if (!mbar_wait(&do_full[t % S], (t / S) & 1, w, 9)) { ok = false; break; }
+                    if (!mbar_wait(&do_full[t % SO], (t / SO) & 1, w, 9)) { ok = false; break; }
+                    if (!mbar_wait(&do_fixed[t % SO], (t / SO) & 1, w, 8)) { ok = false; break; }
                     tc_fence_after();
-                    mma_rows<DP>(t_dp, vd, dod + cur, idesc_s);
+                    mma_rows<DP>(t_dp, vd, dod + static_cast<uint64_t>(t % SO) * (C::kTileBytes >> 4), idesc_s);
                     umma_commit(dp_full);
                 }
             }
@@ -552,6 +561,9 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             const float x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
             return g == 0 ? x * kLog2e : x;
         };
+        if (sq.gap + sh.lead + sh.trail > 0)
+            fill_rows(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
+                      (sq.kl + kAttnTile - 1) / kAttnTile, blockIdx.x / sh.hkv, sh.items / sh.hkv, threadIdx.x);
         bool ok = true;
         float next = n > 0 ? fetch(0) : 0.f;
         for (int t = 0; t < n; ++t) {
@@ -633,26 +645,11 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             tc_fence_after();
         }
         if (ok) {
-            const int key = key0 + r;
-            const bool row_ok = key < sq.kl;
-            uint16_t* dk = p.dK.p + (static_cast<int64_t>(sq.k0) + key) * p.dK.row + static_cast<int64_t>(kvh) * p.dK.head;
-            uint16_t* dv = p.dV.p + (static_cast<int64_t>(sq.k0) + key) * p.dV.row + static_cast<int64_t>(kvh) * p.dV.head;
-            // group 0 writes dV, group 1 dK
-            const uint32_t from = (g == 0 ? t_dv : t_dk) + lanes;
-            uint16_t* out = g == 0 ? dv : dk;
-            const float f = g == 0 ? 1.f : sh.scale;
-#pragma unroll 1
-            for (int c = 0; c < sh.d16; c += 16) {
-                uint32_t o[16];
-                if (n > 0) {
-                    tmem_ld16(from + c, o);
-                    tmem_ld_wait(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
-                }
-                if (row_ok) store_out16(out, o, f, c, sh.d);
-            }
+            // group 0 writes dV, group 1 dK, through V's and K's shared memory: all products are done
+            const AttnMat& m = g == 0 ? p.dV : p.dK;
+            store_tile(m.p + (static_cast<int64_t>(sq.k0) + key0) * m.row + static_cast<int64_t>(kvh) * m.head, m.row, m.head,
+                           0, sq.kl - key0, sh.d, sh.d16, smem_u32(g == 0 ? sV : sK), (g == 0 ? t_dv : t_dk) + lanes, quad, n > 0,
+                           g == 0 ? 1.f : sh.scale);
         }
     }
 

@@ -223,6 +223,10 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         const int head = head0 + (r & (sh.hp - 1));
         const int limit = tok + off;                 // last visible key (clamped below kl: tok < ql)
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+        // under the first loads
+        if (sq.gap + sh.lead + sh.trail > 0)
+            fill_rows(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
+                      local / sh.packs, pairs, blockIdx.x / sh.packs, sh.items / sh.packs, threadIdx.x);
         const uint32_t ts = tmem + lanes + i * 128;
         const uint32_t to = tmem + lanes + 256 + i * DP;
         const float sl = sh.scale_log2;
@@ -310,26 +314,13 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
             tc_fence_after();
         }
         if (ok) {
-            const bool row_ok = tok < sq.ql;
-            const float f = l == 0.f ? 0.f : 1.f / l;   // no visible key: zeros; a NaN stays one
-            uint16_t* out = p.O.p + (static_cast<int64_t>(sq.q0) + tok) * p.O.row + static_cast<int64_t>(head) * p.O.head;
-#pragma unroll 1
-            for (int c = 0; c < sh.d16; c += 16) {
-                uint32_t o[16];
-                if (n > 0) {
-                    tmem_ld16(to + c, o);
-                    tmem_ld_wait(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
-                }
-                if (l == 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
-                }
-                if (row_ok) store_out16(out, o, f, c, sh.d);
-            }
-            if (row_ok)
+            // through the query tile's shared memory: its products are done
+            const int tok_0 = tok0 + i * tpt;
+            const int rows = (sq.ql - tok_0) << sh.hp_log2;   // of the tile that are in the sequence
+            store_tile(p.O.p + (static_cast<int64_t>(sq.q0) + tok_0) * p.O.row + static_cast<int64_t>(head0) * p.O.head,
+                           p.O.row, p.O.head, sh.hp_log2, rows, sh.d, sh.d16, smem_u32(sQ) + i * C::kTileBytes, to, quad, n > 0,
+                           l == 0.f ? 0.f : 1.f / l);   // no visible key: zeros; a NaN stays one
+            if (r < rows)
                 p.lse[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
         }
     }
