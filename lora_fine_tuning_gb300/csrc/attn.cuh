@@ -88,16 +88,22 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[M][N]) {
     for (int i = 0; i < M; ++i) tmem_landed(r[i]);
 }
 
-// The sequence that holds work item `item`: the last whose first item is not after it.
+// A CTA's work item (tile); gridDim.x counts the heads, and gridDim.y alone may not count a long batch's tiles.
+__device__ __forceinline__ int attn_item() { return blockIdx.z * gridDim.y + blockIdx.y; }
+
+// The sequence that holds work item `item`: the last whose first item is not after it.  By a converged warp, a lane an
+// entry: first every 32nd entry of a long table, then the 32 from there.
 template <int N>
 __device__ __forceinline__ AttnSeq find_seq(const AttnSeqs<N>& t, int n, int item) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.s[mid].item0 <= item) lo = mid;
-        else hi = mid;
+    const int lane = lane_id();
+    int from = 0;
+    if (N > 32 && n > 32) {
+        const int at = lane * 32;
+        from = (__popc(__ballot_sync(0xFFFFFFFFu, at < n && t.s[min(at, n - 1)].item0 <= item)) - 1) * 32;
     }
-    return t.s[lo];
+    const int at = from + lane;
+    const int k = from + __popc(__ballot_sync(0xFFFFFFFFu, at < n && t.s[min(at, n - 1)].item0 <= item)) - 1;
+    return t.s[max(k, 0)];
 }
 
 // Zeroes rows [from, 128) of a swizzled tile of `boxes` 64-feature boxes of 128 rows x 128 bytes, by one warp (rows
@@ -146,14 +152,19 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t row_stride, in
             }
         }
         __syncwarp();
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int row = k * 4 + (lane >> 3);
+            v[k] = lds128(box + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+        }
         if (c + (lane & 7) * 8 < d) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const int row = k * 4 + (lane >> 3), tr = quad * 32 + row;
+                const int tr = quad * 32 + k * 4 + (lane >> 3);
                 if (tr < rows)
                     stg128(out + static_cast<int64_t>(tr >> hp_log2) * row_stride +
-                               static_cast<int64_t>(tr & ((1 << hp_log2) - 1)) * head_stride + c + (lane & 7) * 8,
-                           lds128(box + row * 128 + (((lane & 7) ^ (row & 7)) << 4)));
+                               static_cast<int64_t>(tr & ((1 << hp_log2) - 1)) * head_stride + c + (lane & 7) * 8, v[k]);
             }
         }
         __syncwarp();

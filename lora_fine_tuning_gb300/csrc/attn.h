@@ -12,8 +12,9 @@ namespace lora {
 constexpr int kAttnMaxSeqs = 1024;
 constexpr int kAttnTile = 128;        // rows of a query tile and of a key tile
 
-// One sequence of the batch.  A kernel's work items are numbered sequence by sequence; item0 is the first of this
-// one's (the table is in order of falling work, not of rows).
+// One sequence of the batch.  A kernel's work items (tiles, attn_item()) are numbered sequence by sequence; item0 is the
+// first of this one's (the table is in order of falling work, not of rows).  The heads are
+// blockIdx.x: the tiles with the most work of all heads come first.
 struct AttnSeq {
     int32_t q0, k0;      // first row of the queries, of the keys
     int32_t ql, kl;      // rows
@@ -39,7 +40,7 @@ struct AttnMat {
 // packs of a group are separate tiles.
 struct AttnShape {
     int32_t n_seqs;
-    int32_t items;
+    int32_t items;           // tiles of all sequences
     int32_t hq, hkv, group;
     int32_t hp, hp_log2;     // query heads in a tile
     int32_t packs;           // hq / hp: packs of the whole layer
@@ -85,6 +86,11 @@ struct AttnFillParams {
     float* lse;              // may be null
     int32_t n;
 };
+
+inline dim3 attn_grid(int heads, int items) {
+    const int y = items < 65535 ? items : 65535;
+    return dim3(static_cast<unsigned>(heads), static_cast<unsigned>(y), static_cast<unsigned>((items + y - 1) / y));
+}
 
 cudaError_t attn_fwd_configure();
 cudaError_t attn_bwd_configure();

@@ -93,13 +93,13 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int64_t tiles_of(int64_t rows, int per) { return (rows + per - 1) / per; }
 
-// Numbers the items (tiles of `per` rows, times `wide`) of every sequence, in the table's order.
+// Numbers the items (tiles) of every sequence, in the table's order.
 template <class Tiles>
-lora_status number_items(Prepared& c, Tiles tiles, int64_t wide) {
+lora_status number_items(Prepared& c, Tiles tiles) {
     int64_t items = 0;
     for (int i = 0; i < c.n; ++i) {
         c.order.s[i].item0 = static_cast<int32_t>(items);
-        items += tiles(c.order.s[i]) * wide;
+        items += tiles(c.order.s[i]);
         if (items > 0x7FFFFFFF) return LORA_ESHAPE;
     }
     c.sh.n_seqs = c.n;
@@ -192,7 +192,7 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     order_by_keys(c);
     const int tokens = kAttnTile / c.sh.hp;
-    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, 2 * tokens); }, c.sh.packs))) return st;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, 2 * tokens); }))) return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
     }
@@ -266,13 +266,13 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
         AttnDeltaParams d{O, dO, a.o.row, a.o.head, a.d_o.row, a.d_o.head, a.q_rows, a.q_heads, a.head_dim, p.delta};
         LORA_CUDA(timed(kAttnDelta, s, [&] { return launch_attn_delta(d, s); }));
     }
-    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }, c.sh.packs))) return st;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }))) return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
     }
     p.sh = c.sh;
     if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, s); }));
-    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }, c.sh.hkv))) return st;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }))) return st;
     if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, [](const AttnSeq& q) { return q.k0; }, [](const AttnSeq& q) { return q.kl; })) {
         if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
     }

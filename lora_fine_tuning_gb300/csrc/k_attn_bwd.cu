@@ -75,6 +75,8 @@ struct CfgQ {
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    const int item = attn_item();
+    if (item >= p.sh.items) return;   // the last plane of the grid
     using C = CfgQ<DP>;
     constexpr int SK = C::kStagesK, SV = C::kStagesV;
     extern __shared__ uint8_t smem_raw[];
@@ -136,13 +138,13 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDq << 8};
 
     const AttnShape& sh = p.sh;
-    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;
-    const int tiles = (sq.ql + tpt - 1) / tpt;
-    const int local = blockIdx.x - sq.item0;
-    const int tok0 = (tiles - 1 - local / sh.packs) * tpt;
-    const int head0 = (local % sh.packs) << sh.hp_log2;
-    const int kvh = head0 / sh.group;
+    const int tiles = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
+    const int local = item - sq.item0;
+    const int tok0 = (tiles - 1 - local) * tpt;
+    const int head0 = blockIdx.x << sh.hp_log2;
+    const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
     const int off = sq.kl - sq.ql;
     const int last = min(tok0 + tpt, sq.ql) - 1 + off;            // last key the tile sees
     const int n = last >= 0 ? last / kAttnTile + 1 : 0;
@@ -253,7 +255,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
-                      local / sh.packs, tiles, blockIdx.x / sh.packs, sh.items / sh.packs, threadIdx.x);
+                      local, tiles, item, sh.items, threadIdx.x);
         float lse2 = 0.f, delta = 0.f;
         if (row_ok) {
             const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
@@ -347,6 +349,8 @@ __device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" :
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    const int item = attn_item();
+    if (item >= p.sh.items) return;   // the last plane of the grid
     using C = CfgKV<DP>;
     constexpr int SQ = C::kStagesQ, SO = C::kStagesO;
     // no other shared memory: the dynamic part starts on a swizzle atom, and there is no room to move it
@@ -417,16 +421,15 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDkDv << 8};
 
     const AttnShape& sh = p.sh;
-    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;
-    const int local = blockIdx.x - sq.item0;
-    const int kt = local / sh.hkv;                       // the first key tiles have the most queries
-    const int kvh = local - kt * sh.hkv;
+    const int kt = item - sq.item0;                // the first key tiles have the most queries
+    const int kvh = blockIdx.x;
     const int off = sq.kl - sq.ql;
     const int key0 = kt * kAttnTile;
     // the first query tile with a row that sees the first key, and the tiles after it, for each pack of the group
-    const int i0 = max(0, key0 - off) / tpt;
-    const int qt = (sq.ql + tpt - 1) / tpt;
+    const int i0 = max(0, key0 - off) >> (7 - sh.hp_log2);
+    const int qt = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
     const int per = max(0, qt - i0);
     const int packs = sh.group >> sh.hp_log2;
     const int n = per * packs;
@@ -457,7 +460,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         int issued_o = 0;
         for (int t = 0; t < n; ++t) {
             const int s = t % SQ, o = t % SO;
-            const int pack = t / per, i = i0 + (t - pack * per);
+            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const int head0 = kvh * sh.group + (pack << sh.hp_log2);
             const bool ragged_tile = tail && i == qt - 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_empty[s], ((t / SQ) & 1) ^ 1u, w, 1));
@@ -553,7 +556,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         const float* src = g == 0 ? p.lse : p.delta; // group 0 fetches lse, group 1 delta
         // one tile ahead: lse in the exponent's units (a row that is not there, or sees no key: +inf, P = 0), delta
         const auto fetch = [&](int t) -> float {
-            const int pack = t / per, i = i0 + (t - pack * per);
+            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const int tok = i * tpt + (ct >> sh.hp_log2);
             const int head = kvh * sh.group + (pack << sh.hp_log2) + (ct & (sh.hp - 1));
             const bool there = t < n && tok < sq.ql && tok + off >= 0;
@@ -563,7 +566,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         };
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
-                      (sq.kl + kAttnTile - 1) / kAttnTile, blockIdx.x / sh.hkv, sh.items / sh.hkv, threadIdx.x);
+                      (sq.kl + kAttnTile - 1) / kAttnTile, item, sh.items, threadIdx.x);
         bool ok = true;
         float next = n > 0 ? fetch(0) : 0.f;
         for (int t = 0; t < n; ++t) {
@@ -571,7 +574,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             stat[g * 128 + ct] = next;
             score_sync();
             next = fetch(t + 1);
-            const int pack = t / per, i = i0 + (t - pack * per);
+            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const uint32_t st = smem_u32(stat) + g * 256;    // this group's 64 columns
             ok = mbar_wait(s_full, t & 1, w, 12);
             // after a wait that gave up the loop runs on (each later wait returns at once): the barrier above counts
@@ -663,13 +666,13 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
 
 template <int DP, int N>
 cudaError_t run_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
-    return launch_pdl(attn_dq_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), CfgQ<DP>::kSmem, stream, p,
+    return launch_pdl(attn_dq_kernel<DP, N>, attn_grid(p.sh.packs, p.sh.items), dim3(kThreads), CfgQ<DP>::kSmem, stream, p,
                       reinterpret_cast<const AttnSeqs<N>&>(seqs));
 }
 
 template <int DP, int N>
 cudaError_t run_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
-    return launch_pdl(attn_dkdv_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), CfgKV<DP>::kSmem, stream, p,
+    return launch_pdl(attn_dkdv_kernel<DP, N>, attn_grid(p.sh.hkv, p.sh.items), dim3(kThreads), CfgKV<DP>::kSmem, stream, p,
                       reinterpret_cast<const AttnSeqs<N>&>(seqs));
 }
 

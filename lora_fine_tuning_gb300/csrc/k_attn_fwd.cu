@@ -30,6 +30,8 @@ struct Cfg {
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    const int item = attn_item();
+    if (item >= p.sh.items) return;   // the last plane of the grid
     using C = Cfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_1024(smem_raw);
@@ -85,14 +87,13 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
 
     // the item: a pair of query tiles of one pack of heads, the pairs with the most keys first
     const AttnShape& sh = p.sh;
-    const AttnSeq sq = find_seq(seqs, sh.n_seqs, blockIdx.x);
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
-    const int pairs = (sq.ql + 2 * tpt - 1) / (2 * tpt);
-    const int local = blockIdx.x - sq.item0;
-    const int pack = local % sh.packs;
-    const int tok0 = (pairs - 1 - local / sh.packs) * 2 * tpt;      // first token of tile 0
-    const int head0 = pack << sh.hp_log2;
-    const int kvh = head0 / sh.group;
+    const int pairs = (sq.ql + 2 * tpt - 1) >> (8 - sh.hp_log2);    // of 2 tpt tokens
+    const int local = item - sq.item0;
+    const int tok0 = (pairs - 1 - local) * 2 * tpt;                 // first token of tile 0
+    const int head0 = blockIdx.x << sh.hp_log2;
+    const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
     const int off = sq.kl - sq.ql;
     int nk[2];
 #pragma unroll
@@ -226,7 +227,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
-                      local / sh.packs, pairs, blockIdx.x / sh.packs, sh.items / sh.packs, threadIdx.x);
+                      local, pairs, item, sh.items, threadIdx.x);
         const uint32_t ts = tmem + lanes + i * 128;
         const uint32_t to = tmem + lanes + 256 + i * DP;
         const float sl = sh.scale_log2;
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(256) attn_fill_kernel(const __grid_constant__ 
 
 template <int DP, int N>
 cudaError_t run(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
-    return launch_pdl(attn_fwd_kernel<DP, N>, dim3(p.sh.items), dim3(kThreads), Cfg<DP>::kSmem, stream, p,
+    return launch_pdl(attn_fwd_kernel<DP, N>, attn_grid(p.sh.packs, p.sh.items), dim3(kThreads), Cfg<DP>::kSmem, stream, p,
                       reinterpret_cast<const AttnSeqs<N>&>(seqs));
 }
 
