@@ -284,33 +284,36 @@ _STREAM_WS: dict = {}
 class _On:
     """Allocates on the device of `t` and for the stream the call runs on: the caching allocator then hands the
     memory to nobody else before that stream is done with it."""
+    __slots__ = ("index", "stream", "handle")
 
     def __init__(self, t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        if t.device.index != torch.cuda.current_device():
+        self.index = t.get_device()
+        if self.index != torch.cuda.current_device():
             raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-        self.device = t.device
         self.stream = stream
-        self.handle = _stream(stream)
+        self.handle = _current_stream(self.index) if stream is None else stream.cuda_stream
 
     def empty(self, shape, dtype):
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.index)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.index)
 
     def workspace(self, kind: str, size: int) -> torch.Tensor:
         """A cached workspace of this stream (calls on different streams may overlap), zeroed when it is made."""
-        key = (kind, self.device.index, self.handle)
+        key = (kind, self.index, self.handle)
         ws = _STREAM_WS.get(key)
         if ws is None or ws.numel() < size:
-            size = max(256, 1 << (size - 1).bit_length())
-            if self.stream is None:
-                ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
-            else:
-                with torch.cuda.stream(self.stream):
-                    ws = torch.zeros(size, dtype=torch.uint8, device=self.device)
+            ws = self.empty(max(256, 1 << (size - 1).bit_length()), torch.uint8)
+            with torch.cuda.stream(self.stream):
+                ws.zero_()
             _STREAM_WS[key] = ws
         return ws
+
+
+# the handle of a device's current stream, without the objects of torch.cuda.current_stream (3 us of a call's 25)
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class AttnSeqs:
@@ -335,36 +338,36 @@ def attn_seqs(seqs) -> AttnSeqs:
     return AttnSeqs([(s[0], s[1], s[0], s[1]) if len(s) == 2 else s for s in seqs])
 
 
-def _check_heads(name: str, t: torch.Tensor, shape) -> None:
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+def _heads(shape, field: str, name: str, t: torch.Tensor, rows: int, heads: int, d: int) -> None:
+    """Checks one rows x heads x head_dim operand and puts its strides into lora_attn_shape."""
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(2) != 1 and t.shape[2] != 1:
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
+    row, head, inner = t.stride()
+    if inner != 1 and d != 1:
         raise ValueError(f"the features of a head of {name} must be contiguous")
+    m = getattr(shape, field)   # the stride of an extent of one is never used, and torch lets it be anything
+    if rows > 1:
+        m.row = row
+    if heads > 1:
+        m.head = head
 
 
 def _attn_shape(Q, K, V, O, scale):
-    if Q.dim() != 3 or K.dim() != 3 or V.dim() != 3:
+    if Q.dim() != 3 or K.dim() != 3:
         raise ValueError("Q, K and V are rows x heads x head_dim")
     (q_rows, q_heads, d), (k_rows, kv_heads, _) = Q.shape, K.shape
-    _check_heads("Q", Q, (q_rows, q_heads, d))
-    _check_heads("K", K, (k_rows, kv_heads, d))
-    _check_heads("V", V, (k_rows, kv_heads, d))
-    _check_heads("O", O, (q_rows, q_heads, d))
-    s = native.AttnShape(q_rows, k_rows, q_heads, kv_heads, d, d ** -0.5 if scale is None else float(scale))
-    for field, t in (("q", Q), ("k", K), ("v", V), ("o", O)):
-        _set_strides(s, field, t)
+    s = native.AttnShape(q_rows, k_rows, q_heads, kv_heads, d, d ** -0.5 if scale is None else scale)
+    _heads(s, "q", "Q", Q, q_rows, q_heads, d)
+    _heads(s, "k", "K", K, k_rows, kv_heads, d)
+    _heads(s, "v", "V", V, k_rows, kv_heads, d)
+    _heads(s, "o", "O", O, q_rows, q_heads, d)
     return s
 
 
-def _set_strides(shape, field: str, t: torch.Tensor) -> None:
-    m = getattr(shape, field)   # the stride of an extent of one is never used, and torch lets it be anything
-    m.row, m.head = (t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
-
-
 def _check_lse(lse, q_rows: int, q_heads: int) -> None:
-    if lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or tuple(lse.shape) != (q_rows, q_heads):
+    if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (q_rows, q_heads):
         raise ValueError(f"lse must be a contiguous CUDA float32 tensor of shape {(q_rows, q_heads)}")
 
 
@@ -376,9 +379,11 @@ def attn_fwd(Q, K, V, seqs, *, scale: Optional[float] = None, O=None, lse=None, 
     on = _On(Q, stream)
     O = O if O is not None else on.empty(Q.shape, torch.bfloat16)
     shape = _attn_shape(Q, K, V, O, scale)
-    lse = lse if lse is not None else on.empty(Q.shape[:2], torch.float32)
-    _check_lse(lse, Q.shape[0], Q.shape[1])
-    ws = ws if ws is not None else on.workspace("attn", 256)
+    rows, heads = shape.q_rows, shape.q_heads
+    if lse is None:
+        lse = on.empty((rows, heads), torch.float32)
+    _check_lse(lse, rows, heads)
+    ws = ws if ws is not None else on.workspace("attn", attn_workspace_size(rows, heads))
     st = native.lib().attn_fwd(_ptr(Q), _ptr(K), _ptr(V), ctypes.byref(shape), seqs.array, len(seqs), _ptr(O),
                                _ptr(lse), _ptr(ws), ws.numel(), on.handle)
     native.check("attn_fwd", st)
@@ -396,8 +401,7 @@ def attn_bwd(dO, Q, K, V, O, lse, seqs, *, scale: Optional[float] = None, dQ=Non
     dV = dV if dV is not None else on.empty(V.shape, torch.bfloat16)
     shape = _attn_shape(Q, K, V, O, scale)
     for name, field, t, like in (("dO", "d_o", dO, Q), ("dQ", "d_q", dQ, Q), ("dK", "d_k", dK, K), ("dV", "d_v", dV, V)):
-        _check_heads(name, t, like.shape)
-        _set_strides(shape, field, t)
+        _heads(shape, field, name, t, *like.shape)
     _check_lse(lse, Q.shape[0], Q.shape[1])
     ws = ws if ws is not None else on.workspace("attn", attn_workspace_size(Q.shape[0], Q.shape[1]))
     st = native.lib().attn_bwd(_ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), ctypes.byref(shape),
@@ -437,8 +441,13 @@ _DTYPES = {torch.bfloat16: native.BF16, torch.float32: native.F32}
 def _check_rows(name: str, t, rows: int, dtype) -> None:
     if t is None:
         return
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != rows or t.dim() != 1:
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != (rows,):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} vector of {rows}")
+
+
+def _given_f32(name: str, t: torch.Tensor, n: int) -> torch.Tensor:
+    _check_f32(name, t, n)
+    return t
 
 
 def _logits(on, logits, labels, logp, dlogits, want_grad):
@@ -449,19 +458,23 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of a row must be contiguous")
     _check_rows("labels", labels, rows, torch.int64)
-    ld = logits.stride(0) if rows > 1 else vocab
+    ld = d_ld = logits.stride(0) if rows > 1 else vocab
     if logp is None:
         logp = on.empty((rows,), torch.float32)
-    _check_rows("logp", logp, rows, torch.float32)
+    else:
+        _check_rows("logp", logp, rows, torch.float32)
     if dlogits is None and want_grad:
         # rows as far apart as the logits' own: whole 16-byte vectors are then stored as they were loaded
-        dlogits = on.empty((max(rows, 1) * ld,), logits.dtype).as_strided((rows, vocab), (ld, 1))
-    d_ld = vocab
-    if dlogits is not None:
+        if ld == vocab:
+            dlogits = on.empty((rows, vocab), logits.dtype)
+        else:
+            dlogits = on.empty((max(rows, 1) * ld,), logits.dtype).as_strided((rows, vocab), (ld, 1))
+    elif dlogits is not None:
         if dlogits.dtype != logits.dtype or not dlogits.is_cuda or dlogits.shape != logits.shape or \
                 (vocab > 1 and dlogits.stride(1) != 1):
             raise ValueError(f"dlogits must be a CUDA {logits.dtype} matrix of shape {tuple(logits.shape)}, rows contiguous")
-        d_ld = dlogits.stride(0) if rows > 1 else ld
+        if rows > 1:
+            d_ld = dlogits.stride(0)
     g = native.Logits(_ptr(logits), _ptr(dlogits), rows, vocab, ld, d_ld, _ptr(labels), _ptr(logp),
                       _DTYPES[logits.dtype], 0)
     return g, logp, dlogits
@@ -483,10 +496,8 @@ def pref_loss(logits, labels, pairs, ref_logp=None, *, beta: float = 0.1, label_
     on = _On(logits, stream)
     g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
     _check_rows("ref_logp", ref_logp, logits.shape[0], torch.float32)
-    loss = loss if loss is not None else on.empty((), torch.float32)
-    margins = margins if margins is not None else on.empty((len(pairs),), torch.float32)
-    _check_f32("loss", loss, 1)
-    _check_f32("margins", margins, len(pairs))
+    loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
+    margins = on.empty((len(pairs),), torch.float32) if margins is None else _given_f32("margins", margins, len(pairs))
     ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
     st = native.lib().pref_loss(ctypes.byref(g), pairs.array, len(pairs), _ptr(ref_logp), float(beta),
                                 float(label_smoothing), float(scale), _ptr(loss), _ptr(margins), _ptr(ws), ws.numel(),
@@ -505,8 +516,7 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, *, clip_low
     g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
     for name, t in (("old_logp", old_logp), ("advantages", advantages), ("ref_logp", ref_logp)):
         _check_rows(name, t, logits.shape[0], torch.float32)
-    loss = loss if loss is not None else on.empty((), torch.float32)
-    _check_f32("loss", loss, 1)
+    loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
     ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
     st = native.lib().policy_loss(ctypes.byref(g), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp), float(clip_low),
                                   float(clip_high), float(kl_coef), float(scale), _ptr(loss), _ptr(ws), ws.numel(),
@@ -556,6 +566,10 @@ class AdamWTensors:
     def __init__(self, tensors):
         self.tensors = list(tensors)
         self.array = (native.AdamWTensor * max(1, len(self.tensors)))()
+        given = [x for t in self.tensors for x in (t.param, t.grad, t.m, t.v, t.master, t.m_scale, t.v_scale) if x is not None]
+        self.device = given[0].get_device() if given else None
+        if any(x.get_device() != self.device for x in given):
+            raise ValueError("the tensors of one step must be on one device")
         for a, t in zip(self.array, self.tensors):
             n = t.param.numel()
             for name in ("param", "grad"):
@@ -592,10 +606,14 @@ def adamw_step(tensors, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
     """One AdamW step (include/lora.h) over `tensors` (adamw_tensors(...) or a list of AdamWTensor), in place.
     grad_scale: optional fp32 scalar on the device that multiplies every gradient; step counts from 1."""
     tensors = adamw_tensors(tensors)
+    index = torch.cuda.current_device()
+    if tensors.device not in (None, index):
+        raise ValueError(f"tensors are on cuda:{tensors.device}, the current device is cuda:{index}")
     if grad_scale is not None:
         _check_f32("grad_scale", grad_scale, 1)
     st = native.lib().adamw_step(tensors.array, len(tensors), float(lr), float(beta1), float(beta2), float(eps),
-                                 float(weight_decay), int(step), _ptr(grad_scale), _stream(stream))
+                                 float(weight_decay), int(step), _ptr(grad_scale),
+                                 _current_stream(index) if stream is None else stream.cuda_stream)
     native.check("adamw_step", st)
 
 

@@ -20,6 +20,7 @@ struct AttnSeq {
     int32_t ql, kl;      // rows
     int32_t item0;
     int32_t gap;         // unused rows of the output after this sequence that its items fill
+    int32_t split;       // forward, keys split over several items: their number << 20 | first slot; 0: not split
 };
 
 // The table travels as a kernel parameter (no device table, no copy); a small batch passes a small one.
@@ -56,8 +57,14 @@ struct AttnFwdParams {
     AttnShape sh;
     AttnMat O;
     float* lse;              // rows x hq
+    float* part;             // slots of partial results (kAttnSlotFloats each), slot * packs + pack
     DevCtl ctl;
 };
+
+// What an item of a split sequence leaves: the sums into O before their division, feature groups of 4 x 128 rows x 4,
+// then each row's maximum and sum.
+constexpr int kAttnSlotFloats = 128 * 128 + 2 * 128;
+constexpr int kAttnMaxSlots = 640;   // slots x packs of a call: at most four items an SM (attn_api.cu)
 
 struct AttnBwdParams {
     CUtensorMap mapQ, mapK, mapV, mapDO;
@@ -95,6 +102,8 @@ inline dim3 attn_grid(int heads, int items) {
 cudaError_t attn_fwd_configure();
 cudaError_t attn_bwd_configure();
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+// Joins the partial results of the split sequences (n of them, the first of the table).
+cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream);
 cudaError_t launch_attn_delta(const AttnDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);

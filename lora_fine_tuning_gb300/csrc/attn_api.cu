@@ -11,6 +11,7 @@ namespace lora {
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+constexpr size_t kSplitBytes = static_cast<size_t>(kAttnMaxSlots) * kAttnSlotFloats * 4;
 
 struct Prepared {
     AttnShape sh;
@@ -54,7 +55,7 @@ lora_status check_seqs(const lora_attn_seq* seqs, int32_t n, int64_t q_rows, int
         k_end = s.k_start + s.k_rows;
         if (s.q_rows > 0 || s.k_rows > 0)
             c.order.s[c.n++] = AttnSeq{static_cast<int32_t>(s.q_start), static_cast<int32_t>(s.k_start),
-                                       static_cast<int32_t>(s.q_rows), static_cast<int32_t>(s.k_rows), 0, 0};
+                                       static_cast<int32_t>(s.q_rows), static_cast<int32_t>(s.k_rows), 0, 0, 0};
     }
     gap(c.q_gaps, c.nq_gaps, q_end, q_rows);
     gap(c.k_gaps, c.nk_gaps, k_end, k_rows);
@@ -91,6 +92,10 @@ lora_status check_workspace(void* ws, size_t have, size_t need) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+size_t delta_bytes(int64_t q_rows, int32_t q_heads) {
+    return up256(static_cast<size_t>(q_rows) * static_cast<size_t>(q_heads) * 4);
+}
+
 int64_t tiles_of(int64_t rows, int per) { return (rows + per - 1) / per; }
 
 // Numbers the items (tiles) of every sequence, in the table's order.
@@ -109,6 +114,30 @@ lora_status number_items(Prepared& c, Tiles tiles) {
 
 void order_by_keys(Prepared& c) {
     std::stable_sort(c.order.s, c.order.s + c.n, [](const AttnSeq& a, const AttnSeq& b) { return a.kl > b.kl; });
+}
+
+int key_tiles(const AttnSeq& q) { return static_cast<int>(tiles_of(q.kl, kAttnTile)); }
+
+// Splits the keys of sequences whose rows fill one query tile at most (`tokens` of them), where their long ranges would
+// keep a few SMs busy long after the others: into pieces of equal length, of at most what an SM gets of the call's work
+// (but of no fewer than eight key tiles: a piece costs the start and end of an item, about as much as six).  They come
+// first in the table, as the join wants them.  Returns how many they are.  24 continuations of 1 to 22 tokens over prompts of 440 to 12000 keys, 32/8 heads of 128:
+// 63 us and 8 us for the join; pieces of half that length 67 and 10, none 121.
+int split_keys(Prepared& c, int tokens, int sms) {
+    AttnSeq* const end = c.order.s + c.n;
+    int64_t work = 0;
+    for (const AttnSeq* q = c.order.s; q != end; ++q)
+        work += tiles_of(q->ql, 2 * tokens) * key_tiles(*q) * c.sh.packs;
+    const int64_t most = std::max<int64_t>(8, tiles_of(work, sms));
+    int64_t slots = 0;
+    for (AttnSeq* q = c.order.s; q != end; ++q) {
+        if (q->ql == 0 || q->ql > tokens || key_tiles(*q) <= most) continue;
+        const int64_t n = tiles_of(key_tiles(*q), most);
+        if ((slots + n) * c.sh.packs > kAttnMaxSlots) break;
+        q->split = static_cast<int32_t>(n << 20 | slots);
+        slots += n;
+    }
+    return static_cast<int>(std::stable_partition(c.order.s, end, [](const AttnSeq& q) { return q.split != 0; }) - c.order.s);
 }
 
 AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
@@ -168,7 +197,7 @@ extern "C" {
 
 size_t attn_workspace_size(int64_t q_rows, int32_t q_heads) {
     if (q_rows < 0 || q_heads < 0) return 0;
-    return kStatusBytes + up256(static_cast<size_t>(q_rows) * static_cast<size_t>(q_heads) * 4);
+    return kStatusBytes + std::max(kSplitBytes, delta_bytes(q_rows, q_heads));
 }
 
 lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const lora_attn_shape* shape,
@@ -192,7 +221,9 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     order_by_keys(c);
     const int tokens = kAttnTile / c.sh.hp;
-    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, 2 * tokens); }))) return st;
+    const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, tokens, sms) : 0;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q.split >> 20 : tiles_of(q.ql, 2 * tokens); })))
+        return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
     }
@@ -211,7 +242,9 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     p.O = mat(O, a.o);
     p.lse = lse;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
     LORA_CUDA(timed(kAttnFwd, s, [&] { return launch_attn_fwd(p, c.order, s); }));
+    if (split > 0) LORA_CUDA(timed(kAttnJoin, s, [&] { return launch_attn_join(p, c.order, split, s); }));
     return LORA_OK;
 }
 
@@ -235,7 +268,7 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     if ((st = check_mat(dK, a.d_k, a.k_rows, a.kv_heads, a.head_dim))) return st;
     if ((st = check_mat(dV, a.d_v, a.k_rows, a.kv_heads, a.head_dim))) return st;
     if ((st = check_seqs(seqs, n_seqs, a.q_rows, a.k_rows, c))) return st;
-    if ((st = check_workspace(workspace, workspace_bytes, attn_workspace_size(a.q_rows, a.q_heads)))) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes + delta_bytes(a.q_rows, a.q_heads)))) return st;
     int sms = 0;
     if ((st = device_setup(&sms))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

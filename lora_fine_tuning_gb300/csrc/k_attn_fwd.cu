@@ -91,7 +91,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
     const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
     const int pairs = (sq.ql + 2 * tpt - 1) >> (8 - sh.hp_log2);    // of 2 tpt tokens
     const int local = item - sq.item0;
-    const int tok0 = (pairs - 1 - local) * 2 * tpt;                 // first token of tile 0
+    const int tok0 = sq.split ? 0 : (pairs - 1 - local) * 2 * tpt;  // first token of tile 0
     const int head0 = blockIdx.x << sh.hp_log2;
     const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
     const int off = sq.kl - sq.ql;
@@ -102,8 +102,16 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         const int last = min(first + tpt, sq.ql) - 1;               // last token of the tile
         nk[i] = (first < sq.ql && last + off >= 0) ? (last + off) / kAttnTile + 1 : 0;
     }
+    // few rows, many keys: the item has a range of the keys of the sequence's only tile
+    const int splits = sq.split >> 20;
+    int kb = 0;                                                     // its first key tile
+    if (splits > 0) {
+        const int all = nk[0], per = (all + splits - 1) / splits;
+        kb = min(local * per, all);
+        nk[0] = min(per, all - kb);
+    }
     const int nkm = max(nk[0], nk[1]);
-    const bool tail = nkm * kAttnTile > sq.kl;                      // the last key tile ends past the sequence
+    const bool tail = (kb + nkm) * kAttnTile > sq.kl;               // the last key tile ends past the sequence
 
     if (warp == 8) {
         bool ok = true;
@@ -127,7 +135,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                     const CUtensorMap* map = (t & 1) ? &p.mapV : &p.mapK;
                     for (int b = 0; b < C::kBoxes; ++b)
                         tma_load_3d(sKV + s * C::kTileBytes + b * 16384, map, &kv_full[s], b * 64, kvh,
-                                    sq.k0 + (t >> 1) * kAttnTile);
+                                    sq.k0 + (kb + (t >> 1)) * kAttnTile);
                 }
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -139,7 +147,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
             ok = mbar_wait(&kv_full[t % kStages], (t / kStages) & 1, w, 2);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) {
-                zero_tile_rows(sKV + (t % kStages) * C::kTileBytes, C::kBoxes, sq.kl - (nkm - 1) * kAttnTile);
+                zero_tile_rows(sKV + (t % kStages) * C::kTileBytes, C::kBoxes, sq.kl - (kb + nkm - 1) * kAttnTile);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_fixed);
             }
@@ -227,7 +235,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
-                      local, pairs, item, sh.items, threadIdx.x);
+                      local, splits > 0 ? splits : pairs, item, sh.items, threadIdx.x);
         const uint32_t ts = tmem + lanes + i * 128;
         const uint32_t to = tmem + lanes + 256 + i * DP;
         const float sl = sh.scale_log2;
@@ -244,9 +252,9 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, v[c]);
             tmem_ld_wait(v);
-            if ((j + 1) * kAttnTile - 1 > first_limit) {
+            if ((kb + j + 1) * kAttnTile - 1 > first_limit) {
                 // keys past the row's limit (and past the sequence: limit < kl)
-                const int lim = limit - j * kAttnTile;
+                const int lim = limit - (kb + j) * kAttnTile;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -314,7 +322,22 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         }
-        if (ok) {
+        if (ok && splits > 0) {
+            if (i == 0) {
+                float* const slot = p.part + (static_cast<int64_t>((sq.split & 0xFFFFF) + local) * sh.packs + blockIdx.x) * kAttnSlotFloats;
+#pragma unroll 1
+                for (int c = 0; c < sh.d16; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(to + c, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        stg128(slot + ((c + e) * 128 + r * 4), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                }
+                slot[128 * 128 + r] = m;
+                slot[128 * 128 + 128 + r] = l;
+            }
+        } else if (ok) {
             // through the query tile's shared memory: its products are done
             const int tok_0 = tok0 + i * tpt;
             const int rows = (sq.ql - tok_0) << sh.hp_log2;   // of the tile that are in the sequence
@@ -332,6 +355,42 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the partial results of a split sequence's items: with M the largest of their maxima m_s,
+//   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  Blocks of 128 rows x 4 features, a thread a row.
+template <int N>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnFwdParams p,
+                                                        const __grid_constant__ AttnSeqs<N> seqs) {
+    pdl_wait();
+    pdl_trigger();
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = seqs.s[blockIdx.y];
+    const int splits = sq.split >> 20, r = threadIdx.x, c = blockIdx.z * 4;
+    if (r >= sq.ql << sh.hp_log2) return;
+    const float* const slot = p.part + (static_cast<int64_t>(sq.split & 0xFFFFF) * sh.packs + blockIdx.x) * kAttnSlotFloats;
+    const int64_t step = static_cast<int64_t>(sh.packs) * kAttnSlotFloats;
+    float top = neg_inf();
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, slot[s * step + 128 * 128 + r]);
+    const float ts = top == neg_inf() ? 0.f : top;
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s) {
+        const float* const q = slot + s * step;
+        const float f = ex2(q[128 * 128 + r] - ts), ls = q[128 * 128 + 128 + r];
+        if (ls == 0.f) continue;   // no key of this range is visible
+        const float4 v = *reinterpret_cast<const float4*>(q + c * 128 + r * 4);
+        l = fmaf(f, ls, l);
+        o[0] = fmaf(f, v.x, o[0]);
+        o[1] = fmaf(f, v.y, o[1]);
+        o[2] = fmaf(f, v.z, o[2]);
+        o[3] = fmaf(f, v.w, o[3]);
+    }
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const int64_t row = static_cast<int64_t>(sq.q0) + (r >> sh.hp_log2);
+    const int head = (blockIdx.x << sh.hp_log2) + (r & (sh.hp - 1));
+    *reinterpret_cast<uint2*>(p.O.p + row * p.O.row + static_cast<int64_t>(head) * p.O.head + c) =
+        make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+    if (c == 0) p.lse[row * sh.hq + head] = l == 0.f ? neg_inf() : (top + __log2f(l)) * kLn2;
 }
 
 // Rows of no sequence: zeros (and lse -inf), so that what reads the whole batch later finds no stale values.
@@ -380,6 +439,14 @@ cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>
     const bool few = p.sh.n_seqs <= kAttnFewSeqs;
     if (p.sh.d <= 64) return few ? run<64, kAttnFewSeqs>(p, seqs, stream) : run<64, kAttnMaxSeqs>(p, seqs, stream);
     return few ? run<128, kAttnFewSeqs>(p, seqs, stream) : run<128, kAttnMaxSeqs>(p, seqs, stream);
+}
+
+cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream) {
+    const dim3 grid(p.sh.packs, n, p.sh.d / 4);
+    if (n <= kAttnFewSeqs)
+        return launch_pdl(attn_join_kernel<kAttnFewSeqs>, grid, dim3(128), 0, stream, p,
+                          reinterpret_cast<const AttnSeqs<kAttnFewSeqs>&>(seqs));
+    return launch_pdl(attn_join_kernel<kAttnMaxSeqs>, grid, dim3(128), 0, stream, p, seqs);
 }
 
 cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream) {

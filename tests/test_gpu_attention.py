@@ -282,3 +282,27 @@ def test_refusals():
         api.attn_fwd(Q, K, V[:32], [(0, 64, 0, 64)])
     with pytest.raises(TypeError):
         api.attn_fwd(Q.float(), K, V, [(0, 64, 0, 64)])
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 2, 128), (6, 2, 96)])
+def test_few_rows_over_many_keys(hq, hkv, d):
+    """Keys split over several SMs and joined: single tokens and short continuations over long prompts, rows that see
+    no key of a range or none at all, unused rows between; against the formula, and against the unsplit way (a
+    workspace without the region), which rounds the same products in another order."""
+    lens = [(1, 9000), (7, 5003), (20, 1), (1, 130), (13, 4), (2, 0), (1, 7777), (30, 1300)]
+    seqs, q, k = [], 2, 1
+    for a, b in lens:
+        seqs.append((q, a, k, b))
+        q, k = q + a + 3, k + b + 2
+    Q, K, V, _ = inputs(q, k, hq, hkv, d, seed=hq)
+    O, lse = api.attn_fwd(Q, K, V, seqs)
+    r = reference(Q, K, V, seqs, d ** -0.5)
+    assert torch.equal(torch.isinf(lse.cpu()), torch.isinf(r[1]))
+    fin = torch.isfinite(r[1])
+    assert float((lse.double().cpu() - r[1])[fin].abs().max()) <= LSE_TOL
+    assert off(O, r[0]) <= TOL
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    O2, lse2 = api.attn_fwd(Q, K, V, seqs, ws=small)
+    assert off(O2, r[0]) <= TOL and float((lse2 - lse)[torch.isfinite(lse2)].abs().max()) <= LSE_TOL
+    again = api.attn_fwd(Q, K, V, seqs)
+    assert torch.equal(O, again[0]) and torch.equal(lse, again[1])
