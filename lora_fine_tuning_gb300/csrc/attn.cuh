@@ -173,16 +173,18 @@ __device__ __forceinline__ void store_tile(uint16_t* out, int64_t row_stride, in
 
 // Unused rows that an item fills: every tiles-th row of the gap after its sequence (from `after`), its share (item
 // `turn` of `turns`) of the rows before the first and after the last sequence; heads [head0, head0 + hp) of a and, if
-// there, b, and lse.  By 256 threads, 16 a row and head.
+// there, b, and lse.  By 16 G threads, 16 a row and head.
+template <int G>
 static __device__ __noinline__ void fill_rows(const AttnMat& a, const AttnMat* b, float* lse, const AttnShape& sh, int head0,
                                               int hp_log2, int64_t after, int gap, int tile, int tiles, int turn, int turns,
                                               int thread) {
     const int hp = 1 << hp_log2, x = (thread & 15) * 8;
     const int h = (thread >> 4) & (hp - 1);
-    const int per = 16 >> min(hp_log2, 4), mine = (thread >> 4) >> min(hp_log2, 4);   // rows at a time
+    constexpr int kLog = G == 16 ? 4 : 3;
+    const int per = G >> min(hp_log2, kLog), mine = (thread >> 4) >> min(hp_log2, kLog);   // rows at a time
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     const auto clear = [&](int64_t row) {
-        for (int g = head0 + h; g < head0 + hp; g += 16) {
+        for (int g = head0 + h; g < head0 + hp; g += G) {
             if (x < sh.d) {
                 stg128(a.p + row * a.row + g * a.head + x, zero);
                 if (b) stg128(b->p + row * b->row + g * b->head + x, zero);

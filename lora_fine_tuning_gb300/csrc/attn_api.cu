@@ -127,8 +127,8 @@ int split_keys(Prepared& c, int tokens, int sms) {
     AttnSeq* const end = c.order.s + c.n;
     int64_t work = 0;
     for (const AttnSeq* q = c.order.s; q != end; ++q)
-        work += tiles_of(q->ql, 2 * tokens) * key_tiles(*q) * c.sh.packs;
-    const int64_t most = std::max<int64_t>(8, tiles_of(work, sms));
+        work += tiles_of(q->ql, tokens) * key_tiles(*q) * c.sh.packs;
+    const int64_t most = std::max<int64_t>(8, tiles_of(2 * work, 3 * sms));
     int64_t slots = 0;
     for (AttnSeq* q = c.order.s; q != end; ++q) {
         if (q->ql == 0 || q->ql > tokens || key_tiles(*q) <= most) continue;
@@ -222,7 +222,7 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     order_by_keys(c);
     const int tokens = kAttnTile / c.sh.hp;
     const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, tokens, sms) : 0;
-    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q.split >> 20 : tiles_of(q.ql, 2 * tokens); })))
+    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q.split >> 20 : tiles_of(q.ql, tokens); })))
         return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;

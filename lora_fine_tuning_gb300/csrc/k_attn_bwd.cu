@@ -86,8 +86,9 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     uint8_t* sK = sDO + C::kTileBytes;
     uint8_t* sV = sK + SK * C::kTileBytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sV + SV * C::kTileBytes);
-    uint64_t* q_full = bars;               // Q and dO
-    uint64_t* k_full = q_full + 1;         // SK each
+    uint64_t* q_full = bars;
+    uint64_t* do_full = q_full + 1;
+    uint64_t* k_full = do_full + 1;        // SK each
     uint64_t* k_empty = k_full + SK;
     uint64_t* v_full = k_empty + SK;       // SV each
     uint64_t* v_empty = v_full + SV;
@@ -103,40 +104,6 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        for (int s = 0; s < SK; ++s) {
-            mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
-        }
-        for (int s = 0; s < SV; ++s) {
-            mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 1);
-        }
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(dp_full, 1);
-        mbar_init(ds_full, 256);
-        mbar_init(dq_full, 1);
-        mbar_init(k_fixed, 1);
-        mbar_init(dp_read, 256);
-        mbar_init(drain, 1);
-        abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_wait();
-    pdl_trigger();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
-    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDq << 8};
-
     const AttnShape& sh = p.sh;
     const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;
@@ -150,34 +117,89 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     const int n = last >= 0 ? last / kAttnTile + 1 : 0;
     const bool tail = n * kAttnTile > sq.kl;
 
+    const auto load_k = [&](int j) {
+        const int s = j % SK;
+        mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sK + s * C::kTileBytes + b * 16384, &p.mapK, &k_full[s], b * 64, kvh, sq.k0 + j * kAttnTile);
+    };
+    const auto load_v = [&](int j) {
+        const int s = j % SV;
+        mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sV + s * C::kTileBytes + b * 16384, &p.mapV, &v_full[s], b * 64, kvh, sq.k0 + j * kAttnTile);
+    };
+    // the first loads are under way before the CTA's other warps are set up
+    const int ahead = min(SV, n);
     if (warp == 8) {
-        bool ok = true;
-        int issued = 0;
-        if (lane == 0 && n > 0) {
-            mbar_arrive_expect_tx(q_full, 2 * C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b) {
-                tma_load_3d(sQ + b * 16384, &p.mapQ, q_full, b * 64, head0, sq.q0 + tok0);
-                tma_load_3d(sDO + b * 16384, &p.mapDO, q_full, b * 64, head0, sq.q0 + tok0);
+        if (lane == 0) {
+            tma_prefetch_desc(&p.mapQ);
+            tma_prefetch_desc(&p.mapK);
+            tma_prefetch_desc(&p.mapV);
+            tma_prefetch_desc(&p.mapDO);
+            mbar_init(q_full, 1);
+            mbar_init(do_full, 1);
+            for (int s = 0; s < SK; ++s) {
+                mbar_init(&k_full[s], 1);
+                mbar_init(&k_empty[s], 1);
+            }
+            for (int s = 0; s < SV; ++s) {
+                mbar_init(&v_full[s], 1);
+                mbar_init(&v_empty[s], 1);
+            }
+            mbar_init(&s_full[0], 1);
+            mbar_init(&s_full[1], 1);
+            mbar_init(dp_full, 1);
+            mbar_init(ds_full, 256);
+            mbar_init(dq_full, 1);
+            mbar_init(k_fixed, 1);
+            mbar_init(dp_read, 256);
+            mbar_init(drain, 1);
+            abort_flag = 0;
+            fence_barrier_init();
+            pdl_wait();
+            if (n > 0) {
+                mbar_arrive_expect_tx(q_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + b * 16384, &p.mapQ, q_full, b * 64, head0, sq.q0 + tok0);
+                load_k(0);
+                mbar_arrive_expect_tx(do_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sDO + b * 16384, &p.mapDO, do_full, b * 64, head0, sq.q0 + tok0);
+                load_v(0);
+            }
+            for (int j = 1; j < ahead; ++j) {
+                load_k(j);
+                load_v(j);
             }
         }
-        for (int j = 0; j < n; ++j) {
-            const int s = j % SK, v = j % SV;
+        __syncwarp();
+    } else if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 256, t_dq = tmem + 384;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDq << 8};
+
+    if (warp == 8) {
+        bool ok = true;
+        int issued = ahead;
+        for (int j = ahead; j < n; ++j) {
             if (lane == 0) {
-                ok = mbar_wait(&k_empty[s], ((j / SK) & 1) ^ 1u, w, 1);
+                ok = mbar_wait(&k_empty[j % SK], ((j / SK) & 1) ^ 1u, w, 1);
                 if (ok) {
-                    mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        tma_load_3d(sK + s * C::kTileBytes + b * 16384, &p.mapK, &k_full[s], b * 64, kvh,
-                                    sq.k0 + j * kAttnTile);
-                    ok = mbar_wait(&v_empty[v], ((j / SV) & 1) ^ 1u, w, 2);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&v_full[v], C::kTileBytes);
-                        for (int b = 0; b < C::kBoxes; ++b)
-                            tma_load_3d(sV + v * C::kTileBytes + b * 16384, &p.mapV, &v_full[v], b * 64, kvh,
-                                        sq.k0 + j * kAttnTile);
-                    } else {
-                        mbar_wait_drain(&k_full[s], (j / SK) & 1, p.ctl.wait_ns);
-                    }
+                    load_k(j);
+                    ok = mbar_wait(&v_empty[j % SV], ((j / SV) & 1) ^ 1u, w, 2);
+                    if (ok)
+                        load_v(j);
+                    else
+                        mbar_wait_drain(&k_full[j % SK], (j / SK) & 1, p.ctl.wait_ns);
                 }
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -195,7 +217,10 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             }
         }
         if (!ok && lane == 0) {
-            if (n > 0) mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
+            if (n > 0) {
+                mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
+                mbar_wait_drain(do_full, 0, p.ctl.wait_ns);
+            }
             for (int j = max(0, issued - SK); j < issued; ++j) mbar_wait_drain(&k_full[j % SK], (j / SK) & 1, p.ctl.wait_ns);
             for (int j = max(0, issued - SV); j < issued; ++j) mbar_wait_drain(&v_full[j % SV], (j / SV) & 1, p.ctl.wait_ns);
         }
@@ -219,6 +244,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
                     tc_fence_after();
                     mma_rows<DP>(t_s + (j & 1) * 128, qd, kd + static_cast<uint64_t>(j % SK) * (C::kTileBytes >> 4), idesc_s);
                     umma_commit(&s_full[j & 1]);
+                    if (j == 0 && !mbar_wait(do_full, 0, w, 13)) { ok = false; break; }
                     if (!mbar_wait(&v_full[j % SV], (j / SV) & 1, w, 7)) { ok = false; break; }
                     if (j > 0 && !mbar_wait(dp_read, (j - 1) & 1, w, 12)) { ok = false; break; }
                     tc_fence_after();
@@ -254,7 +280,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         const float sl = sh.scale_log2;
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
-            fill_rows(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
+            fill_rows<16>(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
                       local, tiles, item, sh.items, threadIdx.x);
         float lse2 = 0.f, delta = 0.f;
         if (row_ok) {
@@ -385,41 +411,6 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        mbar_init(k_full, 1);
-        mbar_init(v_full, 1);
-        for (int s = 0; s < SQ; ++s) {
-            mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
-            mbar_init(&q_fixed[s], 1);
-        }
-        for (int s = 0; s < SO; ++s) {
-            mbar_init(&do_full[s], 1);
-            mbar_init(&do_empty[s], 1);
-            mbar_init(&do_fixed[s], 1);
-        }
-        mbar_init(s_full, 1);
-        mbar_init(dp_full, 1);
-        mbar_init(p_full, 256);
-        mbar_init(ds_full, 256);
-        mbar_init(out_full, 1);
-        mbar_init(drain, 1);
-        abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_wait();
-    pdl_trigger();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
-    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDkDv << 8};
-
     const AttnShape& sh = p.sh;
     const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;
@@ -436,17 +427,81 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     const int ragged = sq.ql - (qt - 1) * tpt;           // tokens of the last query tile
     const bool tail = ragged < tpt;
 
+    const auto head_of = [&](int t) { return kvh * sh.group + ((packs == 1 ? 0 : t / per) << sh.hp_log2); };
+    const auto tile_of = [&](int t) { return i0 + (packs == 1 ? t : t - t / per * per); };
+    const auto load_q = [&](int t) {
+        const int s = t % SQ;
+        mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sQ + s * C::kTileBytes + b * 16384, &p.mapQ, &q_full[s], b * 64, head_of(t), sq.q0 + tile_of(t) * tpt);
+    };
+    const auto load_do = [&](int t) {
+        const int s = t % SO;
+        mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sDO + s * C::kTileBytes + b * 16384, &p.mapDO, &do_full[s], b * 64, head_of(t), sq.q0 + tile_of(t) * tpt);
+    };
+    // the first loads are under way before the CTA's other warps are set up
+    const int ahead = min(SO, n);
+    if (warp == 8) {
+        if (lane == 0) {
+            tma_prefetch_desc(&p.mapQ);
+            tma_prefetch_desc(&p.mapK);
+            tma_prefetch_desc(&p.mapV);
+            tma_prefetch_desc(&p.mapDO);
+            mbar_init(k_full, 1);
+            mbar_init(v_full, 1);
+            for (int s = 0; s < SQ; ++s) {
+                mbar_init(&q_full[s], 1);
+                mbar_init(&q_empty[s], 1);
+                mbar_init(&q_fixed[s], 1);
+            }
+            for (int s = 0; s < SO; ++s) {
+                mbar_init(&do_full[s], 1);
+                mbar_init(&do_empty[s], 1);
+                mbar_init(&do_fixed[s], 1);
+            }
+            mbar_init(s_full, 1);
+            mbar_init(dp_full, 1);
+            mbar_init(p_full, 256);
+            mbar_init(ds_full, 256);
+            mbar_init(out_full, 1);
+            mbar_init(drain, 1);
+            abort_flag = 0;
+            fence_barrier_init();
+            pdl_wait();
+            if (n > 0) {
+                mbar_arrive_expect_tx(k_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sK + b * 16384, &p.mapK, k_full, b * 64, kvh, sq.k0 + key0);
+                load_q(0);
+                mbar_arrive_expect_tx(v_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sV + b * 16384, &p.mapV, v_full, b * 64, kvh, sq.k0 + key0);
+                load_do(0);
+            }
+            for (int t = 1; t < ahead; ++t) {
+                load_q(t);
+                load_do(t);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDkDv << 8};
+
     if (warp == 8) {
         bool ok = true;
-        int issued = 0;
-        if (lane == 0 && n > 0) {
-            mbar_arrive_expect_tx(k_full, C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b)
-                tma_load_3d(sK + b * 16384, &p.mapK, k_full, b * 64, kvh, sq.k0 + key0);
-            mbar_arrive_expect_tx(v_full, C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b)
-                tma_load_3d(sV + b * 16384, &p.mapV, v_full, b * 64, kvh, sq.k0 + key0);
-        }
+        int issued = ahead, issued_o = ahead;
         const auto fix = [&](uint8_t* tile, uint64_t* full, uint32_t ph, uint64_t* fixed, bool ragged_tile, int site) {
             if (ragged_tile) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(full, ph, w, site));
@@ -457,28 +512,19 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             // the MMAs of every tile wait here: its rows are the sequence's own
             if (lane == 0) mbar_arrive(fixed);
         };
-        int issued_o = 0;
         for (int t = 0; t < n; ++t) {
             const int s = t % SQ, o = t % SO;
-            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
-            const int head0 = kvh * sh.group + (pack << sh.hp_log2);
-            const bool ragged_tile = tail && i == qt - 1;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_empty[s], ((t / SQ) & 1) ^ 1u, w, 1));
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
-                for (int b = 0; b < C::kBoxes; ++b)
-                    tma_load_3d(sQ + s * C::kTileBytes + b * 16384, &p.mapQ, &q_full[s], b * 64, head0, sq.q0 + i * tpt);
+            const bool ragged_tile = tail && tile_of(t) == qt - 1;
+            if (t >= ahead) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&q_empty[s], ((t / SQ) & 1) ^ 1u, w, 1));
+                if (!ok) break;
+                if (lane == 0) load_q(t);
+                ++issued;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&do_empty[o], ((t / SO) & 1) ^ 1u, w, 2));
+                if (!ok) break;
+                if (lane == 0) load_do(t);
+                ++issued_o;
             }
-            ++issued;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&do_empty[o], ((t / SO) & 1) ^ 1u, w, 2));
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&do_full[o], C::kTileBytes);
-                for (int b = 0; b < C::kBoxes; ++b)
-                    tma_load_3d(sDO + o * C::kTileBytes + b * 16384, &p.mapDO, &do_full[o], b * 64, head0, sq.q0 + i * tpt);
-            }
-            ++issued_o;
             fix(sQ + s * C::kTileBytes, &q_full[s], (t / SQ) & 1, &q_fixed[s], ragged_tile, 3);
             if (!ok) break;
             fix(sDO + o * C::kTileBytes, &do_full[o], (t / SO) & 1, &do_fixed[o], ragged_tile, 4);
@@ -503,7 +549,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             const uint64_t qmn = make_smem_desc(smem_u32(sQ), 16384, 1024, kSw128);
             const uint64_t domn = make_smem_desc(smem_u32(sDO), 16384, 1024, kSw128);
             bool ok = true;
-            if (n > 0) ok = mbar_wait(k_full, 0, w, 5) && mbar_wait(v_full, 0, w, 8);
+            if (n > 0) ok = mbar_wait(k_full, 0, w, 5);
             // turn t: dV += P(t - 1)^T dO(t - 1), S^T(t), dK += dS(t - 1)^T Q(t - 1), dP^T(t)
             for (int t = 0; t <= n && n > 0 && ok; ++t) {
                 if (t > 0) {
@@ -532,6 +578,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
                     umma_commit(&q_empty[(t - 1) % SQ]);
                 }
                 if (t < n) {
+                    if (t == 0 && !mbar_wait(v_full, 0, w, 8)) { ok = false; break; }
                     if (!mbar_wait(&do_full[t % SO], (t / SO) & 1, w, 9)) { ok = false; break; }
                     if (!mbar_wait(&do_fixed[t % SO], (t / SO) & 1, w, 8)) { ok = false; break; }
                     tc_fence_after();
@@ -565,7 +612,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             return g == 0 ? x * kLog2e : x;
         };
         if (sq.gap + sh.lead + sh.trail > 0)
-            fill_rows(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
+            fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
                       (sq.kl + kAttnTile - 1) / kAttnTile, item, sh.items, threadIdx.x);
         bool ok = true;
         float next = n > 0 ? fetch(0) : 0.f;

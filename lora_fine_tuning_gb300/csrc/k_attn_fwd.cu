@@ -16,66 +16,105 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kStages = 5;        // of K or V tiles, which alternate
 constexpr float kRescale = 8.f;   // log2 of the growth of a row's maximum that rescales O
+
+constexpr int kThreads = 192;     // warps 0-3: softmax; warp 4: TMA; warp 5: MMAs
 
 template <int DP>
 struct Cfg {
     static constexpr int kBoxes = DP / 64;
     static constexpr uint32_t kTileBytes = kBoxes * 16384u;   // 128 rows x DP bf16
-    static constexpr size_t kSmem = 1024 + (2 + kStages) * static_cast<size_t>(kTileBytes) + 256;
+    static constexpr int kStages = DP == 128 ? 2 : 4;         // of K or V tiles, which alternate
+    static constexpr size_t kSmem = 1024 + (1 + kStages) * static_cast<size_t>(kTileBytes) + 256;   // two CTAs an SM
 };
 
 template <int DP, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
     const int item = attn_item();
     if (item >= p.sh.items) return;   // the last plane of the grid
     using C = Cfg<DP>;
+    constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_1024(smem_raw);
     uint8_t* sQ = smem;
-    uint8_t* sKV = smem + 2 * C::kTileBytes;
+    uint8_t* sKV = smem + C::kTileBytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kStages * C::kTileBytes);
-    uint64_t* q_full = bars;              // 2
-    uint64_t* kv_full = q_full + 2;       // kStages
+    uint64_t* q_full = bars;
+    uint64_t* kv_full = q_full + 1;          // kStages
     uint64_t* kv_empty = kv_full + kStages;
-    uint64_t* s_full = kv_empty + kStages;   // 2
-    uint64_t* p_full = s_full + 2;           // 4: the halves of each tile's P
-    uint64_t* o_full = p_full + 4;           // 2
-    uint64_t* v_fixed = o_full + 2;          // 1: the last V tile's rows past the sequence are zero
+    uint64_t* s_full = kv_empty + kStages;
+    uint64_t* p_full = s_full + 1;           // 2: the halves of P
+    uint64_t* o_full = p_full + 2;
+    uint64_t* v_fixed = o_full + 1;          // the last V tile's rows past the sequence are zero
     uint64_t* drain = v_fixed + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[2 * i], 128);
-            mbar_init(&p_full[2 * i + 1], 128);
-            mbar_init(&o_full[i], 1);
-        }
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
-        }
-        mbar_init(v_fixed, 1);
-        mbar_init(drain, 1);
-        abort_flag = 0;
-        fence_barrier_init();
+    // the item: a query tile of one pack of heads, those with the most keys first
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
+    const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
+    const int tiles = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
+    const int local = item - sq.item0;
+    const int tok0 = sq.split ? 0 : (tiles - 1 - local) * tpt;      // first token
+    const int head0 = blockIdx.x << sh.hp_log2;
+    const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
+    const int off = sq.kl - sq.ql;
+    const int last = min(tok0 + tpt, sq.ql) - 1 + off;              // last key the tile sees
+    int n = last >= 0 ? last / kAttnTile + 1 : 0;                   // its key tiles
+    // few rows, many keys: the item has a range of the keys of the sequence's only tile
+    const int splits = sq.split >> 20;
+    int kb = 0;                                                     // its first key tile
+    if (splits > 0) {
+        const int all = n, per = (all + splits - 1) / splits;
+        kb = min(local * per, all);
+        n = min(per, all - kb);
     }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
+    const bool tail = (kb + n) * kAttnTile > sq.kl;               // the last key tile ends past the sequence
+
+    const auto load_kv = [&](int t) {
+        const int s = t % kStages;
+        mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
+        const CUtensorMap* map = (t & 1) ? &p.mapV : &p.mapK;
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sKV + s * C::kTileBytes + b * 16384, map, &kv_full[s], b * 64, kvh,
+                        sq.k0 + (kb + (t >> 1)) * kAttnTile);
+    };
+    // the first loads are under way before the CTA's other warps are set up
+    const int ahead = min(kStages, 2 * n);
+    if (warp == 4) {
+        if (lane == 0) {
+            tma_prefetch_desc(&p.mapQ);
+            tma_prefetch_desc(&p.mapK);
+            tma_prefetch_desc(&p.mapV);
+            mbar_init(q_full, 1);
+            mbar_init(s_full, 1);
+            mbar_init(&p_full[0], 128);
+            mbar_init(&p_full[1], 128);
+            mbar_init(o_full, 1);
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&kv_full[s], 1);
+                mbar_init(&kv_empty[s], 1);
+            }
+            mbar_init(v_fixed, 1);
+            mbar_init(drain, 1);
+            abort_flag = 0;
+            fence_barrier_init();
+            pdl_wait();
+            if (n > 0) {
+                mbar_arrive_expect_tx(q_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + b * 16384, &p.mapQ, q_full, b * 64, head0, sq.q0 + tok0);
+            }
+            for (int t = 0; t < ahead; ++t) load_kv(t);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        tmem_alloc(tmem_slot, 256);
         tmem_relinquish();
-    }
-    if (warp == 8 && lane == 0) {
-        tma_prefetch_desc(&p.mapQ);
-        tma_prefetch_desc(&p.mapK);
-        tma_prefetch_desc(&p.mapV);
     }
     tc_fence_before();
     __syncthreads();
@@ -85,81 +124,35 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
     const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnFwd << 8};
 
-    // the item: a pair of query tiles of one pack of heads, the pairs with the most keys first
-    const AttnShape& sh = p.sh;
-    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
-    const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
-    const int pairs = (sq.ql + 2 * tpt - 1) >> (8 - sh.hp_log2);    // of 2 tpt tokens
-    const int local = item - sq.item0;
-    const int tok0 = sq.split ? 0 : (pairs - 1 - local) * 2 * tpt;  // first token of tile 0
-    const int head0 = blockIdx.x << sh.hp_log2;
-    const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
-    const int off = sq.kl - sq.ql;
-    int nk[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int first = tok0 + i * tpt;
-        const int last = min(first + tpt, sq.ql) - 1;               // last token of the tile
-        nk[i] = (first < sq.ql && last + off >= 0) ? (last + off) / kAttnTile + 1 : 0;
-    }
-    // few rows, many keys: the item has a range of the keys of the sequence's only tile
-    const int splits = sq.split >> 20;
-    int kb = 0;                                                     // its first key tile
-    if (splits > 0) {
-        const int all = nk[0], per = (all + splits - 1) / splits;
-        kb = min(local * per, all);
-        nk[0] = min(per, all - kb);
-    }
-    const int nkm = max(nk[0], nk[1]);
-    const bool tail = (kb + nkm) * kAttnTile > sq.kl;               // the last key tile ends past the sequence
-
-    if (warp == 8) {
+    if (warp == 4) {
         bool ok = true;
-        int issued = 0;
-        if (lane == 0) {
-            for (int i = 0; i < 2; ++i) {
-                if (nk[i] == 0) continue;
-                mbar_arrive_expect_tx(&q_full[i], C::kTileBytes);
-                for (int b = 0; b < C::kBoxes; ++b)
-                    tma_load_3d(sQ + i * C::kTileBytes + b * 16384, &p.mapQ, &q_full[i], b * 64, head0,
-                                sq.q0 + tok0 + i * tpt);
-            }
-        }
-        for (int t = 0; t < 2 * nkm; ++t) {
-            const int s = t % kStages;
-            const uint32_t ph = (t / kStages) & 1;
+        int issued = ahead;
+        for (int t = ahead; t < 2 * n; ++t) {
             if (lane == 0) {
-                ok = mbar_wait(&kv_empty[s], ph ^ 1u, w, 1);
-                if (ok) {
-                    mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
-                    const CUtensorMap* map = (t & 1) ? &p.mapV : &p.mapK;
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        tma_load_3d(sKV + s * C::kTileBytes + b * 16384, map, &kv_full[s], b * 64, kvh,
-                                    sq.k0 + (kb + (t >> 1)) * kAttnTile);
-                }
+                ok = mbar_wait(&kv_empty[t % kStages], ((t / kStages) & 1) ^ 1u, w, 1);
+                if (ok) load_kv(t);
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             if (!ok) break;
             ++issued;
         }
-        if (ok && tail && nkm > 0) {
-            const int t = 2 * nkm - 1;
+        if (ok && tail && n > 0) {
+            const int t = 2 * n - 1;
             ok = mbar_wait(&kv_full[t % kStages], (t / kStages) & 1, w, 2);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) {
-                zero_tile_rows(sKV + (t % kStages) * C::kTileBytes, C::kBoxes, sq.kl - (kb + nkm - 1) * kAttnTile);
+                zero_tile_rows(sKV + (t % kStages) * C::kTileBytes, C::kBoxes, sq.kl - (kb + n - 1) * kAttnTile);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_fixed);
             }
         }
         if (!ok && lane == 0) {
             // copies in flight land before the CTA exits
-            for (int i = 0; i < 2; ++i)
-                if (nk[i] > 0) mbar_wait_drain(&q_full[i], 0, p.ctl.wait_ns);
+            if (n > 0) mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
             for (int t = max(0, issued - kStages); t < issued; ++t)
                 mbar_wait_drain(&kv_full[t % kStages], (t / kStages) & 1, p.ctl.wait_ns);
         }
-    } else if (warp == 9) {
+    } else if (warp == 5) {
         // the whole warp waits; one lane issues (elect_one)
         const uint32_t idesc_s = make_idesc_bf16(128, 128, false, false);
         const uint32_t idesc_o = make_idesc_bf16(128, sh.d16, false, true);
@@ -172,79 +165,64 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
             tc_fence_after();
             return ok;
         };
-        // turn j: for each query tile the product of P(j - 1) with V(j - 1), then the scores with K(j).  S(j)
-        // overwrites P(j - 1) in TMEM: the MMAs execute in the order in which they are issued.
-        for (int j = 0; j <= nkm && nkm > 0; ++j) {
+        // turn j: the product of P(j - 1) with V(j - 1), then the scores with K(j).  S(j) overwrites P(j - 1) in TMEM:
+        // the MMAs execute in the order in which they are issued.
+        for (int j = 0; j <= n && n > 0; ++j) {
             const int tk = 2 * j, tv = 2 * j - 1;
-            const uint64_t ks_ = kd + static_cast<uint64_t>(tk % kStages) * (C::kTileBytes >> 4);
-            const uint64_t vs_ = vd + static_cast<uint64_t>((tv + kStages) % kStages) * (C::kTileBytes >> 4);
             if (j > 0) {
+                const uint64_t b = vd + static_cast<uint64_t>(tv % kStages) * (C::kTileBytes >> 4);
                 if (!wait(&kv_full[tv % kStages], (tv / kStages) & 1, 3)) break;
-                if (tail && j == nkm && !wait(v_fixed, 0, 4)) break;
+                if (tail && j == n && !wait(v_fixed, 0, 4)) break;
+                if (j < n && !wait(&kv_full[tk % kStages], (tk / kStages) & 1, 5)) break;
+                if (!wait(&p_full[0], (j - 1) & 1, 6)) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_bf16_ta(tmem + 128, tmem + ks * 8, b + ks * 128u, idesc_o, (j != 1 || ks != 0) ? 1u : 0u);
+                }
+                __syncwarp();
+                if (!wait(&p_full[1], (j - 1) & 1, 8)) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks)
+                        umma_bf16_ta(tmem + 128, tmem + ks * 8, b + ks * 128u, idesc_o, 1u);
+                    umma_commit(j == n ? o_full : &kv_empty[tv % kStages]);
+                }
+                __syncwarp();
+            } else if (!wait(q_full, 0, 7) || !wait(&kv_full[0], 0, 5)) {
+                break;
             }
-            if (j < nkm && !wait(&kv_full[tk % kStages], (tk / kStages) & 1, 5)) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (j > 0 && j <= nk[i]) {
-                    if (!wait(&p_full[2 * i], (j - 1) & 1, 6)) break;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_bf16_ta(tmem + 256 + i * DP, tmem + i * 128 + ks * 8, vs_ + ks * 128u, idesc_o,
-                                         (j != 1 || ks != 0) ? 1u : 0u);
-                    }
-                    __syncwarp();
-                    if (!wait(&p_full[2 * i + 1], (j - 1) & 1, 8)) break;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 4; ks < 8; ++ks)
-                            umma_bf16_ta(tmem + 256 + i * DP, tmem + i * 128 + ks * 8, vs_ + ks * 128u, idesc_o, 1u);
-                        if (j == nk[i]) umma_commit(&o_full[i]);
-                    }
-                    __syncwarp();
+            if (j < n) {
+                if (elect_one()) {
+                    mma_rows<DP>(tmem, qd, kd + static_cast<uint64_t>(tk % kStages) * (C::kTileBytes >> 4), idesc_s);
+                    umma_commit(s_full);
+                    umma_commit(&kv_empty[tk % kStages]);
                 }
-                if (i == 1 && j > 0) {
-                    if (elect_one()) umma_commit(&kv_empty[tv % kStages]);
-                    __syncwarp();
-                }
-                if (j < nk[i]) {
-                    if (j == 0 && !wait(&q_full[i], 0, 7)) break;
-                    if (elect_one()) {
-                        mma_rows<DP>(tmem + i * 128, qd + i * (C::kTileBytes >> 4), ks_, idesc_s);
-                        umma_commit(&s_full[i]);
-                    }
-                    __syncwarp();
-                }
+                __syncwarp();
             }
-            if (!ok) break;
-            if (j < nkm && elect_one()) umma_commit(&kv_empty[tk % kStages]);
-            __syncwarp();
         }
         if (elect_one()) umma_commit(drain);
         __syncwarp();
         mbar_wait_drain(drain, 0, p.ctl.wait_ns);
         __syncwarp();
     } else {
-        const int i = warp >> 2;                     // query tile
-        const int quad = warp & 3;
+        const int quad = warp;
         const int r = quad * 32 + lane;              // row of the tile = TMEM lane
-        const int tok = tok0 + i * tpt + (r >> sh.hp_log2);
+        const int tok = tok0 + (r >> sh.hp_log2);
         const int head = head0 + (r & (sh.hp - 1));
         const int limit = tok + off;                 // last visible key (clamped below kl: tok < ql)
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
-            fill_rows(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
-                      local, splits > 0 ? splits : pairs, item, sh.items, threadIdx.x);
-        const uint32_t ts = tmem + lanes + i * 128;
-        const uint32_t to = tmem + lanes + 256 + i * DP;
+            fill_rows<8>(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
+                      local, splits > 0 ? splits : tiles, item, sh.items, threadIdx.x);
+        const uint32_t ts = tmem + lanes, to = ts + 128;
         const float sl = sh.scale_log2;
-        const int n = i == 0 ? nk[0] : nk[1];
-        const int first_limit = tok0 + i * tpt + off;   // last key the tile's first row sees
+        const int first_limit = tok0 + off;          // last key the tile's first row sees
         float m = neg_inf(), l = 0.f;                // maximum (in the exponent's units) and sum
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            ok = mbar_wait(&s_full[i], j & 1, w, 9);
+            ok = mbar_wait(s_full, j & 1, w, 9);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -312,37 +290,34 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&p_full[2 * i + h]);
+                mbar_arrive(&p_full[h]);
             }
             const float2 q = parts(add2(sum[0], sum[1]));
             l += q.x + q.y;
         }
         if (ok && n > 0) {
-            ok = mbar_wait(&o_full[i], 0, w, 10);
+            ok = mbar_wait(o_full, 0, w, 10);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         }
         if (ok && splits > 0) {
-            if (i == 0) {
-                float* const slot = p.part + (static_cast<int64_t>((sq.split & 0xFFFFF) + local) * sh.packs + blockIdx.x) * kAttnSlotFloats;
+            float* const slot = p.part + (static_cast<int64_t>((sq.split & 0xFFFFF) + local) * sh.packs + blockIdx.x) * kAttnSlotFloats;
 #pragma unroll 1
-                for (int c = 0; c < sh.d16; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(to + c, o);
-                    tmem_ld_wait(o);
+            for (int c = 0; c < sh.d16; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + c, o);
+                tmem_ld_wait(o);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        stg128(slot + ((c + e) * 128 + r * 4), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-                }
-                slot[128 * 128 + r] = m;
-                slot[128 * 128 + 128 + r] = l;
+                for (int e = 0; e < 16; e += 4)
+                    stg128(slot + ((c + e) * 128 + r * 4), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
             }
+            slot[128 * 128 + r] = m;
+            slot[128 * 128 + 128 + r] = l;
         } else if (ok) {
             // through the query tile's shared memory: its products are done
-            const int tok_0 = tok0 + i * tpt;
-            const int rows = (sq.ql - tok_0) << sh.hp_log2;   // of the tile that are in the sequence
-            store_tile(p.O.p + (static_cast<int64_t>(sq.q0) + tok_0) * p.O.row + static_cast<int64_t>(head0) * p.O.head,
-                           p.O.row, p.O.head, sh.hp_log2, rows, sh.d, sh.d16, smem_u32(sQ) + i * C::kTileBytes, to, quad, n > 0,
+            const int rows = (sq.ql - tok0) << sh.hp_log2;    // of the tile that are in the sequence
+            store_tile(p.O.p + (static_cast<int64_t>(sq.q0) + tok0) * p.O.row + static_cast<int64_t>(head0) * p.O.head,
+                           p.O.row, p.O.head, sh.hp_log2, rows, sh.d, sh.d16, smem_u32(sQ), to, quad, n > 0,
                            l == 0.f ? 0.f : 1.f / l);   // no visible key: zeros; a NaN stays one
             if (r < rows)
                 p.lse[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head] = l == 0.f ? neg_inf() : (m + __log2f(l)) * kLn2;
@@ -351,9 +326,9 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, 256);
     }
 }
 
