@@ -474,13 +474,13 @@ const char* lora_status_string(lora_status s);
  * time in ms and the number of launches.  Kinds: 0 down-projection,
  * 1 finalize S, 2 forward GEMM, 3 dS/dB, 4 finalize dS/dB, 5 backward GEMM,
  * 6 dA, 7 finalize dA, 8 memset (gradients of adapters that own no rows),
- * 9-12 DoRA (U, norm, dZ, dmag), 13-18 attention
- * (forward, joining of split rows, delta, dQ, dK and dV, unused rows),
- * 19-22 losses (rows, pairs, gradient, sum), 23 AdamW.  When kind 6 runs on the library's side
+ * 9-12 DoRA (U, norm, dZ, dmag), 13-17 attention
+ * (forward, joining of split rows, dQ, dK and dV, unused rows),
+ * 18-21 losses (rows, pairs, gradient, sum), 22 AdamW.  When kind 6 runs on the library's side
  * stream beside the backward GEMM, its event pair spans from the fork to its
  * end.
  * Host-side cost: two event records per launch. */
-enum { LORA_KERNEL_KINDS = 24 };
+enum { LORA_KERNEL_KINDS = 23 };
 lora_status lora_timing_begin(void);
 lora_status lora_timing_end(float* total_ms, int32_t* launches, int32_t n_kinds);
 const char* lora_kernel_name(int32_t kind);

@@ -65,7 +65,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 const char* const kKindNames[kKinds] = {"down_proj", "finalize_s", "gemm_fwd", "ds_db", "finalize_ds_db",
                                         "gemm_bwd", "da", "finalize_da", "memset",
                                         "dora_u", "dora_norm", "dora_dz", "dora_dmag",
-                                        "attn_fwd", "attn_join", "attn_delta", "attn_dq", "attn_dkdv", "attn_fill",
+                                        "attn_fwd", "attn_join", "attn_dq", "attn_dkdv", "attn_fill",
                                         "loss_rows", "loss_pairs", "loss_grad", "loss_sum", "adamw"};
 
 struct TimingRec {

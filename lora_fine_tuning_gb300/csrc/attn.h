@@ -67,20 +67,12 @@ constexpr int kAttnSlotFloats = 128 * 128 + 2 * 128;
 constexpr int kAttnMaxSlots = 640;   // slots x packs of a call: at most four items an SM (attn_api.cu)
 
 struct AttnBwdParams {
-    CUtensorMap mapQ, mapK, mapV, mapDO;
+    CUtensorMap mapQ, mapK, mapV, mapO, mapDO;
     AttnShape sh;
     const float* lse;        // rows x hq
-    float* delta;            // rows x hq
+    float* delta;            // rows x hq, from the first pass to the second
     AttnMat dQ, dK, dV;
     DevCtl ctl;
-};
-
-struct AttnDeltaParams {
-    const uint16_t *O, *dO;
-    int64_t o_row, o_head, do_row, do_head;
-    int64_t rows;
-    int32_t hq, d;
-    float* delta;
 };
 
 // Rows of the outputs that belong to no sequence: rows [from, to) of up to three matrices get zeros, lse -inf.
@@ -104,7 +96,6 @@ cudaError_t attn_bwd_configure();
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 // Joins the partial results of the split sequences (n of them, the first of the table).
 cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream);
-cudaError_t launch_attn_delta(const AttnDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream);

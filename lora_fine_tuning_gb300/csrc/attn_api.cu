@@ -285,6 +285,7 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     const int64_t qr = std::max<int64_t>(a.q_rows, 1), kr = std::max<int64_t>(a.k_rows, 1);
     const lora_bf16* any = no_q ? K : Q;
     if (!make_map_heads(&p.mapQ, no_q ? any : Q, a.head_dim, a.q_heads, qr, a.q.head, a.q.row, c.sh.hp, tokens) ||
+        !make_map_heads(&p.mapO, no_q ? any : O, a.head_dim, a.q_heads, qr, a.o.head, a.o.row, c.sh.hp, tokens) ||
         !make_map_heads(&p.mapDO, no_q ? any : dO, a.head_dim, a.q_heads, qr, a.d_o.head, a.d_o.row, c.sh.hp, tokens) ||
         !make_map_heads(&p.mapK, no_k ? any : K, a.head_dim, a.kv_heads, kr, a.k.head, a.k.row, 1, kAttnTile) ||
         !make_map_heads(&p.mapV, no_k ? any : V, a.head_dim, a.kv_heads, kr, a.v.head, a.v.row, 1, kAttnTile))
@@ -295,10 +296,6 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     p.dK = mk;
     p.dV = mv;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
-    if (!no_q) {
-        AttnDeltaParams d{O, dO, a.o.row, a.o.head, a.d_o.row, a.d_o.head, a.q_rows, a.q_heads, a.head_dim, p.delta};
-        LORA_CUDA(timed(kAttnDelta, s, [&] { return launch_attn_delta(d, s); }));
-    }
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }))) return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;

@@ -28,7 +28,7 @@ uint64_t wait_limit_ns();
 enum Kind : int {
     kDownProj = 0, kFinalizeS, kGemmFwd, kDsDb, kFinalize, kGemmBwd, kDa, kFinalizeDa, kMemset,
     kDoraU, kDoraNorm, kDoraDz, kDoraDmag,
-    kAttnFwd, kAttnJoin, kAttnDelta, kAttnDq, kAttnDkDv, kAttnFill, kLossRows, kLossPairs, kLossGrad, kLossSum,
+    kAttnFwd, kAttnJoin, kAttnDq, kAttnDkDv, kAttnFill, kLossRows, kLossPairs, kLossGrad, kLossSum,
     kAdamW, kKinds
 };
 static_assert(static_cast<int>(kKinds) == static_cast<int>(LORA_KERNEL_KINDS), "the header counts the kinds");

@@ -3,7 +3,7 @@
 //   P = exp(scale Q K^T - lse),  delta_i = sum_d dO_id O_id,  dP = dO V^T,  dS = P (dP - delta)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,   dK and dV summed over the query heads of a group
 //
-// Three passes: delta; dQ, a CTA a 128-row query tile over its keys; dK and dV, a CTA a 128-key tile over the query
+// Two passes: dQ, a CTA a 128-row query tile over its keys (delta on the way); dK and dV, a CTA a 128-key tile over the query
 // tiles of all heads of its group.  Each gradient element is summed by one CTA in a fixed order, in TMEM in fp32:
 // the results are the same from call to call, and no partial sum goes through memory.  The price is that S and dP are
 // formed twice (seven products instead of five).
@@ -28,36 +28,8 @@ __device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
     tmem_ld_wait(v);
 }
 
-// ---------------------------------------------------------------------------------------------------------------
-// delta
-// ---------------------------------------------------------------------------------------------------------------
-
-// One (row, head) per group of 16 lanes, 8 features a lane.
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnDeltaParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t n = p.rows * p.hq;
-    const int sub = threadIdx.x & 15;
-    for (int64_t i = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 4; i < (n + 1) / 2 * 2;
-         i += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 4) {
-        float sum = 0.f;
-        const int64_t row = i / p.hq;
-        const int h = static_cast<int>(i - row * p.hq);
-        if (i < n && sub * 8 < p.d) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p.O + row * p.o_row + h * p.o_head + sub * 8);
-            const uint4 b = *reinterpret_cast<const uint4*>(p.dO + row * p.do_row + h * p.do_head + sub * 8);
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
-                sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
-            }
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (i < n && sub == 0) p.delta[i] = sum;
-    }
-}
+// Barrier among the 256 threads of the score warps.
+__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------------------------------
 // dQ
@@ -69,7 +41,7 @@ struct CfgQ {
     static constexpr uint32_t kTileBytes = kBoxes * 16384u;
     // a K tile is held from its scores to its gradients, a V tile for one product
     static constexpr int kStagesK = 3, kStagesV = 2;
-    static constexpr size_t kSmem = 1024 + (2 + kStagesK + kStagesV) * static_cast<size_t>(kTileBytes) + 256;
+    static constexpr size_t kSmem = 1024 + (2 + kStagesK + kStagesV) * static_cast<size_t>(kTileBytes) + 512 + 256;
 };
 
 template <int DP, int N>
@@ -85,10 +57,13 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     uint8_t* sDO = sQ + C::kTileBytes;
     uint8_t* sK = sDO + C::kTileBytes;
     uint8_t* sV = sK + SK * C::kTileBytes;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sV + SV * C::kTileBytes);
+    float* sDelta = reinterpret_cast<float*>(sV + SV * C::kTileBytes);   // 128
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sDelta + 128);
     uint64_t* q_full = bars;
     uint64_t* do_full = q_full + 1;
-    uint64_t* k_full = do_full + 1;        // SK each
+    uint64_t* o_full = do_full + 1;
+    uint64_t* o_read = o_full + 1;
+    uint64_t* k_full = o_read + 1;        // SK each
     uint64_t* k_empty = k_full + SK;
     uint64_t* v_full = k_empty + SK;       // SV each
     uint64_t* v_empty = v_full + SV;
@@ -129,7 +104,8 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         for (int b = 0; b < C::kBoxes; ++b)
             tma_load_3d(sV + s * C::kTileBytes + b * 16384, &p.mapV, &v_full[s], b * 64, kvh, sq.k0 + j * kAttnTile);
     };
-    // the first loads are under way before the CTA's other warps are set up
+    uint8_t* const sO = sK + (SK - 1) * C::kTileBytes;   // O, for delta, where a later K tile goes
+    // the first loads are under way before the CTA is set up
     const int ahead = min(SV, n);
     if (warp == 8) {
         if (lane == 0) {
@@ -139,6 +115,9 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             tma_prefetch_desc(&p.mapDO);
             mbar_init(q_full, 1);
             mbar_init(do_full, 1);
+            mbar_init(o_full, 1);
+            mbar_init(o_read, 256);
+            tma_prefetch_desc(&p.mapO);
             for (int s = 0; s < SK; ++s) {
                 mbar_init(&k_full[s], 1);
                 mbar_init(&k_empty[s], 1);
@@ -167,6 +146,9 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
                 for (int b = 0; b < C::kBoxes; ++b)
                     tma_load_3d(sDO + b * 16384, &p.mapDO, do_full, b * 64, head0, sq.q0 + tok0);
                 load_v(0);
+                mbar_arrive_expect_tx(o_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sO + b * 16384, &p.mapO, o_full, b * 64, head0, sq.q0 + tok0);
             }
             for (int j = 1; j < ahead; ++j) {
                 load_k(j);
@@ -193,6 +175,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         for (int j = ahead; j < n; ++j) {
             if (lane == 0) {
                 ok = mbar_wait(&k_empty[j % SK], ((j / SK) & 1) ^ 1u, w, 1);
+                if (ok && j == SK - 1) ok = mbar_wait(o_read, 0, w, 15);
                 if (ok) {
                     load_k(j);
                     ok = mbar_wait(&v_empty[j % SV], ((j / SV) & 1) ^ 1u, w, 2);
@@ -216,10 +199,12 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(k_fixed);
             }
         }
-        if (!ok && lane == 0) {
+        if (lane == 0) {
+            // every copy lands before the CTA exits, also when another warp gave up
             if (n > 0) {
                 mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
                 mbar_wait_drain(do_full, 0, p.ctl.wait_ns);
+                mbar_wait_drain(o_full, 0, p.ctl.wait_ns);
             }
             for (int j = max(0, issued - SK); j < issued; ++j) mbar_wait_drain(&k_full[j % SK], (j / SK) & 1, p.ctl.wait_ns);
             for (int j = max(0, issued - SV); j < issued; ++j) mbar_wait_drain(&v_full[j % SV], (j / SV) & 1, p.ctl.wait_ns);
@@ -282,15 +267,38 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows<16>(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
                       local, tiles, item, sh.items, threadIdx.x);
-        float lse2 = 0.f, delta = 0.f;
-        if (row_ok) {
-            const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
-            lse2 = p.lse[at] * kLog2e;
-            delta = p.delta[at];
-            if (limit < 0) lse2 = 0.f;               // no visible key: every score is masked below
-        }
+        const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
+        // a row that is not there, or sees no key: every score is masked below
+        const float lse2 = row_ok && limit >= 0 ? p.lse[at] * kLog2e : 0.f;
+        // delta of the tile's rows, while the first scores are formed
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        if (n > 0) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(do_full, 0, w, 14) && mbar_wait(o_full, 0, w, 16));
+            // DP / 8 lanes a row, 8 features a lane
+            constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kSteps = 128 / kRows;
+            const int sub = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const int dr = k * kRows + first;
+                const uint32_t at_ = (sub >> 3) * 16384 + dr * 128 + (((sub & 7) ^ (dr & 7)) << 4);
+                const uint4 a = lds128(smem_u32(sO) + at_), b = lds128(smem_u32(sDO) + at_);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                    sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+                }
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                if (sub == 0) sDelta[dr] = sum;
+            }
+            mbar_arrive(o_read);
+            score_sync();
+        }
+        const float delta = n > 0 ? sDelta[r] : 0.f;
+        if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
+        for (int j = 0; ok && j < n; ++j) {
             const uint32_t ts = t_s + (j & 1) * 128 + lanes + g * 64;
             ok = mbar_wait(&s_full[j & 1], (j >> 1) & 1, w, 9);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -368,9 +376,6 @@ struct CfgKV {
     static constexpr int kStagesQ = 3, kStagesO = 2;
     static constexpr size_t kSmem = (2 + kStagesQ + kStagesO) * static_cast<size_t>(kTileBytes) + 2 * 2 * 512 + 256;
 };
-
-// Barrier among the 256 threads of the score warps.
-__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -530,7 +535,8 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             fix(sDO + o * C::kTileBytes, &do_full[o], (t / SO) & 1, &do_fixed[o], ragged_tile, 4);
             if (!ok) break;
         }
-        if (!ok && lane == 0) {
+        if (lane == 0) {
+            // every copy lands before the CTA exits, also when another warp gave up
             if (n > 0) {
                 mbar_wait_drain(k_full, 0, p.ctl.wait_ns);
                 mbar_wait_drain(v_full, 0, p.ctl.wait_ns);
@@ -740,11 +746,6 @@ cudaError_t attn_bwd_configure() {
     if (e == cudaSuccess) e = configure<128, kAttnFewSeqs>();
     if (e == cudaSuccess) e = configure<128, kAttnMaxSeqs>();
     return e;
-}
-
-cudaError_t launch_attn_delta(const AttnDeltaParams& p, cudaStream_t stream) {
-    const int64_t blocks = std::min<int64_t>((p.rows * p.hq + 15) / 16, 152 * 16);
-    return launch_pdl(attn_delta_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {

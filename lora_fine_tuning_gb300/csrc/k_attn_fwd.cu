@@ -146,8 +146,8 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
                 if (lane == 0) mbar_arrive(v_fixed);
             }
         }
-        if (!ok && lane == 0) {
-            // copies in flight land before the CTA exits
+        if (lane == 0) {
+            // every copy lands before the CTA exits, also when another warp gave up
             if (n > 0) mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
             for (int t = max(0, issued - kStages); t < issued; ++t)
                 mbar_wait_drain(&kv_full[t % kStages], (t / kStages) & 1, p.ctl.wait_ns);

@@ -247,7 +247,7 @@ def gemm_runs(M: int, N: int, bn: int, stages: int, max_pairs: int, allow_split:
     return pairs.value, split.value, runs
 
 
-KERNEL_KINDS = 24
+KERNEL_KINDS = 23
 
 
 def timing_begin() -> None:

@@ -171,6 +171,6 @@ def test_adamw_arguments(lib):
     assert adamw(lib, tensor(), grad_scale=258) == 2
 
 
-@pytest.mark.parametrize("kind,name", [(13, "attn_fwd"), (14, "attn_join"), (18, "attn_fill"), (19, "loss_rows"), (23, "adamw")])
+@pytest.mark.parametrize("kind,name", [(13, "attn_fwd"), (14, "attn_join"), (17, "attn_fill"), (18, "loss_rows"), (22, "adamw")])
 def test_kernel_names(lib, kind, name):
     assert lib.lora_kernel_name(kind).decode() == name
