@@ -6,6 +6,7 @@ current CUDA stream to it; PyTorch only allocates outputs and workspace.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -338,8 +339,8 @@ def attn_seqs(seqs) -> AttnSeqs:
     return AttnSeqs([(s[0], s[1], s[0], s[1]) if len(s) == 2 else s for s in seqs])
 
 
-def _heads(shape, field: str, name: str, t: torch.Tensor, rows: int, heads: int, d: int) -> None:
-    """Checks one rows x heads x head_dim operand and puts its strides into lora_attn_shape."""
+def _heads(name: str, t: torch.Tensor, rows: int, heads: int, d: int):
+    """Checks one rows x heads x head_dim operand.  Returns its strides (row, head)."""
     if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
     if t.shape != (rows, heads, d):
@@ -347,23 +348,29 @@ def _heads(shape, field: str, name: str, t: torch.Tensor, rows: int, heads: int,
     row, head, inner = t.stride()
     if inner != 1 and d != 1:
         raise ValueError(f"the features of a head of {name} must be contiguous")
-    m = getattr(shape, field)   # the stride of an extent of one is never used, and torch lets it be anything
-    if rows > 1:
-        m.row = row
-    if heads > 1:
-        m.head = head
+    # the stride of an extent of one is never used, and torch lets it be anything
+    return row if rows > 1 else 0, head if heads > 1 else 0
 
 
-def _attn_shape(Q, K, V, O, scale):
+# lora_attn_shape in one go: setting the fields one by one costs as much as the launch
+_ATTN_SHAPE = struct.Struct("qqiiif16q")
+
+
+def _attn_shape(sizes, scale, strides):
+    rows, k_rows, heads, kv_heads, d = sizes
+    packed = _ATTN_SHAPE.pack(rows, k_rows, heads, kv_heads, d, d ** -0.5 if scale is None else scale, *strides)
+    return native.AttnShape.from_buffer_copy(packed)
+
+
+_NO_STRIDES = (0,) * 8
+
+
+def _attn_sizes(Q, K):
     if Q.dim() != 3 or K.dim() != 3:
         raise ValueError("Q, K and V are rows x heads x head_dim")
-    (q_rows, q_heads, d), (k_rows, kv_heads, _) = Q.shape, K.shape
-    s = native.AttnShape(q_rows, k_rows, q_heads, kv_heads, d, d ** -0.5 if scale is None else scale)
-    _heads(s, "q", "Q", Q, q_rows, q_heads, d)
-    _heads(s, "k", "K", K, k_rows, kv_heads, d)
-    _heads(s, "v", "V", V, k_rows, kv_heads, d)
-    _heads(s, "o", "O", O, q_rows, q_heads, d)
-    return s
+    rows, heads, d = Q.shape
+    k_rows, kv_heads, _ = K.shape
+    return rows, k_rows, heads, kv_heads, d
 
 
 def _check_lse(lse, q_rows: int, q_heads: int) -> None:
@@ -377,16 +384,21 @@ def attn_fwd(Q, K, V, seqs, *, scale: Optional[float] = None, O=None, lse=None, 
     1/sqrt(head_dim) if not given.  Returns (O, lse), lse the fp32 log-sum-exp of each row and head."""
     seqs = attn_seqs(seqs)
     on = _On(Q, stream)
-    O = O if O is not None else on.empty(Q.shape, torch.bfloat16)
-    shape = _attn_shape(Q, K, V, O, scale)
-    rows, heads = shape.q_rows, shape.q_heads
+    sizes = rows, k_rows, heads, kv_heads, d = _attn_sizes(Q, K)
+    if O is None:
+        O = on.empty((rows, heads, d), torch.bfloat16)
     if lse is None:
         lse = on.empty((rows, heads), torch.float32)
-    _check_lse(lse, rows, heads)
-    ws = ws if ws is not None else on.workspace("attn", attn_workspace_size(rows, heads))
-    st = native.lib().attn_fwd(_ptr(Q), _ptr(K), _ptr(V), ctypes.byref(shape), seqs.array, len(seqs), _ptr(O),
-                               _ptr(lse), _ptr(ws), ws.numel(), on.handle)
-    native.check("attn_fwd", st)
+    else:
+        _check_lse(lse, rows, heads)
+    shape = _attn_shape(sizes, scale, _heads("Q", Q, rows, heads, d) + _heads("K", K, k_rows, kv_heads, d) +
+                        _heads("V", V, k_rows, kv_heads, d) + _heads("O", O, rows, heads, d) + _NO_STRIDES)
+    if ws is None:
+        ws = on.workspace("attn", attn_workspace_size(rows, heads))
+    st = native.lib().attn_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, seqs.array, len(seqs.seqs), O.data_ptr(),
+                               lse.data_ptr(), ws.data_ptr(), ws.numel(), on.handle)
+    if st:
+        native.check("attn_fwd", st)
     return O, lse
 
 
@@ -396,17 +408,24 @@ def attn_bwd(dO, Q, K, V, O, lse, seqs, *, scale: Optional[float] = None, dQ=Non
     heads that share them."""
     seqs = attn_seqs(seqs)
     on = _On(Q, stream)
-    dQ = dQ if dQ is not None else on.empty(Q.shape, torch.bfloat16)
-    dK = dK if dK is not None else on.empty(K.shape, torch.bfloat16)
-    dV = dV if dV is not None else on.empty(V.shape, torch.bfloat16)
-    shape = _attn_shape(Q, K, V, O, scale)
-    for name, field, t, like in (("dO", "d_o", dO, Q), ("dQ", "d_q", dQ, Q), ("dK", "d_k", dK, K), ("dV", "d_v", dV, V)):
-        _heads(shape, field, name, t, *like.shape)
-    _check_lse(lse, Q.shape[0], Q.shape[1])
-    ws = ws if ws is not None else on.workspace("attn", attn_workspace_size(Q.shape[0], Q.shape[1]))
-    st = native.lib().attn_bwd(_ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse), ctypes.byref(shape),
-                               seqs.array, len(seqs), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(), on.handle)
-    native.check("attn_bwd", st)
+    sizes = rows, k_rows, heads, kv_heads, d = _attn_sizes(Q, K)
+    q, kv = (rows, heads, d), (k_rows, kv_heads, d)
+    if dQ is None:
+        dQ = on.empty(q, torch.bfloat16)
+    if dK is None:
+        dK = on.empty(kv, torch.bfloat16)
+    if dV is None:
+        dV = on.empty(kv, torch.bfloat16)
+    _check_lse(lse, rows, heads)
+    shape = _attn_shape(sizes, scale, _heads("Q", Q, *q) + _heads("K", K, *kv) + _heads("V", V, *kv) + _heads("O", O, *q) +
+                        _heads("dO", dO, *q) + _heads("dQ", dQ, *q) + _heads("dK", dK, *kv) + _heads("dV", dV, *kv))
+    if ws is None:
+        ws = on.workspace("attn", attn_workspace_size(rows, heads))
+    st = native.lib().attn_bwd(dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), shape,
+                               seqs.array, len(seqs.seqs), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
+                               ws.numel(), on.handle)
+    if st:
+        native.check("attn_bwd", st)
     return dQ, dK, dV
 
 
@@ -475,7 +494,7 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
             raise ValueError(f"dlogits must be a CUDA {logits.dtype} matrix of shape {tuple(logits.shape)}, rows contiguous")
         if rows > 1:
             d_ld = dlogits.stride(0)
-    g = native.Logits(_ptr(logits), _ptr(dlogits), rows, vocab, ld, d_ld, _ptr(labels), _ptr(logp),
+    g = native.Logits(logits.data_ptr(), _ptr(dlogits), rows, vocab, ld, d_ld, labels.data_ptr(), logp.data_ptr(),
                       _DTYPES[logits.dtype], 0)
     return g, logp, dlogits
 
@@ -499,7 +518,7 @@ def pref_loss(logits, labels, pairs, ref_logp=None, *, beta: float = 0.1, label_
     loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
     margins = on.empty((len(pairs),), torch.float32) if margins is None else _given_f32("margins", margins, len(pairs))
     ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
-    st = native.lib().pref_loss(ctypes.byref(g), pairs.array, len(pairs), _ptr(ref_logp), float(beta),
+    st = native.lib().pref_loss(g, pairs.array, len(pairs), _ptr(ref_logp), float(beta),
                                 float(label_smoothing), float(scale), _ptr(loss), _ptr(margins), _ptr(ws), ws.numel(),
                                 on.handle)
     native.check("pref_loss", st)
@@ -518,7 +537,7 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, *, clip_low
         _check_rows(name, t, logits.shape[0], torch.float32)
     loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
     ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
-    st = native.lib().policy_loss(ctypes.byref(g), _ptr(old_logp), _ptr(advantages), _ptr(ref_logp), float(clip_low),
+    st = native.lib().policy_loss(g, _ptr(old_logp), _ptr(advantages), _ptr(ref_logp), float(clip_low),
                                   float(clip_high), float(kl_coef), float(scale), _ptr(loss), _ptr(ws), ws.numel(),
                                   on.handle)
     native.check("policy_loss", st)
