@@ -31,6 +31,11 @@ __device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
 // Barrier among the 256 threads of the score warps.
 __device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// Columns 2 e and 2 e + 1 of what ld64 read.
+__device__ __forceinline__ F2 pair(const uint32_t (&v)[2][32], int e) {
+    return f2(__uint_as_float(v[e >> 4][2 * (e & 15)]), __uint_as_float(v[e >> 4][2 * (e & 15) + 1]));
+}
+
 // ---------------------------------------------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------------------------------------------
@@ -298,19 +303,21 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         }
         const float delta = n > 0 ? sDelta[r] : 0.f;
         if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
+        const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2), delta2 = f2(-delta, -delta);
         for (int j = 0; ok && j < n; ++j) {
             const uint32_t ts = t_s + (j & 1) * 128 + lanes + g * 64;
             ok = mbar_wait(&s_full[j & 1], (j >> 1) & 1, w, 9);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
-            uint32_t v[2][32], x[2][32];
-            ld64(ts, v);
+            uint32_t x[2][32];
+            F2 pr[32];
+            ld64(ts, x);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    v[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e]), sl, -lse2)));
+            for (int e = 0; e < 32; ++e) {
+                const float2 q = parts(fma2(pair(x, e), sl2, lse22));
+                pr[e] = f2(ex2(q.x), ex2(q.y));
+            }
             ok = mbar_wait(dp_full, j & 1, w, 10);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
@@ -319,10 +326,11 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             tc_fence_before();
             mbar_arrive(dp_read);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    x[c][e] = __float_as_uint(__uint_as_float(v[c][e]) * (__uint_as_float(x[c][e]) - delta));
+            for (int e = 0; e < 32; ++e) {
+                const float2 q = parts(mul(pr[e], add2(pair(x, e), delta2)));
+                x[e >> 4][2 * (e & 15)] = __float_as_uint(q.x);
+                x[e >> 4][2 * (e & 15) + 1] = __float_as_uint(q.y);
+            }
             if ((j + 1) * kAttnTile - 1 > tok0 + off) {
                 const int lim = limit - j * kAttnTile - g * 64;
 #pragma unroll
@@ -395,7 +403,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     uint8_t* sV = sK + C::kTileBytes;
     uint8_t* sQ = sV + C::kTileBytes;
     uint8_t* sDO = sQ + SQ * C::kTileBytes;
-    float* sStat = reinterpret_cast<float*>(sDO + SO * C::kTileBytes);   // [2][lse2 128, delta 128]
+    float* sStat = reinterpret_cast<float*>(sDO + SO * C::kTileBytes);   // [2][-lse2 128, -delta 128]
     uint64_t* bars = reinterpret_cast<uint64_t*>(sStat + 2 * 256);
     uint64_t* k_full = bars;               // K
     uint64_t* v_full = k_full + 1;         // V
@@ -607,15 +615,16 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         const uint32_t tdp = t_dp + lanes + g * 64;
         const float sl = sh.scale_log2;
         const float* src = g == 0 ? p.lse : p.delta; // group 0 fetches lse, group 1 delta
-        // one tile ahead: lse in the exponent's units (a row that is not there, or sees no key: +inf, P = 0), delta
+        const F2 sl2 = f2(sl, sl);
+        // one tile ahead: -lse in the exponent's units (a row that is not there, or sees no key: -inf, P = 0), -delta
         const auto fetch = [&](int t) -> float {
             const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const int tok = i * tpt + (ct >> sh.hp_log2);
             const int head = kvh * sh.group + (pack << sh.hp_log2) + (ct & (sh.hp - 1));
             const bool there = t < n && tok < sq.ql && tok + off >= 0;
-            if (!there) return g == 0 ? -neg_inf() : 0.f;
+            if (!there) return g == 0 ? neg_inf() : 0.f;
             const float x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
-            return g == 0 ? x * kLog2e : x;
+            return g == 0 ? x * -kLog2e : -x;
         };
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
@@ -642,10 +651,14 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const uint4 q = lds128(st + (c * 32 + e) * 4);
-                    v[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e]), sl, -__uint_as_float(q.x))));
-                    v[c][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 1]), sl, -__uint_as_float(q.y))));
-                    v[c][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 2]), sl, -__uint_as_float(q.z))));
-                    v[c][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c][e + 3]), sl, -__uint_as_float(q.w))));
+                    const float2 a = parts(fma2(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sl2,
+                                                f2(__uint_as_float(q.x), __uint_as_float(q.y))));
+                    const float2 b = parts(fma2(f2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])), sl2,
+                                                f2(__uint_as_float(q.z), __uint_as_float(q.w))));
+                    v[c][e] = __float_as_uint(ex2(a.x));
+                    v[c][e + 1] = __float_as_uint(ex2(a.y));
+                    v[c][e + 2] = __float_as_uint(ex2(b.x));
+                    v[c][e + 3] = __float_as_uint(ex2(b.y));
                 }
             // keys after a query's limit: key0 + r > tok + off
             int cmin = 0;
@@ -680,12 +693,14 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const uint4 q = lds128(st + 512 + (c * 32 + e) * 4);
-                    const float d0 = __uint_as_float(v[c][e]) * (__uint_as_float(x[c][e]) - __uint_as_float(q.x));
-                    const float d1 = __uint_as_float(v[c][e + 1]) * (__uint_as_float(x[c][e + 1]) - __uint_as_float(q.y));
-                    const float d2 = __uint_as_float(v[c][e + 2]) * (__uint_as_float(x[c][e + 2]) - __uint_as_float(q.z));
-                    const float d3 = __uint_as_float(v[c][e + 3]) * (__uint_as_float(x[c][e + 3]) - __uint_as_float(q.w));
-                    o[e / 2] = pack_bf16x2(d0, d1);
-                    o[e / 2 + 1] = pack_bf16x2(d2, d3);
+                    const float2 a = parts(mul(f2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])),
+                                               add2(f2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])),
+                                                    f2(__uint_as_float(q.x), __uint_as_float(q.y)))));
+                    const float2 b = parts(mul(f2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3])),
+                                               add2(f2(__uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3])),
+                                                    f2(__uint_as_float(q.z), __uint_as_float(q.w)))));
+                    o[e / 2] = pack_bf16x2(a.x, a.y);
+                    o[e / 2 + 1] = pack_bf16x2(b.x, b.y);
                 }
                 tmem_st16(tdp + c * 16, o);
             }
