@@ -275,40 +275,14 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
         // a row that is not there, or sees no key: every score is masked below
         const float lse2 = row_ok && limit >= 0 ? p.lse[at] * kLog2e : 0.f;
-        // delta of the tile's rows, while the first scores are formed
         bool ok = true;
-        if (n > 0) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(do_full, 0, w, 14) && mbar_wait(o_full, 0, w, 16));
-            // DP / 8 lanes a row, 8 features a lane
-            constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kSteps = 128 / kRows;
-            const int sub = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int dr = k * kRows + first;
-                const uint32_t at_ = (sub >> 3) * 16384 + dr * 128 + (((sub & 7) ^ (dr & 7)) << 4);
-                const uint4 a = lds128(smem_u32(sO) + at_), b = lds128(smem_u32(sDO) + at_);
-                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
-                    sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
-                }
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                if (sub == 0) sDelta[dr] = sum;
-            }
-            mbar_arrive(o_read);
-            score_sync();
-        }
-        const float delta = n > 0 ? sDelta[r] : 0.f;
-        if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
-        const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2), delta2 = f2(-delta, -delta);
-        for (int j = 0; ok && j < n; ++j) {
+        const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2);
+        F2 delta2 = f2(0.f, 0.f);
+        for (int j = 0; j < n; ++j) {
             const uint32_t ts = t_s + (j & 1) * 128 + lanes + g * 64;
             ok = mbar_wait(&s_full[j & 1], (j >> 1) & 1, w, 9);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            if (!ok && j > 0) break;   // the first turn has a barrier of all score warps
             tc_fence_after();
             uint32_t x[2][32];
             F2 pr[32];
@@ -317,6 +291,35 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             for (int e = 0; e < 32; ++e) {
                 const float2 q = parts(fma2(pair(x, e), sl2, lse22));
                 pr[e] = f2(ex2(q.x), ex2(q.y));
+            }
+            if (j == 0) {
+                // delta of the tile's rows: needed from here on
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(do_full, 0, w, 14) && mbar_wait(o_full, 0, w, 16));
+                // DP / 8 lanes a row, 8 features a lane
+                constexpr int kLanes = DP / 8, kRows = 256 / kLanes, kSteps = 128 / kRows;
+                const int sub = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const int dr = k * kRows + first;
+                    const uint32_t at_ = (sub >> 3) * 16384 + dr * 128 + (((sub & 7) ^ (dr & 7)) << 4);
+                    const uint4 a = lds128(smem_u32(sO) + at_), b = lds128(smem_u32(sDO) + at_);
+                    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+                        sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+                    }
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    if (sub == 0) sDelta[dr] = sum;
+                }
+                mbar_arrive(o_read);
+                score_sync();
+                if (!ok) break;
+                const float delta = sDelta[r];
+                if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
+                delta2 = f2(-delta, -delta);
             }
             ok = mbar_wait(dp_full, j & 1, w, 10);
             ok = __all_sync(0xFFFFFFFFu, ok);
