@@ -421,7 +421,8 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     uint64_t* p_full = dp_full + 1;
     uint64_t* ds_full = p_full + 1;
     uint64_t* out_full = ds_full + 1;
-    uint64_t* drain = out_full + 1;
+    uint64_t* stat_full = out_full + 1;    // the next tile's statistics are in shared memory
+    uint64_t* drain = stat_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -482,6 +483,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             mbar_init(p_full, 256);
             mbar_init(ds_full, 256);
             mbar_init(out_full, 1);
+            mbar_init(stat_full, 256);
             mbar_init(drain, 1);
             abort_flag = 0;
             fence_barrier_init();
@@ -633,19 +635,17 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
                       (sq.kl + kAttnTile - 1) / kAttnTile, item, sh.items, threadIdx.x);
         bool ok = true;
-        float next = n > 0 ? fetch(0) : 0.f;
+        // statistics of tile t in buffer t & 1: tile 0's now, each later one's in the turn before
+        sStat[g * 128 + ct] = n > 0 ? fetch(0) : 0.f;
+        mbar_arrive(stat_full);
+        float next = n > 0 ? fetch(1) : 0.f;
         for (int t = 0; t < n; ++t) {
             float* stat = sStat + (t & 1) * 256;
-            stat[g * 128 + ct] = next;
-            score_sync();
-            next = fetch(t + 1);
             const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const uint32_t st = smem_u32(stat) + g * 256;    // this group's 64 columns
             ok = mbar_wait(s_full, t & 1, w, 12);
-            // after a wait that gave up the loop runs on (each later wait returns at once): the barrier above counts
-            // all 256 threads
-            if (!ok) abort_flag = 1;
-            __syncwarp();
+            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(stat_full, t & 1, w, 15));
+            if (!ok) break;
             tc_fence_after();
             uint32_t v[2][32], x[2][32];
             ld64(ts, v);
@@ -685,9 +685,13 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(p_full);
-            ok = mbar_wait(dp_full, t & 1, w, 13);
-            if (!ok) abort_flag = 1;
-            __syncwarp();
+            // the other buffer is free once every warp is through with the tile before
+            ok = t == 0 || mbar_wait(ds_full, (t - 1) & 1, w, 16);
+            sStat[((t + 1) & 1) * 256 + g * 128 + ct] = next;
+            mbar_arrive(stat_full);
+            next = fetch(t + 2);
+            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(dp_full, t & 1, w, 13));
+            if (!ok) break;
             tc_fence_after();
             ld64(tdp, x);
 #pragma unroll
@@ -711,8 +715,6 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             tc_fence_before();
             mbar_arrive(ds_full);
         }
-        ok = *static_cast<volatile int*>(&abort_flag) == 0;
-        ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok && n > 0) {
             ok = mbar_wait(out_full, 0, w, 14);
             ok = __all_sync(0xFFFFFFFFu, ok);
