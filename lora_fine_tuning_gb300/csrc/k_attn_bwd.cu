@@ -621,22 +621,23 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         const float sl = sh.scale_log2;
         const float* src = g == 0 ? p.lse : p.delta; // group 0 fetches lse, group 1 delta
         const F2 sl2 = f2(sl, sl);
-        // one tile ahead: -lse in the exponent's units (a row that is not there, or sees no key: -inf, P = 0), -delta
+        // two tiles ahead: lse (a row that is not there, or sees no key: +inf, P = 0) or delta
         const auto fetch = [&](int t) -> float {
             const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
             const int tok = i * tpt + (ct >> sh.hp_log2);
             const int head = kvh * sh.group + (pack << sh.hp_log2) + (ct & (sh.hp - 1));
             const bool there = t < n && tok < sq.ql && tok + off >= 0;
-            if (!there) return g == 0 ? neg_inf() : 0.f;
-            const float x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
-            return g == 0 ? x * -kLog2e : -x;
+            float x = g == 0 ? -neg_inf() : 0.f;
+            if (there) x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
+            return x;
         };
+        const float unit = g == 0 ? -kLog2e : -1.f;   // applied when it is stored: the load is not waited for before
         if (sq.gap + sh.lead + sh.trail > 0)
             fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
                       (sq.kl + kAttnTile - 1) / kAttnTile, item, sh.items, threadIdx.x);
         bool ok = true;
         // statistics of tile t in buffer t & 1: tile 0's now, each later one's in the turn before
-        sStat[g * 128 + ct] = n > 0 ? fetch(0) : 0.f;
+        sStat[g * 128 + ct] = n > 0 ? fetch(0) * unit : 0.f;
         mbar_arrive(stat_full);
         float next = n > 0 ? fetch(1) : 0.f;
         for (int t = 0; t < n; ++t) {
@@ -687,7 +688,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             mbar_arrive(p_full);
             // the other buffer is free once every warp is through with the tile before
             ok = t == 0 || mbar_wait(ds_full, (t - 1) & 1, w, 16);
-            sStat[((t + 1) & 1) * 256 + g * 128 + ct] = next;
+            sStat[((t + 1) & 1) * 256 + g * 128 + ct] = next * unit;
             mbar_arrive(stat_full);
             next = fetch(t + 2);
             ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(dp_full, t & 1, w, 13));
