@@ -282,8 +282,9 @@ lora_status lora_fwd_static_scratch(const lora_bf16* X, const lora_bf16* W, cons
  *  - head_dim is a multiple of 8 up to 128, q_heads <= 1024 and a multiple of kv_heads, at most 262144 rows.
  *  - seqs is a HOST array, read before the call returns: q_start and k_start do not decrease and no two sequences
  *    share a row (LORA_ETABLE).  Rows of no sequence are never read; they get O = 0, lse = -inf, dQ = dK = dV = 0.
- *  - A sequence's results depend on its own rows only, whatever lies beside it.  Within a sequence a K, V or dO that
- *    is infinite or NaN may reach rows that do not see it.
+ *  - A sequence's results depend on its own rows only, whatever lies beside it (to fp32 rounding: how the sums are
+ *    grouped follows the lengths of the whole batch).  Within a sequence a K, V or dO that is infinite or NaN may reach
+ *    rows that do not see it.
  *  - P and dS are rounded to bf16 for their products with V, K, Q and dO; everything else is fp32 until the outputs.
  *    Every sum has a fixed order: results are bit-identical from call to call in both reduction modes.
  *  - workspace: attn_workspace_size() bytes, 256-byte aligned, not shared by calls that may overlap.  Its first 256

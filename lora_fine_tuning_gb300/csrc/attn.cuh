@@ -35,14 +35,14 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// One 128 x 128 product over DP features, both operands K-major 128-row tiles of 64-feature boxes.  Every K step is
+// One product of 128 x kBRows values over DP features, both operands K-major tiles of 64-feature boxes.  Every K step is
 // issued, past the head's width too (the tiles hold zeros there): no branch stands between the steps.
-template <int DP>
+template <int DP, int kBRows = 128>
 __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
 #pragma unroll
     for (int ks = 0; ks < DP / 16; ++ks) {
         const uint64_t h = static_cast<uint64_t>(ks >> 2), kk = static_cast<uint64_t>(ks & 3);
-        umma_bf16(d_tmem, a + h * 1024u + kk * 2u, b + h * 1024u + kk * 2u, idesc, ks != 0 ? 1u : 0u);
+        umma_bf16(d_tmem, a + h * 1024u + kk * 2u, b + h * (kBRows * 8u) + kk * 2u, idesc, ks != 0 ? 1u : 0u);
     }
 }
 
@@ -106,15 +106,16 @@ __device__ __forceinline__ AttnSeq find_seq(const AttnSeqs<N>& t, int n, int ite
     return t.s[max(k, 0)];
 }
 
-// Zeroes rows [from, 128) of a swizzled tile of `boxes` 64-feature boxes of 128 rows x 128 bytes, by one warp (rows
+// Zeroes rows [from, R) of a swizzled tile of `boxes` 64-feature boxes of R rows x 128 bytes, by one warp (rows
 // past the end of a sequence belong to another sequence or to nobody: a probability of zero times what lies there
 // would still be a NaN when it is infinite or NaN).  The caller orders it before the MMAs that read the tile.
+template <int R = 128>
 __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int boxes, int from) {
     const uint32_t base = smem_u32(tile);
-    const int n = (128 - from) * 8;
+    const int n = (R - from) * 8;
     for (int b = 0; b < boxes; ++b)
         for (int i = lane_id(); i < n; i += 32)
-            sts128(base + b * 16384 + from * 128 + i * 16, make_uint4(0u, 0u, 0u, 0u));
+            sts128(base + b * (R * 128) + from * 128 + i * 16, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
 }
 

@@ -71,6 +71,7 @@ struct AttnBwdParams {
     AttnShape sh;
     const float* lse;        // rows x hq
     float* delta;            // rows x hq, from the first pass to the second
+    AttnMat O;
     AttnMat dQ, dK, dV;
     DevCtl ctl;
 };
@@ -96,7 +97,8 @@ cudaError_t attn_bwd_configure();
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 // Joins the partial results of the split sequences (n of them, the first of the table).
 cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream);
-cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+// short_keys: key tiles of 64, which mapK and mapV then describe.
+cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, bool short_keys, cudaStream_t stream);
 cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
 cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream);
 

@@ -118,6 +118,19 @@ void order_by_keys(Prepared& c) {
 
 int key_tiles(const AttnSeq& q) { return static_cast<int>(tiles_of(q.kl, kAttnTile)); }
 
+// Whether the query tiles see at most 512 keys in the mean: the dQ pass then has key tiles of 64 (k_attn_bwd.cu: the two
+// forms meet there).
+bool few_keys(const Prepared& c, int tokens) {
+    int64_t tiles = 0, keys = 0;
+    for (int i = 0; i < c.n; ++i) {
+        const AttnSeq& q = c.order.s[i];
+        const int64_t t = tiles_of(q.ql, tokens);
+        tiles += t;
+        keys += t * std::max(q.kl - q.ql / 2, q.kl / 2);
+    }
+    return keys <= 512 * tiles;
+}
+
 // Splits the keys of sequences whose rows fill one query tile at most (`tokens` of them), where their long ranges would
 // keep a few SMs busy long after the others: into pieces of equal length, of at most what an SM gets of the call's work
 // (but of no fewer than eight key tiles: a piece costs the start and end of an item, about as much as six).  They come
@@ -286,12 +299,11 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     const lora_bf16* any = no_q ? K : Q;
     if (!make_map_heads(&p.mapQ, no_q ? any : Q, a.head_dim, a.q_heads, qr, a.q.head, a.q.row, c.sh.hp, tokens) ||
         !make_map_heads(&p.mapO, no_q ? any : O, a.head_dim, a.q_heads, qr, a.o.head, a.o.row, c.sh.hp, tokens) ||
-        !make_map_heads(&p.mapDO, no_q ? any : dO, a.head_dim, a.q_heads, qr, a.d_o.head, a.d_o.row, c.sh.hp, tokens) ||
-        !make_map_heads(&p.mapK, no_k ? any : K, a.head_dim, a.kv_heads, kr, a.k.head, a.k.row, 1, kAttnTile) ||
-        !make_map_heads(&p.mapV, no_k ? any : V, a.head_dim, a.kv_heads, kr, a.v.head, a.v.row, 1, kAttnTile))
+        !make_map_heads(&p.mapDO, no_q ? any : dO, a.head_dim, a.q_heads, qr, a.d_o.head, a.d_o.row, c.sh.hp, tokens))
         return LORA_ECUDA;
     p.lse = lse;
     p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+    p.O = mat(O, a.o);
     p.dQ = mat(dQ, a.d_q);
     p.dK = mk;
     p.dV = mv;
@@ -301,7 +313,14 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
         if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
     }
     p.sh = c.sh;
-    if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, s); }));
+    const bool short_keys = few_keys(c, tokens);
+    const auto key_maps = [&](int rows) {
+        return make_map_heads(&p.mapK, no_k ? any : K, a.head_dim, a.kv_heads, kr, a.k.head, a.k.row, 1, rows) &&
+               make_map_heads(&p.mapV, no_k ? any : V, a.head_dim, a.kv_heads, kr, a.v.head, a.v.row, 1, rows);
+    };
+    if (!key_maps(short_keys ? kAttnTile / 2 : kAttnTile)) return LORA_ECUDA;
+    if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, short_keys, s); }));
+    if (short_keys && !key_maps(kAttnTile)) return LORA_ECUDA;
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }))) return st;
     if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, [](const AttnSeq& q) { return q.k0; }, [](const AttnSeq& q) { return q.kl; })) {
         if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;

@@ -3,10 +3,15 @@
 //   P = exp(scale Q K^T - lse),  delta_i = sum_d dO_id O_id,  dP = dO V^T,  dS = P (dP - delta)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,   dK and dV summed over the query heads of a group
 //
-// Two passes: dQ, a CTA a 128-row query tile over its keys (delta on the way); dK and dV, a CTA a 128-key tile over the query
-// tiles of all heads of its group.  Each gradient element is summed by one CTA in a fixed order, in TMEM in fp32:
+// Two passes: dQ, a CTA a 128-row query tile over its keys (delta on the way); dK and dV, a CTA a 128-key tile over the
+// query tiles of all heads of its group.  Each gradient element is summed by one CTA in a fixed order, in TMEM in fp32:
 // the results are the same from call to call, and no partial sum goes through memory.  The price is that S and dP are
-// formed twice (seven products instead of five).
+// formed twice (seven products instead of five).  dS and, for dV, P are rounded to bf16, the tensor cores' operand type;
+// dS comes from P and dP in fp32.
+//
+// Bound by the tensor cores on long sequences: four of 4096 tokens, 64/8 heads of 128, take 1095 to 1130 us for dQ (three
+// products, 880 us at the cuBLAS rate; a turn of 128 keys takes 1645 cycles, its products 1536) and 1274 to 1310 us for
+// dK and dV (four products, 1173 us).  On short ones by the start of a CTA, whose first tiles of 32 KB arrive together.
 #include "attn.cuh"
 #include "kernels.h"
 
@@ -28,12 +33,58 @@ __device__ __forceinline__ void ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
     tmem_ld_wait(v);
 }
 
-// Barrier among the 256 threads of the score warps.
-__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Barrier among the T threads of the score warps.
+template <int T>
+__device__ __forceinline__ void score_sync() { asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory"); }
 
 // Columns 2 e and 2 e + 1 of what ld64 read.
 __device__ __forceinline__ F2 pair(const uint32_t (&v)[2][32], int e) {
     return f2(__uint_as_float(v[e >> 4][2 * (e & 15)]), __uint_as_float(v[e >> 4][2 * (e & 15) + 1]));
+}
+
+// Dot product of eight bf16 pairs; sum over groups of L lanes.
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
+        sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
+    }
+    return sum;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
+
+// x = P (x - delta) for a row's 64 columns; zeros after column `last`; to TMEM in bf16, over the first 32 columns.
+__device__ __forceinline__ void gradient_of_scores(uint32_t (&x)[2][32], const F2 (&pr)[32], F2 minus_delta) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        const float2 q = parts(mul(pr[e], add2(pair(x, e), minus_delta)));
+        x[e >> 4][2 * (e & 15)] = __float_as_uint(q.x);
+        x[e >> 4][2 * (e & 15) + 1] = __float_as_uint(q.y);
+    }
+}
+__device__ __forceinline__ void mask_after(uint32_t (&x)[2][32], int last) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (c * 32 + e > last) x[c][e] = 0u;
+}
+__device__ __forceinline__ void store_scores(uint32_t taddr, const uint32_t (&x)[2][32]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[e] = pack_bf16x2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
+        tmem_st16(taddr + c * 16, o);
+    }
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -303,19 +354,11 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
                     const int dr = k * kRows + first;
                     const uint32_t at_ = (sub >> 3) * 16384 + dr * 128 + (((sub & 7) ^ (dr & 7)) << 4);
                     const uint4 a = lds128(smem_u32(sO) + at_), b = lds128(smem_u32(sDO) + at_);
-                    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-                    float sum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), sum);
-                        sum = fmaf(__uint_as_float(x[e] & 0xFFFF0000u), __uint_as_float(y[e] & 0xFFFF0000u), sum);
-                    }
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    const float sum = lanes_sum<kLanes>(dot8(a, b));
                     if (sub == 0) sDelta[dr] = sum;
                 }
                 mbar_arrive(o_read);
-                score_sync();
+                score_sync<256>();
                 if (!ok) break;
                 const float delta = sDelta[r];
                 if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
@@ -328,28 +371,9 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             ld64(t_dp + lanes + g * 64, x);
             tc_fence_before();
             mbar_arrive(dp_read);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const float2 q = parts(mul(pr[e], add2(pair(x, e), delta2)));
-                x[e >> 4][2 * (e & 15)] = __float_as_uint(q.x);
-                x[e >> 4][2 * (e & 15) + 1] = __float_as_uint(q.y);
-            }
-            if ((j + 1) * kAttnTile - 1 > tok0 + off) {
-                const int lim = limit - j * kAttnTile - g * 64;
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e > lim) x[c][e] = 0u;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t o[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    o[e] = pack_bf16x2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
-                tmem_st16(ts + c * 16, o);
-            }
+            gradient_of_scores(x, pr, delta2);
+            if ((j + 1) * kAttnTile - 1 > tok0 + off) mask_after(x, limit - j * kAttnTile - g * 64);
+            store_scores(ts, x);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(ds_full);
@@ -372,6 +396,321 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// dQ over few keys
+// ---------------------------------------------------------------------------------------------------------------
+
+// The same pass with key tiles of 64, four score warps and half the shared memory and TMEM: two CTAs an SM, one of which
+// works while the other starts (its first tiles take 5000 cycles) or ends.  A product of 64 columns with both operands
+// in shared memory costs 3/4 of one of 128, so long ranges are slower.  us for 8192 tokens with 32/8 heads of 128 in
+// samples of 77, 128, 256, 450, 1024, 2048, 4096 tokens: 86, 78, 83, 100, 135, 204, 343 against 119, 100, 100, 115, 136,
+// 186, 276 with tiles of 128; 32 heads of 64 the same way (58 against 83 at 128, 256 against 233 at 4096).
+constexpr int kShortKeys = 64;
+constexpr int kShortThreads = 192;   // warps 0-3: scores and gradients of scores; warp 4: TMA; warp 5: MMAs
+
+template <int DP>
+struct CfgShort {
+    static constexpr int kBoxes = DP / 64;
+    static constexpr uint32_t kTileBytes = kBoxes * 16384u, kKeyBytes = kTileBytes / 2;
+    static constexpr int kStagesK = 2;
+    static constexpr size_t kSmem = 2 * static_cast<size_t>(kTileBytes) + (kStagesK + 1) * static_cast<size_t>(kKeyBytes) + 512 + 256;
+};
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kShortThreads, 2)
+attn_dq_short_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    const int item = attn_item();
+    if (item >= p.sh.items) return;   // the last plane of the grid
+    using C = CfgShort<DP>;
+    constexpr int SK = C::kStagesK, KT = kShortKeys;
+    // no other shared memory: the dynamic part starts on a swizzle atom, and there is no room to move it
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw;
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0 && p.ctl.status) atomicCAS(p.ctl.status, 0, (kKAttnDq << 8) | 0xFF);
+        return;
+    }
+    uint8_t* sQ = smem;
+    uint8_t* sDO = sQ + C::kTileBytes;
+    uint8_t* sK = sDO + C::kTileBytes;
+    uint8_t* sV = sK + SK * C::kKeyBytes;
+    float* sDelta = reinterpret_cast<float*>(sV + C::kKeyBytes);   // 128
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sDelta + 128);
+    uint64_t* q_full = bars;
+    uint64_t* do_full = q_full + 1;
+    uint64_t* k_full = do_full + 1;        // SK each
+    uint64_t* k_empty = k_full + SK;
+    uint64_t* v_full = k_empty + SK;
+    uint64_t* v_empty = v_full + 1;
+    uint64_t* s_full = v_empty + 1;
+    uint64_t* dp_full = s_full + 1;
+    uint64_t* ds_full = dp_full + 1;
+    uint64_t* dq_full = ds_full + 1;
+    uint64_t* k_fixed = dq_full + 1;
+    uint64_t* dp_read = k_fixed + 1;
+    uint64_t* drain = dp_read + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const AttnShape& sh = p.sh;
+    const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
+    const int tpt = kAttnTile >> sh.hp_log2;
+    const int tiles = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
+    const int local = item - sq.item0;
+    const int tok0 = (tiles - 1 - local) * tpt;
+    const int head0 = blockIdx.x << sh.hp_log2;
+    const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
+    const int off = sq.kl - sq.ql;
+    const int last = min(tok0 + tpt, sq.ql) - 1 + off;            // last key the tile sees
+    const int n = last >= 0 ? last / KT + 1 : 0;
+    const bool tail = n * KT > sq.kl;
+
+    const auto load_k = [&](int j) {
+        const int s = j % SK;
+        mbar_arrive_expect_tx(&k_full[s], C::kKeyBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sK + s * C::kKeyBytes + b * 8192, &p.mapK, &k_full[s], b * 64, kvh, sq.k0 + j * KT);
+    };
+    const auto load_v = [&](int j) {
+        mbar_arrive_expect_tx(v_full, C::kKeyBytes);
+        for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(sV + b * 8192, &p.mapV, v_full, b * 64, kvh, sq.k0 + j * KT);
+    };
+    // O, of which delta needs the rows: DP / 8 lanes a row, 8 features a lane
+    constexpr int kLanes = DP / 8, kRows = 128 / kLanes, kSteps = 128 / kRows;
+    const int dsub = threadIdx.x % kLanes, dfirst = threadIdx.x / kLanes;
+    uint4 o_rows[kSteps];
+    if (warp == 4) {
+        if (lane == 0) {
+            tma_prefetch_desc(&p.mapQ);
+            tma_prefetch_desc(&p.mapK);
+            tma_prefetch_desc(&p.mapV);
+            tma_prefetch_desc(&p.mapDO);
+            mbar_init(q_full, 1);
+            mbar_init(do_full, 1);
+            for (int s = 0; s < SK; ++s) {
+                mbar_init(&k_full[s], 1);
+                mbar_init(&k_empty[s], 1);
+            }
+            mbar_init(v_full, 1);
+            mbar_init(v_empty, 1);
+            mbar_init(s_full, 1);
+            mbar_init(dp_full, 1);
+            mbar_init(ds_full, 128);
+            mbar_init(dq_full, 1);
+            mbar_init(k_fixed, 1);
+            mbar_init(dp_read, 128);
+            mbar_init(drain, 1);
+            abort_flag = 0;
+            fence_barrier_init();
+            pdl_wait();
+            if (n > 0) {
+                mbar_arrive_expect_tx(q_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sQ + b * 16384, &p.mapQ, q_full, b * 64, head0, sq.q0 + tok0);
+                load_k(0);
+                mbar_arrive_expect_tx(do_full, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                    tma_load_3d(sDO + b * 16384, &p.mapDO, do_full, b * 64, head0, sq.q0 + tok0);
+                load_v(0);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        tmem_alloc(tmem_slot, 256);
+        tmem_relinquish();
+    } else if (n > 0) {
+        pdl_wait();
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const int dr = k * kRows + dfirst, dt = tok0 + (dr >> sh.hp_log2), dh = head0 + (dr & (sh.hp - 1));
+            o_rows[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (dt < sq.ql && dsub * 8 < sh.d)
+                o_rows[k] = *reinterpret_cast<const uint4*>(p.O.p + (static_cast<int64_t>(sq.q0) + dt) * p.O.row +
+                                                            dh * p.O.head + dsub * 8);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    // two buffers of 64 columns: turn j has S(j) (then dS(j)) in buffer j & 1 and dP(j) in the other
+    const uint32_t t_dq = tmem + 128;
+    const WaitCtx w{&abort_flag, p.ctl.status, p.ctl.wait_ns, kKAttnDq << 8};
+
+    if (warp == 4) {
+        bool ok = true;
+        const int ahead = min(1, n);
+        int issued = ahead, issued_v = ahead;
+        for (int j = ahead; j < n; ++j) {
+            if (lane == 0) {
+                ok = mbar_wait(&k_empty[j % SK], ((j / SK) & 1) ^ 1u, w, 1);
+                if (ok) {
+                    load_k(j);
+                    ++issued;
+                    ok = mbar_wait(v_empty, (j & 1) ^ 1u, w, 2);
+                    if (ok) {
+                        load_v(j);
+                        ++issued_v;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) break;
+        }
+        if (ok && tail && n > 0) {
+            const int s = (n - 1) % SK;
+            ok = mbar_wait(&k_full[s], ((n - 1) / SK) & 1, w, 3);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+                zero_tile_rows<KT>(sK + s * C::kKeyBytes, C::kBoxes, sq.kl - (n - 1) * KT);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(k_fixed);
+            }
+        }
+        if (lane == 0) {
+            // every copy lands before the CTA exits, also when another warp gave up
+            if (n > 0) {
+                mbar_wait_drain(q_full, 0, p.ctl.wait_ns);
+                mbar_wait_drain(do_full, 0, p.ctl.wait_ns);
+            }
+            for (int j = max(0, issued - SK); j < issued; ++j) mbar_wait_drain(&k_full[j % SK], (j / SK) & 1, p.ctl.wait_ns);
+            if (issued_v > 0) mbar_wait_drain(v_full, (issued_v - 1) & 1, p.ctl.wait_ns);
+        }
+    } else if (warp == 5) {
+        if (elect_one()) {
+            const uint32_t idesc_s = make_idesc_bf16(128, KT, false, false);
+            const uint32_t idesc_q = make_idesc_bf16(128, sh.d16, false, true);
+            const uint64_t qd = make_smem_desc(smem_u32(sQ), 16, 1024, kSw128);
+            const uint64_t dod = make_smem_desc(smem_u32(sDO), 16, 1024, kSw128);
+            const uint64_t kd = make_smem_desc(smem_u32(sK), 16, 1024, kSw128);
+            const uint64_t kmn = make_smem_desc(smem_u32(sK), 8192, 1024, kSw128);
+            const uint64_t vd = make_smem_desc(smem_u32(sV), 16, 1024, kSw128);
+            const auto k_ready = [&](int j) {
+                return mbar_wait(&k_full[j % SK], (j / SK) & 1, w, 5) && (!tail || j != n - 1 || mbar_wait(k_fixed, 0, w, 6));
+            };
+            const auto at = [&](int j) { return tmem + (j & 1) * 64; };
+            bool ok = n > 0 && mbar_wait(q_full, 0, w, 4) && k_ready(0);
+            if (ok) {
+                tc_fence_after();
+                mma_rows<DP, KT>(at(0), qd, kd, idesc_s);
+                umma_commit(s_full);
+                ok = mbar_wait(do_full, 0, w, 13) && mbar_wait(v_full, 0, w, 7);
+            }
+            if (ok) {
+                tc_fence_after();
+                mma_rows<DP, KT>(at(1), dod, vd, idesc_s);
+                umma_commit(dp_full);
+                umma_commit(v_empty);
+            }
+            // turn j: S(j + 1) as soon as dP(j) has been read from its buffer, dQ += dS(j) K(j), then dP(j + 1) over dS(j)
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) {
+                    if (!k_ready(j + 1) || !mbar_wait(dp_read, j & 1, w, 12)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP, KT>(at(j + 1), qd, kd + static_cast<uint64_t>((j + 1) % SK) * (C::kKeyBytes >> 4), idesc_s);
+                    umma_commit(s_full);
+                }
+                if (!mbar_wait(ds_full, j & 1, w, 8)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t b = kmn + static_cast<uint64_t>(j % SK) * (C::kKeyBytes >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    umma_bf16_ta(t_dq, at(j) + ks * 8, b + ks * 128u, idesc_q, (j != 0 || ks != 0) ? 1u : 0u);
+                umma_commit(&k_empty[j % SK]);
+                if (j + 1 < n) {
+                    if (!mbar_wait(v_full, (j + 1) & 1, w, 7)) { ok = false; break; }
+                    tc_fence_after();
+                    mma_rows<DP, KT>(at(j), dod, vd, idesc_s);
+                    umma_commit(dp_full);
+                    umma_commit(v_empty);
+                }
+            }
+            if (ok) umma_commit(dq_full);
+            umma_commit(drain);
+            mbar_wait_drain(drain, 0, p.ctl.wait_ns);
+        }
+        __syncwarp();
+    } else {
+        const int r = warp * 32 + lane;
+        const int tok = tok0 + (r >> sh.hp_log2);
+        const int head = head0 + (r & (sh.hp - 1));
+        const bool row_ok = tok < sq.ql;
+        const int limit = tok + off;
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const float sl = sh.scale_log2;
+        const int64_t at = (static_cast<int64_t>(sq.q0) + tok) * sh.hq + head;
+        // a row that is not there, or sees no key: every score is masked below
+        const float lse2 = row_ok && limit >= 0 ? p.lse[at] * kLog2e : 0.f;
+        // under the first loads
+        if (sq.gap + sh.lead + sh.trail > 0)
+            fill_rows<8>(p.dQ, nullptr, nullptr, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
+                         local, tiles, item, sh.items, threadIdx.x);
+        bool ok = true;
+        float delta = 0.f;
+        if (n > 0) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(do_full, 0, w, 14));
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const int dr = k * kRows + dfirst;
+                const uint4 b = lds128(smem_u32(sDO) + (dsub >> 3) * 16384 + dr * 128 + (((dsub & 7) ^ (dr & 7)) << 4));
+                const float sum = lanes_sum<kLanes>(dot8(o_rows[k], b));
+                if (dsub == 0) sDelta[dr] = sum;
+            }
+            score_sync<128>();
+            delta = sDelta[r];
+            if (row_ok) p.delta[at] = delta;         // for the next pass
+        }
+        const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2), delta2 = f2(-delta, -delta);
+        for (int j = 0; ok && j < n; ++j) {
+            const uint32_t ts = tmem + (j & 1) * 64 + lanes, tdp = tmem + ((j + 1) & 1) * 64 + lanes;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full, j & 1, w, 9));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[2][32];
+            F2 pr[32];
+            ld64(ts, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const float2 q = parts(fma2(pair(x, e), sl2, lse22));
+                pr[e] = f2(ex2(q.x), ex2(q.y));
+            }
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(dp_full, j & 1, w, 10));
+            if (!ok) break;
+            tc_fence_after();
+            ld64(tdp, x);
+            tc_fence_before();
+            mbar_arrive(dp_read);
+            gradient_of_scores(x, pr, delta2);
+            if ((j + 1) * KT - 1 > tok0 + off) mask_after(x, limit - j * KT);
+            store_scores(ts, x);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(ds_full);
+        }
+        if (ok && n > 0) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(dq_full, 0, w, 11));
+            tc_fence_after();
+        }
+        if (ok)
+            // through Q's shared memory: all products are done
+            store_tile(p.dQ.p + (static_cast<int64_t>(sq.q0) + tok0) * p.dQ.row + static_cast<int64_t>(head0) * p.dQ.head,
+                       p.dQ.row, p.dQ.head, sh.hp_log2, (sq.ql - tok0) << sh.hp_log2, sh.d, sh.d16, smem_u32(sQ),
+                       t_dq + lanes, warp, n > 0, sh.scale);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
     }
 }
 
@@ -739,6 +1078,12 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
 }
 
 template <int DP, int N>
+cudaError_t run_dq_short(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+    return launch_pdl(attn_dq_short_kernel<DP, N>, attn_grid(p.sh.packs, p.sh.items), dim3(kShortThreads), CfgShort<DP>::kSmem,
+                      stream, p, reinterpret_cast<const AttnSeqs<N>&>(seqs));
+}
+
+template <int DP, int N>
 cudaError_t run_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
     return launch_pdl(attn_dq_kernel<DP, N>, attn_grid(p.sh.packs, p.sh.items), dim3(kThreads), CfgQ<DP>::kSmem, stream, p,
                       reinterpret_cast<const AttnSeqs<N>&>(seqs));
@@ -752,8 +1097,11 @@ cudaError_t run_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs,
 
 template <int DP, int N>
 cudaError_t configure() {
-    const cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(CfgQ<DP>::kSmem));
+    cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(CfgQ<DP>::kSmem));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_dq_short_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(CfgShort<DP>::kSmem));
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(attn_dkdv_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(CfgKV<DP>::kSmem));
@@ -769,8 +1117,12 @@ cudaError_t attn_bwd_configure() {
     return e;
 }
 
-cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream) {
+cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, bool short_keys, cudaStream_t stream) {
     const bool few = p.sh.n_seqs <= kAttnFewSeqs;
+    if (short_keys) {
+        if (p.sh.d <= 64) return few ? run_dq_short<64, kAttnFewSeqs>(p, seqs, stream) : run_dq_short<64, kAttnMaxSeqs>(p, seqs, stream);
+        return few ? run_dq_short<128, kAttnFewSeqs>(p, seqs, stream) : run_dq_short<128, kAttnMaxSeqs>(p, seqs, stream);
+    }
     if (p.sh.d <= 64) return few ? run_dq<64, kAttnFewSeqs>(p, seqs, stream) : run_dq<64, kAttnMaxSeqs>(p, seqs, stream);
     return few ? run_dq<128, kAttnFewSeqs>(p, seqs, stream) : run_dq<128, kAttnMaxSeqs>(p, seqs, stream);
 }

@@ -2,13 +2,19 @@
 //
 //   S = scale Q K^T,  visible keys j <= i + (k_len - q_len),  lse_i = log sum_j exp S_ij,  O = exp(S - lse) V
 //
-// in one pass over the keys with the running maximum and sum of each row.  A CTA works on two 128-row query tiles
-// (tokens x heads of one group, attn.h) that share every K and V tile: while the softmax of one tile runs, the tensor
-// cores work on the other's products.  Warps 0-3 and 4-7: the softmax of tile 0 and 1, a thread one row; warp 8: TMA
-// (K and V tiles of 128 keys through a ring of stages); warp 9: the MMAs.  S (fp32) lives in TMEM, is read by its
-// row's thread, and P goes back in bf16 over S's columns, from where the second product reads it as its A operand.
+// in one pass over the keys with the running maximum and sum of each row.  A CTA works on one 128-row query tile (tokens x
+// heads of one group, attn.h); two CTAs share an SM: while the softmax of one runs, the tensor cores work on the other's
+// products, and its start and end (about 10000 cycles) are covered, too.  Warps 0-3: the softmax, a thread one row; warp 4:
+// TMA (K and V tiles of 128 keys through a ring of stages); warp 5: the MMAs.  S (fp32) lives in TMEM, is read by its
+// row's thread, and P goes back in bf16 (the tensor cores' operand type; the sum is of the values before this rounding)
+// over S's columns, from where the second product reads it as its A operand.
 // The rows of O are rescaled in TMEM only when a row's maximum grew by more than 2^8 since the last rescaling (the
 // statistics keep the older maximum until then: P stays below 2^8, far inside bf16's and fp32's ranges).
+//
+// Bound by the tensor cores and the chain S, softmax, P of two tiles: a turn of both takes 2870 cycles, their products
+// 2048, each tile's softmax 1380.  8192 tokens with 32/8 heads of 128: 351 us (293 at the cuBLAS rate); four sequences of
+// 4096 with 64/8 heads: 760 to 785 (587).  One CTA an SM with two query tiles that share K and V: 357 us, 77 us against
+// 58 for samples of 77 tokens.
 #include "attn.cuh"
 #include "kernels.h"
 

@@ -306,3 +306,45 @@ def test_few_rows_over_many_keys(hq, hkv, d):
     assert off(O2, r[0]) <= TOL and float((lse2 - lse)[torch.isfinite(lse2)].abs().max()) <= LSE_TOL
     again = api.attn_fwd(Q, K, V, seqs)
     assert torch.equal(O, again[0]) and torch.equal(lse, again[1])
+
+
+LONG = 6000   # keys of a few-row sequence that raises the batch's mean: dQ then runs with key tiles of 128
+
+
+@pytest.mark.parametrize("lengths,pad,hq,hkv,d,layout", [
+    ([1, 2, 127, 128, 129], 1, 4, 1, 64, "rows"), ([255, 0, 257, 1], 128, 4, 2, 128, "rows"), ([300], 1, 3, 1, 128, "rows"),
+    ([150, 33], 1, 28, 4, 64, "rows"), ([150, 33], 1, 7, 1, 40, "heads"), ([140, 61], 1, 4, 2, 8, "rows"),
+    ([140, 61], 1, 4, 2, 72, "heads"), ([140, 61], 1, 8, 8, 120, "rows"), ([40, 400], 1, 16, 1, 96, "rows")])
+def test_key_tiles_of_128(lengths, pad, hq, hkv, d, layout):
+    """The shapes of the tests above beside a long range of keys, and past it: both forms of the dQ pass are exact to
+    the same tolerance, and a sequence's gradients do not depend on the form beyond rounding."""
+    short, rows = packed(lengths, pad)
+    seqs = short + [(rows + 1, 8, rows + 2, LONG)]
+    Q, K, V, dO = inputs(rows + 9, rows + 2 + LONG, hq, hkv, d, layout, seed=sum(lengths))
+    got = run(Q, K, V, dO, seqs, None)
+    check(Q, K, V, seqs, d ** -0.5, dO, got)
+    alone = run(Q, K, V, dO, short, None)
+    for a, b in zip(got[2:], alone[2:]):
+        for q0, n, _, _ in short:
+            if n:
+                assert off(a[q0:q0 + n], b[q0:q0 + n].double().cpu()) <= TOL
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_beside_a_long_sequence(bad):
+    """As test_rows_beside_a_sequence_do_not_reach_it, with key tiles of 128."""
+    seqs = [(0, 70, 0, 70), (100, 9, 90, LONG - 5)]
+    Q, K, V, dO = inputs(120, 90 + LONG, 4, 2, 64, seed=2)
+    want = run(Q, K, V, dO, seqs, None)
+    for t, used in ((Q, seqs), (dO, seqs)):
+        mask = torch.ones(t.shape[0], dtype=torch.bool, device="cuda")
+        for q0, n, _, _ in used:
+            mask[q0:q0 + n] = False
+        t[mask] = bad
+    for t in (K, V):
+        mask = torch.ones(t.shape[0], dtype=torch.bool, device="cuda")
+        for _, _, k0, n in seqs:
+            mask[k0:k0 + n] = False
+        t[mask] = bad
+    for a, b in zip(run(Q, K, V, dO, seqs, None), want):
+        assert torch.equal(a, b)
