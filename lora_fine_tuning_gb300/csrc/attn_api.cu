@@ -134,7 +134,7 @@ bool few_keys(const Prepared& c, int tokens) {
 // Splits the keys of sequences whose rows fill one query tile at most (`tokens` of them), where their long ranges would
 // keep a few SMs busy long after the others: into pieces of equal length, of at most what an SM gets of the call's work
 // (but of no fewer than eight key tiles: a piece costs the start and end of an item, about as much as six).  They come
-// first in the table, as the join wants them.  Returns how many they are.  24 continuations of 1 to 22 tokens over prompts of 440 to 12000 keys, 32/8 heads of 128:
+// first in the table, as the join wants them.  Returns how many they are.  24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128:
 // 63 us and 8 us for the join; pieces of half that length 67 and 10, none 121.
 int split_keys(Prepared& c, int tokens, int sms) {
     AttnSeq* const end = c.order.s + c.n;
