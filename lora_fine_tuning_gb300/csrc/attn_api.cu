@@ -132,16 +132,16 @@ bool few_keys(const Prepared& c, int tokens) {
 }
 
 // Splits the keys of sequences whose rows fill one query tile at most (`tokens` of them), where their long ranges would
-// keep a few SMs busy long after the others: into pieces of equal length, of at most what an SM gets of the call's work
-// (but of no fewer than eight key tiles: a piece costs the start and end of an item, about as much as six).  They come
-// first in the table, as the join wants them.  Returns how many they are.  24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128:
-// 63 us and 8 us for the join; pieces of half that length 67 and 10, none 121.
+// keep a few SMs busy long after the others: into pieces of equal length, of at most two thirds of what an SM gets of the
+// call's work, but of no fewer than four key tiles.  They come first in the table, as the join wants them.  Returns how
+// many they are.  24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128: 63 us with the join; pieces
+// of all or half an SM's share 71 and 77, none 121.  One token over 4096 keys: 12 us, with at least eight tiles a piece 14.
 int split_keys(Prepared& c, int tokens, int sms) {
     AttnSeq* const end = c.order.s + c.n;
     int64_t work = 0;
     for (const AttnSeq* q = c.order.s; q != end; ++q)
         work += tiles_of(q->ql, tokens) * key_tiles(*q) * c.sh.packs;
-    const int64_t most = std::max<int64_t>(8, tiles_of(2 * work, 3 * sms));
+    const int64_t most = std::max<int64_t>(4, tiles_of(2 * work, 3 * sms));
     int64_t slots = 0;
     for (AttnSeq* q = c.order.s; q != end; ++q) {
         if (q->ql == 0 || q->ql > tokens || key_tiles(*q) <= most) continue;
