@@ -242,3 +242,25 @@ def test_refusals():
     before = [x.clone() for x in (t.param, t.m, t.v)]
     refused(1, [t, api.AdamWTensor(f.param, f.grad, f.m, f.v, master=torch.zeros(100, device="cuda"))])
     assert all(torch.equal(a, b) for a, b in zip(before, (t.param, t.m, t.v)))   # nothing of a refused call runs
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(bits):
+    """A tensor of more than 2^31 values: its ends are updated as the same values in a small tensor."""
+    n, k = 2 ** 31 + 4096 + 17, 4096 + 17
+    g = torch.Generator(device="cuda").manual_seed(4)
+    small = [api.adamw_tensor(torch.randn(k, device="cuda", generator=g).bfloat16(),
+                              torch.randn(k, device="cuda", generator=g).bfloat16(), bits=bits) for _ in range(2)]
+    p, gr = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for x, name in ((p, "param"), (gr, "grad")):
+        x[:k], x[n - k:] = getattr(small[0], name), getattr(small[1], name)
+    big = api.adamw_tensor(p, gr, bits=bits)
+    assert (n - k) % 256 == 0
+    for step in (1, 2):
+        api.adamw_step([big], lr=1e-3, step=step)
+        api.adamw_step(small, lr=1e-3, step=step)
+    for name in ("param", "m", "v"):
+        x = getattr(big, name)
+        # the first block after the small tensor's end shares its scale with zeros: the last whole block is compared
+        assert torch.equal(x[:4096], getattr(small[0], name)[:4096]) and torch.equal(x[n - k:], getattr(small[1], name))
+        assert not x[k:n - k].count_nonzero()

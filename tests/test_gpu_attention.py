@@ -348,3 +348,35 @@ def test_rows_beside_a_long_sequence(bad):
         t[mask] = bad
     for a, b in zip(run(Q, K, V, dO, seqs, None), want):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose element offsets pass 2^31 and 2^32: the last rows of long buffers with wide rows, every operand and
+    output a slice.  The same rows copied together give bit-identical results."""
+    rows, wide, hq, hkv, d = 140000, 32768, 2, 1, 64
+    assert (rows - 1) * wide > 2 ** 32
+    n, k0 = 300, rows - 1000
+    seqs = [(0, 40, 0, 40), (rows - n, n, k0, 1000)]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    buf = torch.empty(rows, wide, dtype=torch.bfloat16, device="cuda")   # 9.2 GB, only the sequences' rows are filled
+    at = 0
+
+    def part(heads):
+        nonlocal at
+        x = buf[:, at:at + heads * d].unflatten(1, (heads, d))
+        at += heads * d
+        return x
+
+    Q, K, V, dO, O, dQ, dK, dV = (part(h) for h in (hq, hkv, hkv, hq, hq, hq, hkv, hkv))
+    for x in (Q, K, V, dO):
+        for a, b in ((0, 40), (k0, rows)):
+            x[a:b] = torch.randn(x[a:b].shape, device="cuda", generator=g).bfloat16()
+    _, lse = api.attn_fwd(Q, K, V, seqs, O=O)
+    api.attn_bwd(dO, Q, K, V, O, lse, seqs, dQ=dQ, dK=dK, dV=dV)
+    q, do = (torch.cat([x[:40], x[rows - n:]]) for x in (Q, dO))
+    k, v = (torch.cat([x[:40], x[k0:]]) for x in (K, V))
+    near = [(0, 40, 0, 40), (40, n, 40, 1000)]
+    want = run(q, k, v, do, near, None)
+    for got, ref, m in ((O, want[0], n), (dQ, want[2], n), (dK, want[3], 1000), (dV, want[4], 1000), (lse, want[1], n)):
+        assert torch.equal(got[:40], ref[:40]) and torch.equal(got[rows - m:], ref[40:])
+    assert not O[40:rows - n].count_nonzero() and not dK[40:k0].count_nonzero()

@@ -283,3 +283,31 @@ def test_refusals():
         api.policy_loss(z, y, noise[0, :5], noise[1])
     with pytest.raises(ValueError):
         api.pref_loss(z, y, [(0, 1, 2)])
+
+
+@pytest.mark.parametrize("vocab", [1000, 30001])
+def test_offsets_past_32_bits(vocab):
+    """Rows far apart: element offsets past 2^32, of the logits and of their gradient."""
+    rows, ld, n = 4500, 2 ** 20, 6
+    assert (rows - n) * ld > 2 ** 32
+    z0, y0, noise = inputs(n, vocab, torch.bfloat16, seed=21, ignored=0.0)
+    buf = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")     # 9.4 GB, only the last rows are filled
+    z = buf[:, :vocab]
+    z[rows - n:] = z0
+    y = torch.full((rows,), -1, device="cuda")
+    y[rows - n:] = y0
+    ref = torch.zeros(rows, device="cuda")
+    ref[rows - n:] = noise[0, :n]
+    pairs, near_pairs = [(rows - n, rows - n + 3, 3, 3)], [(0, 3, 3, 3)]
+    want = api.pref_loss(z0.clone(), y0, near_pairs, noise[0, :n].contiguous())
+    dz = buf[:, 2 ** 19:2 ** 19 + vocab]
+    got = api.pref_loss(z, y, pairs, ref, dlogits=dz)
+    assert torch.allclose(got[0], want[0], rtol=1e-5) and torch.allclose(got[2], want[2], rtol=1e-4, atol=n * LOGP)
+    assert torch.allclose(got[1][rows - n:], want[1], atol=LOGP) and not got[1][:rows - n].count_nonzero()
+    near(dz[rows - n:], want[3].double().cpu(), grad_tol(torch.bfloat16))
+    assert not dz[:rows - n].count_nonzero()
+    old, adv = ref - 0.1, ref + 1
+    want = api.policy_loss(z0.clone(), y0, old[rows - n:].contiguous(), adv[rows - n:].contiguous())
+    got = api.policy_loss(z, y, old, adv, dlogits=z)                     # in place
+    assert torch.allclose(got[0], want[0], rtol=1e-4)
+    near(z[rows - n:], want[2].double().cpu(), grad_tol(torch.bfloat16))
