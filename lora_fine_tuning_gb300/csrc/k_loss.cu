@@ -312,6 +312,23 @@ __global__ void __launch_bounds__(kT, 2) loss_rows_kernel(const __grid_constant_
     }
 }
 
+// out = scale * sum x, in fp64 in a fixed order, by a CTA of T threads.
+template <int T>
+__device__ __forceinline__ void block_sum(const float* x, int64_t n, float scale, float* out) {
+    __shared__ double sums[T / 32];
+    double s = 0.0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += T) s += static_cast<double>(__ldcg(x + i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < T / 32; ++w) s += sums[w];
+        *out = static_cast<float>(s * static_cast<double>(scale));
+    }
+}
+
 // Long rows: a cluster of C CTAs takes rows in turn, each CTA its slice of a row.  Warps 0-15 work on a slice in
 // shared memory, warp 16 keeps the ring of slices filled with bulk copies rows ahead, warp 17 sends the slice's
 // statistics to the cluster's CTAs, warp 18 joins what they sent and turns it into the row's coefficient.  The
@@ -562,6 +579,20 @@ loss_long_rows_kernel(const __grid_constant__ P p, int32_t cluster, int32_t slic
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while a peer may still write to it
+    if constexpr (kPolicy) {
+        // the cluster that finishes last (a ticket in the workspace, which it takes back to zero) adds the rows' losses
+        if (rank != 0) return;
+        __shared__ bool last;
+        if (threadIdx.x == 0) {
+            __threadfence();
+            last = atomicAdd(p.ticket, 1u) == static_cast<uint32_t>(step) - 1u;
+        }
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        block_sum<kLongThreads>(p.row_loss, in.rows, p.scale, p.loss);
+        if (threadIdx.x == 0) *p.ticket = 0u;
+    }
 }
 
 // Margins, losses and the rows' coefficients: a CTA a pair.
@@ -665,22 +696,10 @@ __global__ void __launch_bounds__(kT) loss_grad_kernel(const __grid_constant__ P
         if (begin + k * kT < rv.vecs) grad_vec(rv, begin + k * kT, v[k], st.top, st.inv, c, y);
 }
 
-// out = scale * sum x, in fp64 in a fixed order, by one CTA.
 __global__ void __launch_bounds__(1024) loss_sum_kernel(const float* x, int64_t n, float scale, float* out) {
-    __shared__ double part[32];
     pdl_wait();
     pdl_trigger();
-    double s = 0.0;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(x[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 32; ++w) s += part[w];
-        *out = static_cast<float>(s * static_cast<double>(scale));
-    }
+    block_sum<1024>(x, n, scale, out);
 }
 
 // Rows of at most this many vectors take the register kernel: four a thread.
@@ -707,8 +726,11 @@ cudaError_t run_long(const P& p, int64_t vecs, int sms, cudaStream_t stream) {
     const int slices = static_cast<int>(std::min<size_t>(kMaxSlices, kRingBytes / slice));
     if (slices < 1) return cudaErrorInvalidValue;
     // clusters that fit the device at a time; the pipeline waits on nothing outside its cluster, so more would only queue
-    static std::atomic<int> fit[4];
-    const int log2c = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
+    static std::atomic<int> fits[64][4];   // of each device
+    int dev = 0;
+    const cudaError_t d = cudaGetDevice(&dev);
+    if (d != cudaSuccess) return d;
+    std::atomic<int>& fit = fits[dev & 63][c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kLongThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(slice) * slices;
@@ -722,7 +744,7 @@ cudaError_t run_long(const P& p, int64_t vecs, int sms, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     auto kernel = loss_long_rows_kernel<T, kPolicy, P>;
-    int n = fit[log2c].load(std::memory_order_relaxed);
+    int n = fit.load(std::memory_order_relaxed);
     if (n == 0) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
         if (e != cudaSuccess) return e;
@@ -732,7 +754,7 @@ cudaError_t run_long(const P& p, int64_t vecs, int sms, cudaStream_t stream) {
         e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
-        fit[log2c].store(n, std::memory_order_relaxed);
+        fit.store(n, std::memory_order_relaxed);
         cfg.dynamicSmemBytes = static_cast<size_t>(slice) * slices;
     }
     cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(p.in.rows, n) * c));
@@ -740,9 +762,15 @@ cudaError_t run_long(const P& p, int64_t vecs, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kernel, p, static_cast<int32_t>(c), static_cast<int32_t>(slices), static_cast<int32_t>(slice));
 }
 
+// Vectors of the longest row, however it lies.
+template <typename T, typename P>
+int64_t row_vecs(const P& p) {
+    return (p.in.vocab + 2 * (Vec<T>::n - 1)) / Vec<T>::n;
+}
+
 template <typename T, bool kPolicy, typename P>
 cudaError_t rows_of(const P& p, int sms, cudaStream_t stream) {
-    const int64_t vecs = (p.in.vocab + 2 * (Vec<T>::n - 1)) / Vec<T>::n;   // of the longest row, however it lies
+    const int64_t vecs = row_vecs<T>(p);
     if (vecs > kShortVecs) return run_long<T, kPolicy>(p, vecs, sms, stream);
     if (vecs <= kT) return run_short<T, 1, kPolicy>(p, stream);
     if (vecs <= 2 * kT) return run_short<T, 2, kPolicy>(p, stream);
@@ -755,7 +783,8 @@ cudaError_t launch_loss_stats(const PrefParams& p, int sms, cudaStream_t stream)
     return p.in.f32 ? rows_of<float, false>(p, sms, stream) : rows_of<uint16_t, false>(p, sms, stream);
 }
 
-cudaError_t launch_policy_rows(const PolicyParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_policy_rows(const PolicyParams& p, int sms, bool* summed, cudaStream_t stream) {
+    *summed = (p.in.f32 ? row_vecs<float>(p) : row_vecs<uint16_t>(p)) > kShortVecs;
     return p.in.f32 ? rows_of<float, true>(p, sms, stream) : rows_of<uint16_t, true>(p, sms, stream);
 }
 

@@ -52,6 +52,7 @@ struct PolicyParams {
     LossLogits in;
     const float *old_logp, *adv, *ref;   // rows; ref may be null
     float* row_loss;       // workspace, rows
+    uint32_t* ticket;      // workspace, zero between calls
     float* loss;           // 1
     float lo, hi;          // 1 - clip_low, 1 + clip_high
     float kl, scale;
@@ -61,7 +62,8 @@ struct PolicyParams {
 cudaError_t launch_loss_stats(const PrefParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_loss_pairs(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, cudaStream_t stream);
 cudaError_t launch_loss_grad(const PrefParams& p, cudaStream_t stream);
-cudaError_t launch_policy_rows(const PolicyParams& p, int sms, cudaStream_t stream);
+// *summed: the kernel also wrote the loss (launch_loss_sum otherwise).
+cudaError_t launch_policy_rows(const PolicyParams& p, int sms, bool* summed, cudaStream_t stream);
 cudaError_t launch_loss_sum(const float* x, int64_t n, float scale, float* out, cudaStream_t stream);
 
 }  // namespace lora

@@ -139,14 +139,16 @@ lora_status policy_loss(const lora_logits* logits, const float* old_logp, const 
     p.adv = advantages;
     p.ref = kl_coef != 0.f ? ref_logp : nullptr;
     p.row_loss = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + loss_layout(p.in.rows).row);
+    p.ticket = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + 128);   // beside the status word
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
     p.loss = loss;
     p.lo = static_cast<float>(1.0 - static_cast<double>(clip_low));
     p.hi = static_cast<float>(1.0 + static_cast<double>(clip_high));
     p.kl = kl_coef;
     p.scale = scale;
-    if (p.in.rows > 0) LORA_CUDA(timed(kLossRows, s, [&] { return launch_policy_rows(p, sms, s); }));
-    LORA_CUDA(timed(kLossSum, s, [&] { return launch_loss_sum(p.row_loss, p.in.rows, scale, loss, s); }));
+    bool summed = false;
+    if (p.in.rows > 0) LORA_CUDA(timed(kLossRows, s, [&] { return launch_policy_rows(p, sms, &summed, s); }));
+    if (!summed) LORA_CUDA(timed(kLossSum, s, [&] { return launch_loss_sum(p.row_loss, p.in.rows, scale, loss, s); }));
     return LORA_OK;
 }
 
