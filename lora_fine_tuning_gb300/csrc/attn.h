@@ -21,6 +21,7 @@ struct AttnSeq {
     int32_t item0;
     int32_t gap;         // unused rows of the output after this sequence that its items fill
     int32_t split;       // forward, keys split over several items: their number << 20 | first slot; 0: not split
+                         // dK and dV, queries split over several items: first slot + 1; 0: not split
 };
 
 // The table travels as a kernel parameter (no device table, no copy); a small batch passes a small one.
@@ -71,6 +72,8 @@ struct AttnBwdParams {
     AttnShape sh;
     const float* lse;        // rows x hq
     float* delta;            // rows x hq, from the first pass to the second
+    int32_t most;            // query tiles of an item of a sequence whose queries are split for dK and dV
+    float* part;             // their partial results: slots of kAttnKvSlotFloats, slot * hkv + head
     AttnMat O;
     AttnMat dQ, dK, dV;
     DevCtl ctl;
@@ -87,6 +90,26 @@ struct AttnFillParams {
     int32_t n;
 };
 
+// What an item of a sequence with split queries leaves: dV, then dK, each as feature groups of 4 x 128 rows x 4.
+constexpr int kAttnKvSlotFloats = 2 * 128 * 128;
+
+// Key tiles of a sequence that more than `turns` query tiles (of all packs of a group) see; these are its first ones.
+// Items of a sequence with split queries: first one for every key tile, with up to `most` query tiles, then one for each
+// with more than `most`, and so on.
+__host__ __device__ inline int attn_tiles_over(const AttnSeq& q, const AttnShape& sh, int turns) {
+    const int lg = 7 - sh.hp_log2, qt = (q.ql + (1 << lg) - 1) >> lg;
+    const int before = qt - turns / (sh.group >> sh.hp_log2);   // a key tile counts if its first query tile is before this
+    const int64_t keys = before > 0 ? (static_cast<int64_t>(before) << lg) + q.kl - q.ql : 0;
+    const int64_t seen = keys > 0 ? (keys + kAttnTile - 1) / kAttnTile : 0, all = (q.kl + kAttnTile - 1) / kAttnTile;
+    return static_cast<int>(seen < all ? seen : all);
+}
+__host__ __device__ inline int attn_turns(const AttnSeq& q, const AttnShape& sh, int key_tile) {
+    const int lg = 7 - sh.hp_log2, qt = (q.ql + (1 << lg) - 1) >> lg;
+    const int first = key_tile * kAttnTile - (q.kl - q.ql);
+    const int n = qt - ((first > 0 ? first : 0) >> lg);
+    return (n > 0 ? n : 0) * (sh.group >> sh.hp_log2);
+}
+
 inline dim3 attn_grid(int heads, int items) {
     const int y = items < 65535 ? items : 65535;
     return dim3(static_cast<unsigned>(heads), static_cast<unsigned>(y), static_cast<unsigned>((items + y - 1) / y));
@@ -100,6 +123,8 @@ cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs
 // short_keys: key tiles of 64, which mapK and mapV then describe.
 cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, bool short_keys, cudaStream_t stream);
 cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
+// Joins the partial results of `tiles` key tiles, those of the first n sequences of the table.
+cudaError_t launch_attn_kv_join(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, int tiles, cudaStream_t stream);
 cudaError_t launch_attn_fill(const AttnFillParams& p, const AttnGaps& gaps, cudaStream_t stream);
 
 }  // namespace lora

@@ -12,6 +12,7 @@ namespace {
 
 constexpr size_t kStatusBytes = 256;
 constexpr size_t kSplitBytes = static_cast<size_t>(kAttnMaxSlots) * kAttnSlotFloats * 4;
+constexpr int64_t kMaxKvSlots = kSplitBytes / 4 / kAttnKvSlotFloats;
 
 struct Prepared {
     AttnShape sh;
@@ -153,6 +154,37 @@ int split_keys(Prepared& c, int tokens, int sms) {
     return static_cast<int>(std::stable_partition(c.order.s, end, [](const AttnSeq& q) { return q.split != 0; }) - c.order.s);
 }
 
+int kv_items(const AttnSeq& q, const AttnShape& sh, int most) {
+    int n = key_tiles(q);
+    for (int over = most; attn_tiles_over(q, sh, over) > 0; over += most) n += attn_tiles_over(q, sh, over);
+    return n;
+}
+
+// Splits the queries of dK and dV where a key tile sees more of them than one and a half times what an SM gets of the call's work (few
+// key/value heads, shared by many query heads): an item then has that share at most, but no fewer than four query tiles.
+// These sequences come first in the table.  Returns how many they are, and their key tiles.
+int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
+    AttnSeq* const end = c.order.s + c.n;
+    int64_t work = 0;
+    for (AttnSeq* q = c.order.s; q != end; ++q) {
+        q->split = 0;
+        const int64_t first = attn_turns(*q, c.sh, 0), last = attn_turns(*q, c.sh, std::max(key_tiles(*q) - 1, 0));
+        work += (first + last) * key_tiles(*q) / 2 * c.sh.hkv;   // falling along the keys
+    }
+    *most = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(4, tiles_of(work, sms)), 1 << 30));
+    int64_t slots = 0;
+    *tiles = 0;
+    for (AttnSeq* q = c.order.s; q != end; ++q) {
+        if (attn_turns(*q, c.sh, 0) * 2 <= *most * 3) continue;
+        const int64_t n = kv_items(*q, c.sh, *most);
+        if ((slots + n) * c.sh.hkv > kMaxKvSlots || *tiles + key_tiles(*q) > 65535) break;
+        q->split = static_cast<int32_t>(slots + 1);
+        slots += n;
+        *tiles += key_tiles(*q);
+    }
+    return static_cast<int>(std::stable_partition(c.order.s, end, [](const AttnSeq& q) { return q.split != 0; }) - c.order.s);
+}
+
 AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
 
 // Unused rows that an item of the sequence before them is asked to fill at most; a batch with longer gaps between its
@@ -210,7 +242,7 @@ extern "C" {
 
 size_t attn_workspace_size(int64_t q_rows, int32_t q_heads) {
     if (q_rows < 0 || q_heads < 0) return 0;
-    return kStatusBytes + std::max(kSplitBytes, delta_bytes(q_rows, q_heads));
+    return kStatusBytes + kSplitBytes + delta_bytes(q_rows, q_heads);
 }
 
 lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const lora_attn_shape* shape,
@@ -321,12 +353,18 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     if (!key_maps(short_keys ? kAttnTile / 2 : kAttnTile)) return LORA_ECUDA;
     if (c.sh.items > 0) LORA_CUDA(timed(kAttnDq, s, [&] { return launch_attn_dq(p, c.order, short_keys, s); }));
     if (short_keys && !key_maps(kAttnTile)) return LORA_ECUDA;
-    if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.kl, kAttnTile); }))) return st;
+    int split = 0, split_tiles = 0;
+    if (workspace_bytes >= kStatusBytes + delta_bytes(a.q_rows, a.q_heads) + kSplitBytes)
+        split = split_queries(c, sms, &p.most, &split_tiles);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes + delta_bytes(a.q_rows, a.q_heads));
+    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? kv_items(q, c.sh, p.most) : key_tiles(q); })))
+        return st;
     if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, [](const AttnSeq& q) { return q.k0; }, [](const AttnSeq& q) { return q.kl; })) {
         if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
     }
     p.sh = c.sh;
     if (c.sh.items > 0) LORA_CUDA(timed(kAttnDkDv, s, [&] { return launch_attn_dkdv(p, c.order, s); }));
+    if (split > 0) LORA_CUDA(timed(kAttnJoin, s, [&] { return launch_attn_kv_join(p, c.order, split, split_tiles, s); }));
     return LORA_OK;
 }
 

@@ -770,7 +770,13 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     const AttnShape& sh = p.sh;
     const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;
-    const int kt = item - sq.item0;                // the first key tiles have the most queries
+    // the first key tiles have the most queries; of a sequence with split queries the item has piece `piece` of a tile's
+    int kt = item - sq.item0, piece = 0;
+    if (sq.split)
+        for (int c = (sq.kl + kAttnTile - 1) / kAttnTile; kt >= c; c = attn_tiles_over(sq, sh, piece * p.most)) {
+            kt -= c;
+            ++piece;
+        }
     const int kvh = blockIdx.x;
     const int off = sq.kl - sq.ql;
     const int key0 = kt * kAttnTile;
@@ -779,12 +785,14 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
     const int qt = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
     const int per = max(0, qt - i0);
     const int packs = sh.group >> sh.hp_log2;
-    const int n = per * packs;
+    const int all = per * packs;
+    const int pieces = sq.split ? max(1, (all + p.most - 1) / p.most) : 1, each = (all + pieces - 1) / pieces;
+    const int t0 = piece * each, n = min(each, all - t0);   // the item's turns
     const int ragged = sq.ql - (qt - 1) * tpt;           // tokens of the last query tile
     const bool tail = ragged < tpt;
 
-    const auto head_of = [&](int t) { return kvh * sh.group + ((packs == 1 ? 0 : t / per) << sh.hp_log2); };
-    const auto tile_of = [&](int t) { return i0 + (packs == 1 ? t : t - t / per * per); };
+    const auto head_of = [&](int t) { return kvh * sh.group + ((packs == 1 ? 0 : (t0 + t) / per) << sh.hp_log2); };
+    const auto tile_of = [&](int t) { return i0 + (packs == 1 ? t0 + t : (t0 + t) % per); };
     const auto load_q = [&](int t) {
         const int s = t % SQ;
         mbar_arrive_expect_tx(&q_full[s], C::kTileBytes);
@@ -962,9 +970,8 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         const F2 sl2 = f2(sl, sl);
         // two tiles ahead: lse (a row that is not there, or sees no key: +inf, P = 0) or delta
         const auto fetch = [&](int t) -> float {
-            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
-            const int tok = i * tpt + (ct >> sh.hp_log2);
-            const int head = kvh * sh.group + (pack << sh.hp_log2) + (ct & (sh.hp - 1));
+            const int tok = tile_of(t) * tpt + (ct >> sh.hp_log2);
+            const int head = head_of(t) + (ct & (sh.hp - 1));
             const bool there = t < n && tok < sq.ql && tok + off >= 0;
             float x = g == 0 ? -neg_inf() : 0.f;
             if (there) x = src[(static_cast<int64_t>(sq.q0) + tok) * sh.hq + head];
@@ -972,7 +979,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         };
         const float unit = g == 0 ? -kLog2e : -1.f;   // applied when it is stored: the load is not waited for before
         if (sq.gap + sh.lead + sh.trail > 0)
-            fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, sq.gap, kt,
+            fill_rows<16>(p.dK, &p.dV, nullptr, sh, kvh, 0, static_cast<int64_t>(sq.k0) + sq.kl, piece == 0 ? sq.gap : 0, kt,
                       (sq.kl + kAttnTile - 1) / kAttnTile, item, sh.items, threadIdx.x);
         bool ok = true;
         // statistics of tile t in buffer t & 1: tile 0's now, each later one's in the turn before
@@ -981,7 +988,7 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         float next = n > 0 ? fetch(1) : 0.f;
         for (int t = 0; t < n; ++t) {
             float* stat = sStat + (t & 1) * 256;
-            const int pack = packs == 1 ? 0 : t / per, i = i0 + (t - pack * per);
+            const int i = tile_of(t);
             const uint32_t st = smem_u32(stat) + g * 256;    // this group's 64 columns
             ok = mbar_wait(s_full, t & 1, w, 12);
             ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(stat_full, t & 1, w, 15));
@@ -1060,7 +1067,18 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         }
-        if (ok) {
+        if (ok && pieces > 1) {
+            float* const slot = p.part + (static_cast<int64_t>(sq.split - 1 + item - sq.item0) * sh.hkv + kvh) * kAttnKvSlotFloats + g * 128 * 128;
+#pragma unroll 1
+            for (int c = 0; c < sh.d16; c += 16) {
+                uint32_t o[16];
+                tmem_ld16((g == 0 ? t_dv : t_dk) + lanes + c, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    stg128(slot + ((c + e) * 128 + r * 4), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+            }
+        } else if (ok) {
             // group 0 writes dV, group 1 dK, through V's and K's shared memory: all products are done
             const AttnMat& m = g == 0 ? p.dV : p.dK;
             store_tile(m.p + (static_cast<int64_t>(sq.k0) + key0) * m.row + static_cast<int64_t>(kvh) * m.head, m.row, m.head,
@@ -1075,6 +1093,36 @@ attn_dkdv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the partial dK and dV of the key tiles whose queries were split, in the pieces' order.  A block a key tile, a key/value
+// head and eight features of dV or dK, a thread a row.
+template <int N>
+__global__ void __launch_bounds__(128) attn_kv_join_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnSeqs<N> seqs) {
+    pdl_wait();
+    pdl_trigger();
+    const AttnShape& sh = p.sh;
+    int i = 0, kt = blockIdx.y;
+    for (int c; kt >= (c = (seqs.s[i].kl + kAttnTile - 1) / kAttnTile); ++i) kt -= c;
+    const AttnSeq& sq = seqs.s[i];
+    const int pieces = (attn_turns(sq, sh, kt) + p.most - 1) / p.most;
+    const int r = threadIdx.x, key = kt * kAttnTile + r;
+    if (pieces < 2 || key >= sq.kl) return;
+    const int groups = sh.d / 8, which = blockIdx.z / groups, c = (blockIdx.z - which * groups) * 8;   // dV, dK
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int at = sq.split - 1 + kt;
+    for (int q = 0; q < pieces; ++q) {
+        const float* const x = p.part + (static_cast<int64_t>(at) * sh.hkv + blockIdx.x) * kAttnKvSlotFloats + which * 128 * 128 + c * 128 + r * 4;
+        const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4 * 128);
+        o[0] += a.x, o[1] += a.y, o[2] += a.z, o[3] += a.w;
+        o[4] += b.x, o[5] += b.y, o[6] += b.z, o[7] += b.w;
+        at += q == 0 ? (sq.kl + kAttnTile - 1) / kAttnTile : attn_tiles_over(sq, sh, q * p.most);
+    }
+    const AttnMat& m = which == 0 ? p.dV : p.dK;
+    const float f = which == 0 ? 1.f : sh.scale;
+    stg128(m.p + (static_cast<int64_t>(sq.k0) + key) * m.row + static_cast<int64_t>(blockIdx.x) * m.head + c,
+           make_uint4(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f), pack_bf16x2(o[4] * f, o[5] * f),
+                      pack_bf16x2(o[6] * f, o[7] * f)));
 }
 
 template <int DP, int N>
@@ -1132,6 +1180,14 @@ cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs
     if (p.sh.d <= 64)
         return few ? run_dkdv<64, kAttnFewSeqs>(p, seqs, stream) : run_dkdv<64, kAttnMaxSeqs>(p, seqs, stream);
     return few ? run_dkdv<128, kAttnFewSeqs>(p, seqs, stream) : run_dkdv<128, kAttnMaxSeqs>(p, seqs, stream);
+}
+
+cudaError_t launch_attn_kv_join(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, int tiles, cudaStream_t stream) {
+    const dim3 grid(p.sh.hkv, tiles, 2 * (p.sh.d / 8));
+    if (n <= kAttnFewSeqs)
+        return launch_pdl(attn_kv_join_kernel<kAttnFewSeqs>, grid, dim3(128), 0, stream, p,
+                          reinterpret_cast<const AttnSeqs<kAttnFewSeqs>&>(seqs));
+    return launch_pdl(attn_kv_join_kernel<kAttnMaxSeqs>, grid, dim3(128), 0, stream, p, seqs);
 }
 
 }  // namespace lora

@@ -380,3 +380,27 @@ def test_offsets_past_32_bits():
     for got, ref, m in ((O, want[0], n), (dQ, want[2], n), (dK, want[3], 1000), (dV, want[4], 1000), (lse, want[1], n)):
         assert torch.equal(got[:40], ref[:40]) and torch.equal(got[rows - m:], ref[40:])
     assert not O[40:rows - n].count_nonzero() and not dK[40:k0].count_nonzero()
+
+
+@pytest.mark.parametrize("lengths,hq,hkv,d,layout", [
+    ([900], 8, 1, 128, "rows"), ([1500], 1, 1, 64, "heads"), ([700, 3, 0, 130, 257], 12, 1, 72, "rows"),
+    ([1300, 40], 7, 1, 128, "fused"), ([513, 512, 511], 16, 2, 40, "rows"), ([260], 128, 1, 64, "rows")])
+def test_few_key_heads(lengths, hq, hkv, d, layout):
+    """Queries of dK and dV split over several SMs and joined: many query heads on few key heads, ends that do not fill a
+    tile, unused rows between; against the formula, and against the unsplit way (a workspace without the region)."""
+    seqs, rows = packed(lengths, 128)
+    seqs.append((rows, 300, rows, 41))           # more queries than keys
+    seqs.append((rows + 301, 5, rows + 43, 700))   # fewer
+    tq, tk = rows + 310, rows + 750
+    if layout == "fused":
+        tq = tk = max(tq, tk)
+    Q, K, V, dO = inputs(tq, tk, hq, hkv, d, layout, seed=hq)
+    got = run(Q, K, V, dO, seqs, None)
+    check(Q, K, V, seqs, d ** -0.5, dO, got)
+    ws = torch.zeros(256 + -(-tq * hq * 4 // 256) * 256, dtype=torch.uint8, device="cuda")
+    whole = api.attn_bwd(dO, Q, K, V, got[0], got[1], seqs, ws=ws)
+    assert torch.equal(whole[0], got[2])
+    for a, b in zip(whole[1:], got[3:]):
+        assert off(a, b.double().cpu()) <= TOL
+    again = api.attn_bwd(dO, Q, K, V, got[0], got[1], seqs)
+    assert all(torch.equal(a, b) for a, b in zip(again, got[2:]))
