@@ -289,9 +289,10 @@ lora_status lora_fwd_static_scratch(const lora_bf16* X, const lora_bf16* W, cons
  *    Every sum has a fixed order: results are bit-identical from call to call in both reduction modes.
  *  - workspace: attn_workspace_size() bytes, 256-byte aligned, not shared by calls that may overlap.  Its first 256
  *    bytes (the device status word) are zero before the first use and stay so; the rest is scratch whose contents do
- *    not matter, so it is no workspace for the calls above.  attn_fwd runs with 256 bytes, too: it then splits no
- *    sequence's keys over several SMs (it does so for a few query rows over a long prompt; the results of the two ways
- *    agree to fp32 rounding). */
+ *    not matter, so it is no workspace for the calls above.  43 MB of it hold the partial results of sequences whose keys
+ *    (attn_fwd: a few rows or heads over a long prompt) or queries (attn_bwd: many query heads on few key/value heads)
+ *    are split over several SMs.  Without that region (256 bytes for attn_fwd, 256 and fp32 q_rows x q_heads rounded up
+ *    to 256 for attn_bwd) nothing is split; the results of the two ways agree to fp32 rounding. */
 enum { LORA_ATTN_MAX_SEQS = 1024, LORA_ATTN_MAX_HEADS = 1024, LORA_ATTN_MAX_HEAD_DIM = 128 };
 
 typedef struct {

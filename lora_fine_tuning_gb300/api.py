@@ -282,6 +282,9 @@ def dora_bwd(dY, X, W, A, B, S_saved, Y, mag, g_saved, alpha: float, p: float, s
 _STREAM_WS: dict = {}
 
 
+_GRAIN = 1 << 20   # bytes: a slightly larger batch then needs no new workspace
+
+
 class _On:
     """Allocates on the device of `t` and for the stream the call runs on: the caching allocator then hands the
     memory to nobody else before that stream is done with it."""
@@ -305,7 +308,7 @@ class _On:
         key = (kind, self.index, self.handle)
         ws = _STREAM_WS.get(key)
         if ws is None or ws.numel() < size:
-            ws = self.empty(max(256, 1 << (size - 1).bit_length()), torch.uint8)
+            ws = self.empty(-(-size // _GRAIN) * _GRAIN, torch.uint8)
             with torch.cuda.stream(self.stream):
                 ws.zero_()
             _STREAM_WS[key] = ws

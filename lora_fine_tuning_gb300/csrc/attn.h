@@ -20,8 +20,7 @@ struct AttnSeq {
     int32_t ql, kl;      // rows
     int32_t item0;
     int32_t gap;         // unused rows of the output after this sequence that its items fill
-    int32_t split;       // forward, keys split over several items: their number << 20 | first slot; 0: not split
-                         // dK and dV, queries split over several items: first slot + 1; 0: not split
+    int32_t split;       // keys (forward) or queries (dK and dV) split over several items: first slot + 1; 0: not split
 };
 
 // The table travels as a kernel parameter (no device table, no copy); a small batch passes a small one.
@@ -58,7 +57,8 @@ struct AttnFwdParams {
     AttnShape sh;
     AttnMat O;
     float* lse;              // rows x hq
-    float* part;             // slots of partial results (kAttnSlotFloats each), slot * packs + pack
+    int32_t most;            // key tiles of an item of a sequence whose keys are split
+    float* part;             // their partial results: slots of kAttnSlotFloats, slot * packs + pack
     DevCtl ctl;
 };
 
@@ -93,6 +93,27 @@ struct AttnFillParams {
 // What an item of a sequence with split queries leaves: dV, then dK, each as feature groups of 4 x 128 rows x 4.
 constexpr int kAttnKvSlotFloats = 2 * 128 * 128;
 
+// Key tiles that query tile `tile` of a sequence sees, and the query tiles that see more than `n` of them; these are its last
+// ones.  Items of a sequence with split keys: first one for every query tile, from the last, with up to `most` key tiles,
+// then one for each that sees more than `most`, and so on.
+__host__ __device__ inline int attn_query_tiles(const AttnSeq& q, const AttnShape& sh) {
+    const int lg = 7 - sh.hp_log2;
+    return (q.ql + (1 << lg) - 1) >> lg;
+}
+__host__ __device__ inline int attn_seen(const AttnSeq& q, const AttnShape& sh, int tile) {
+    const int end = (tile + 1) << (7 - sh.hp_log2), last = (end < q.ql ? end : q.ql) - 1 + q.kl - q.ql;
+    return last >= 0 ? last / kAttnTile + 1 : 0;
+}
+// Pieces of the keys of a sequence's last query tile: each of its tiles has as many slots.
+__host__ __device__ inline int attn_pieces(const AttnSeq& q, int most) { return ((q.kl + kAttnTile - 1) / kAttnTile + most - 1) / most; }
+__host__ __device__ inline int attn_tiles_seeing(const AttnSeq& q, const AttnShape& sh, int n) {
+    if (q.ql == 0 || q.kl <= static_cast<int64_t>(n) * kAttnTile) return 0;
+    const int lg = 7 - sh.hp_log2, tiles = attn_query_tiles(q, sh);
+    // the first token that sees key n * 128, and its tile
+    const int64_t token = static_cast<int64_t>(n) * kAttnTile - (q.kl - q.ql);
+    return tiles - (token > 0 ? static_cast<int>(token >> lg) : 0);
+}
+
 // Key tiles of a sequence that more than `turns` query tiles (of all packs of a group) see; these are its first ones.
 // Items of a sequence with split queries: first one for every key tile, with up to `most` query tiles, then one for each
 // with more than `most`, and so on.
@@ -118,8 +139,8 @@ inline dim3 attn_grid(int heads, int items) {
 cudaError_t attn_fwd_configure();
 cudaError_t attn_bwd_configure();
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);
-// Joins the partial results of the split sequences (n of them, the first of the table).
-cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream);
+// Joins the partial results of `tiles` query tiles, those of the first n sequences of the table.
+cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, int tiles, cudaStream_t stream);
 // short_keys: key tiles of 64, which mapK and mapV then describe.
 cudaError_t launch_attn_dq(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, bool short_keys, cudaStream_t stream);
 cudaError_t launch_attn_dkdv(const AttnBwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, cudaStream_t stream);

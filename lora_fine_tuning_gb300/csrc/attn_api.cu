@@ -132,24 +132,38 @@ bool few_keys(const Prepared& c, int tokens) {
     return keys <= 512 * tiles;
 }
 
-// Splits the keys of sequences whose rows fill one query tile at most (`tokens` of them), where their long ranges would
-// keep a few SMs busy long after the others: into pieces of equal length, of at most two thirds of what an SM gets of the
-// call's work, but of no fewer than four key tiles.  They come first in the table, as the join wants them.  Returns how
-// many they are.  24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128: 63 us with the join; pieces
-// of all or half an SM's share 71 and 77, none 121.  One token over 4096 keys: 12 us, with at least eight tiles a piece 14.
-int split_keys(Prepared& c, int tokens, int sms) {
+int q_items(const AttnSeq& q, const AttnShape& sh, int most) {
+    int n = attn_query_tiles(q, sh);
+    for (int over = most; attn_tiles_seeing(q, sh, over) > 0; over += most) n += attn_tiles_seeing(q, sh, over);
+    return n;
+}
+
+// Splits the keys of the forward's query tiles, where few rows or heads over long ranges would keep a few SMs busy long after
+// the others: an item then has at most two thirds of what an SM gets of the call's work, but no fewer than four key tiles.
+// Sequences of one query tile are split from there on, longer ones, which a few long tiles do not hold up as much, from
+// four times that.  They come first in the table, as the join wants them.  Returns how many they are, and their query tiles.
+// 24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128: 63 us with the join; pieces of all or half
+// an SM's share 71 and 77, none 121.  One token over 4096 keys: 12 us, with at least eight tiles a piece 14.  A prompt of
+// 8192 tokens with one head of 128: 25 us and 10 for the join, whole 82; with 8/1 heads, 4096 tokens (1.7 times): 45 and 10,
+// whole 48.
+int split_keys(Prepared& c, int sms, int32_t* most, int* tiles) {
     AttnSeq* const end = c.order.s + c.n;
     int64_t work = 0;
-    for (const AttnSeq* q = c.order.s; q != end; ++q)
-        work += tiles_of(q->ql, tokens) * key_tiles(*q) * c.sh.packs;
-    const int64_t most = std::max<int64_t>(4, tiles_of(2 * work, 3 * sms));
+    for (const AttnSeq* q = c.order.s; q != end; ++q) {
+        const int t = attn_query_tiles(*q, c.sh);
+        if (t > 0) work += static_cast<int64_t>(attn_seen(*q, c.sh, 0) + attn_seen(*q, c.sh, t - 1)) * t * c.sh.packs;   // twice
+    }
+    *most = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(4, tiles_of(work, 3 * sms)), 1 << 30));
     int64_t slots = 0;
+    *tiles = 0;
     for (AttnSeq* q = c.order.s; q != end; ++q) {
-        if (q->ql == 0 || q->ql > tokens || key_tiles(*q) <= most) continue;
-        const int64_t n = tiles_of(key_tiles(*q), most);
+        const int t = attn_query_tiles(*q, c.sh);
+        if (t == 0 || key_tiles(*q) < (t == 1 ? *most + 1 : 4 * static_cast<int64_t>(*most))) continue;
+        const int64_t n = static_cast<int64_t>(t) * attn_pieces(*q, *most);
         if ((slots + n) * c.sh.packs > kAttnMaxSlots) break;
-        q->split = static_cast<int32_t>(n << 20 | slots);
+        q->split = static_cast<int32_t>(slots + 1);
         slots += n;
+        *tiles += t;
     }
     return static_cast<int>(std::stable_partition(c.order.s, end, [](const AttnSeq& q) { return q.split != 0; }) - c.order.s);
 }
@@ -160,9 +174,11 @@ int kv_items(const AttnSeq& q, const AttnShape& sh, int most) {
     return n;
 }
 
-// Splits the queries of dK and dV where a key tile sees more of them than one and a half times what an SM gets of the call's work (few
-// key/value heads, shared by many query heads): an item then has that share at most, but no fewer than four query tiles.
-// These sequences come first in the table.  Returns how many they are, and their key tiles.
+// Splits the queries of dK and dV where a key tile sees more of them than one and a half times what an SM gets of the call's
+// work (few key/value heads, shared by many query heads): an item then has that share at most, but no fewer than four
+// query tiles.  These sequences come first in the table.  Returns how many they are, and their key tiles.  One sequence of
+// 2048 tokens with 8/1 heads of 128: 25 us and 8 for the join, pieces of half that length 33 and 15, none 177; of 4096
+// tokens 82 and 6, 74 and 10, 342.
 int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
     AttnSeq* const end = c.order.s + c.n;
     int64_t work = 0;
@@ -266,8 +282,10 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     order_by_keys(c);
     const int tokens = kAttnTile / c.sh.hp;
-    const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, tokens, sms) : 0;
-    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q.split >> 20 : tiles_of(q.ql, tokens); })))
+    int32_t most = 0;
+    int split_tiles = 0;
+    const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, sms, &most, &split_tiles) : 0;
+    if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q_items(q, c.sh, most) : attn_query_tiles(q, c.sh); })))
         return st;
     if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
@@ -287,9 +305,10 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     p.O = mat(O, a.o);
     p.lse = lse;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
+    p.most = most;
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
     LORA_CUDA(timed(kAttnFwd, s, [&] { return launch_attn_fwd(p, c.order, s); }));
-    if (split > 0) LORA_CUDA(timed(kAttnJoin, s, [&] { return launch_attn_join(p, c.order, split, s); }));
+    if (split > 0) LORA_CUDA(timed(kAttnJoin, s, [&] { return launch_attn_join(p, c.order, split, split_tiles, s); }));
     return LORA_OK;
 }
 

@@ -63,22 +63,21 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
     const AttnShape& sh = p.sh;
     const AttnSeq sq = find_seq(seqs, sh.n_seqs, item);
     const int tpt = kAttnTile >> sh.hp_log2;                       // tokens in a tile
-    const int tiles = (sq.ql + tpt - 1) >> (7 - sh.hp_log2);
-    const int local = item - sq.item0;
-    const int tok0 = sq.split ? 0 : (tiles - 1 - local) * tpt;      // first token
+    const int tiles = attn_query_tiles(sq, sh);
+    // of a sequence with split keys the item has piece `piece` of a tile's
+    int local = item - sq.item0, piece = 0;
+    if (sq.split)
+        for (int c = tiles; local >= c; c = attn_tiles_seeing(sq, sh, piece * p.most)) {
+            local -= c;
+            ++piece;
+        }
+    const int tok0 = (tiles - 1 - local) * tpt;                     // first token
     const int head0 = blockIdx.x << sh.hp_log2;
     const int kvh = sh.hp == sh.group ? blockIdx.x : head0 / sh.group;
     const int off = sq.kl - sq.ql;
-    const int last = min(tok0 + tpt, sq.ql) - 1 + off;              // last key the tile sees
-    int n = last >= 0 ? last / kAttnTile + 1 : 0;                   // its key tiles
-    // few rows, many keys: the item has a range of the keys of the sequence's only tile
-    const int splits = sq.split >> 20;
-    int kb = 0;                                                     // its first key tile
-    if (splits > 0) {
-        const int all = n, per = (all + splits - 1) / splits;
-        kb = min(local * per, all);
-        n = min(per, all - kb);
-    }
+    const int all = attn_seen(sq, sh, tiles - 1 - local);           // its key tiles
+    const int pieces = sq.split ? max(1, (all + p.most - 1) / p.most) : 1, each = (all + pieces - 1) / pieces;
+    const int kb = piece * each, n = min(each, all - kb);           // the item's
     const bool tail = (kb + n) * kAttnTile > sq.kl;               // the last key tile ends past the sequence
 
     const auto load_kv = [&](int t) {
@@ -220,8 +219,8 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
         const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
         // under the first loads
         if (sq.gap + sh.lead + sh.trail > 0)
-            fill_rows<8>(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql, sq.gap,
-                      local, splits > 0 ? splits : tiles, item, sh.items, threadIdx.x);
+            fill_rows<8>(p.O, nullptr, p.lse, sh, head0, sh.hp_log2, static_cast<int64_t>(sq.q0) + sq.ql,
+                      piece == 0 ? sq.gap : 0, local, tiles, item, sh.items, threadIdx.x);
         const uint32_t ts = tmem + lanes, to = ts + 128;
         const float sl = sh.scale_log2;
         const int first_limit = tok0 + off;          // last key the tile's first row sees
@@ -306,8 +305,8 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
         }
-        if (ok && splits > 0) {
-            float* const slot = p.part + (static_cast<int64_t>((sq.split & 0xFFFFF) + local) * sh.packs + blockIdx.x) * kAttnSlotFloats;
+        if (ok && pieces > 1) {
+            float* const slot = p.part + (static_cast<int64_t>(sq.split - 1 + local * attn_pieces(sq, p.most) + piece) * sh.packs + blockIdx.x) * kAttnSlotFloats;
 #pragma unroll 1
             for (int c = 0; c < sh.d16; c += 16) {
                 uint32_t o[16];
@@ -338,7 +337,7 @@ attn_fwd_kernel(const __grid_constant__ AttnFwdParams p, const __grid_constant__
     }
 }
 
-// Joins the partial results of a split sequence's items: with M the largest of their maxima m_s,
+// Joins the partial results of the tiles whose keys were split: with M the largest of their maxima m_s,
 //   O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  Blocks of 128 rows x 4 features, a thread a row.
 template <int N>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnFwdParams p,
@@ -346,16 +345,19 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     pdl_wait();
     pdl_trigger();
     const AttnShape& sh = p.sh;
-    const AttnSeq sq = seqs.s[blockIdx.y];
-    const int splits = sq.split >> 20, r = threadIdx.x, c = blockIdx.z * 4;
-    if (r >= sq.ql << sh.hp_log2) return;
-    const float* const slot = p.part + (static_cast<int64_t>(sq.split & 0xFFFFF) * sh.packs + blockIdx.x) * kAttnSlotFloats;
+    int i = 0, u = blockIdx.y;   // tile, from the sequence's last
+    for (int c; u >= (c = attn_query_tiles(seqs.s[i], sh)); ++i) u -= c;
+    const AttnSeq& sq = seqs.s[i];
+    const int tiles = attn_query_tiles(sq, sh), pieces = (attn_seen(sq, sh, tiles - 1 - u) + p.most - 1) / p.most;
+    const int r = threadIdx.x, c = blockIdx.z * 4, tok = ((tiles - 1 - u) << (7 - sh.hp_log2)) + (r >> sh.hp_log2);
+    if (pieces < 2 || tok >= sq.ql) return;
+    const float* const slot = p.part + (static_cast<int64_t>(sq.split - 1 + u * attn_pieces(sq, p.most)) * sh.packs + blockIdx.x) * kAttnSlotFloats;
     const int64_t step = static_cast<int64_t>(sh.packs) * kAttnSlotFloats;
     float top = neg_inf();
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, slot[s * step + 128 * 128 + r]);
+    for (int s = 0; s < pieces; ++s) top = fmaxf(top, slot[s * step + 128 * 128 + r]);
     const float ts = top == neg_inf() ? 0.f : top;
     float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) {
+    for (int s = 0; s < pieces; ++s) {
         const float* const q = slot + s * step;
         const float f = ex2(q[128 * 128 + r] - ts), ls = q[128 * 128 + 128 + r];
         if (ls == 0.f) continue;   // no key of this range is visible
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
         o[3] = fmaf(f, v.w, o[3]);
     }
     const float f = l == 0.f ? 0.f : 1.f / l;
-    const int64_t row = static_cast<int64_t>(sq.q0) + (r >> sh.hp_log2);
+    const int64_t row = static_cast<int64_t>(sq.q0) + tok;
     const int head = (blockIdx.x << sh.hp_log2) + (r & (sh.hp - 1));
     *reinterpret_cast<uint2*>(p.O.p + row * p.O.row + static_cast<int64_t>(head) * p.O.head + c) =
         make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
@@ -422,8 +424,8 @@ cudaError_t launch_attn_fwd(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>
     return few ? run<128, kAttnFewSeqs>(p, seqs, stream) : run<128, kAttnMaxSeqs>(p, seqs, stream);
 }
 
-cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, cudaStream_t stream) {
-    const dim3 grid(p.sh.packs, n, p.sh.d / 4);
+cudaError_t launch_attn_join(const AttnFwdParams& p, const AttnSeqs<kAttnMaxSeqs>& seqs, int n, int tiles, cudaStream_t stream) {
+    const dim3 grid(p.sh.packs, tiles, p.sh.d / 4);
     if (n <= kAttnFewSeqs)
         return launch_pdl(attn_join_kernel<kAttnFewSeqs>, grid, dim3(128), 0, stream, p,
                           reinterpret_cast<const AttnSeqs<kAttnFewSeqs>&>(seqs));

@@ -404,3 +404,24 @@ def test_few_key_heads(lengths, hq, hkv, d, layout):
         assert off(a, b.double().cpu()) <= TOL
     again = api.attn_bwd(dO, Q, K, V, got[0], got[1], seqs)
     assert all(torch.equal(a, b) for a, b in zip(again, got[2:]))
+
+
+@pytest.mark.parametrize("lengths,hq,hkv,d,layout", [
+    ([2500], 1, 1, 128, "rows"), ([1900], 4, 1, 64, "heads"), ([1700, 3, 0, 130], 2, 2, 72, "rows"),
+    ([1300, 40], 6, 1, 96, "fused"), ([3001], 16, 1, 40, "rows")])
+def test_long_rows_on_few_heads(lengths, hq, hkv, d, layout):
+    """Keys of whole prompts split over several SMs: some of their tiles in several pieces, some in one."""
+    seqs, rows = packed(lengths, 128)
+    seqs.append((rows, 300, rows, 41))             # more queries than keys
+    seqs.append((rows + 301, 70, rows + 43, 1800))   # fewer
+    tq, tk = rows + 375, rows + 1850
+    if layout == "fused":
+        tq = tk = max(tq, tk)
+    Q, K, V, dO = inputs(tq, tk, hq, hkv, d, layout, seed=hq)
+    got = run(Q, K, V, dO, seqs, None)
+    check(Q, K, V, seqs, d ** -0.5, dO, got)
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    O, lse = api.attn_fwd(Q, K, V, seqs, ws=small)
+    assert off(O, got[0].double().cpu()) <= TOL and torch.equal(torch.isinf(lse), torch.isinf(got[1]))
+    again = api.attn_fwd(Q, K, V, seqs)
+    assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
