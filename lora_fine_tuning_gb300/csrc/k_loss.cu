@@ -11,6 +11,7 @@
 // All statistics are fp32 relative to the row's maximum (p of the label is then exact to 2^-23 also near 1, where
 // 1 - p is the gradient); sums over tokens are fp64 in a fixed order.
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -329,6 +330,66 @@ __device__ __forceinline__ void block_sum(const float* x, int64_t n, float scale
     }
 }
 
+// The rows of a pair: its chosen ones, then its rejected ones.
+struct PairRows {
+    PrefPair q;
+    __device__ __forceinline__ int count() const { return q.chosen_rows + q.rejected_rows; }
+    __device__ __forceinline__ int64_t row(int i) const { return i < q.chosen_rows ? q.chosen + i : q.rejected + (i - q.chosen_rows); }
+};
+// What rows [from, from + step, ...) of a pair add to its margin.
+__device__ __forceinline__ double margin_part(const PrefParams& p, const PairRows& pr, int from, int step) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = from; i < pr.count(); i += step) {
+        const int64_t r = pr.row(i), y = p.in.labels[r];
+        const double d = static_cast<double>(__ldcg(p.in.logp + r)) - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
+        if (y >= 0 && y < p.in.vocab) sum += i < pr.q.chosen_rows ? d : -d;
+    }
+    return sum;
+}
+// The pair's loss (without `scale`) and d (scale loss) / d margin.
+__device__ __forceinline__ float2 pair_loss(const PrefParams& p, double margin) {
+    const float h = static_cast<float>(static_cast<double>(p.beta) * margin);
+    const float e = p.smoothing;
+    // log sigmoid(h) = min(h, 0) - log1p(exp(-|h|)),  log sigmoid(-h) = log sigmoid(h) - h
+    const float small = expf(-fabsf(h)), tail = log1pf(small);
+    const float loss = h != h ? h : (1.f - e) * (tail - fminf(h, 0.f)) + e * (tail + fmaxf(h, 0.f));
+    const float s_neg = (h >= 0.f ? small : 1.f) / (1.f + small);   // sigmoid(-h)
+    const float s_pos = (h >= 0.f ? 1.f : small) / (1.f + small);
+    const float g = h != h ? h : p.scale * p.beta * (e * s_pos - (1.f - e) * s_neg);
+    return make_float2(loss, g);
+}
+__device__ __forceinline__ void write_coefs(const PrefParams& p, const PairRows& pr, float g, int from, int step) {
+    for (int i = from; i < pr.count(); i += step) {
+        const int64_t r = pr.row(i), y = p.in.labels[r];
+        if (y >= 0 && y < p.in.vocab) p.coef[r] = i < pr.q.chosen_rows ? g : -g;
+    }
+}
+
+// All pairs by the warps of one CTA, a warp a pair, and the loss.
+__device__ __forceinline__ void pairs_by_warps(const PrefLong& p, int warps) {
+    const int lane = threadIdx.x & 31;
+    for (int q = threadIdx.x >> 5; q < p.n_pairs; q += warps) {
+        const PairRows pr{p.pairs.p[q]};
+        double sum = margin_part(p, pr, lane, 32);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float2 lg = pair_loss(p, sum);
+        write_coefs(p, pr, lg.y, lane, 32);
+        if (lane == 0) {
+            p.margin[q] = static_cast<float>(sum);
+            p.pair_loss[q] = lg.x;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    double total = 0.0;
+    for (int i = lane; i < p.n_pairs; i += 32) total += static_cast<double>(__ldcg(p.pair_loss + i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    if (lane == 0) *p.loss = static_cast<float>(total * static_cast<double>(p.scale));
+}
+
 // Long rows: a cluster of C CTAs takes rows in turn, each CTA its slice of a row.  Warps 0-15 work on a slice in
 // shared memory, warp 16 keeps the ring of slices filled with bulk copies rows ahead, warp 17 sends the slice's
 // statistics to the cluster's CTAs, warp 18 joins what they sent and turns it into the row's coefficient.  The
@@ -579,20 +640,22 @@ loss_long_rows_kernel(const __grid_constant__ P p, int32_t cluster, int32_t slic
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while a peer may still write to it
-    if constexpr (kPolicy) {
-        // the cluster that finishes last (a ticket in the workspace, which it takes back to zero) adds the rows' losses
-        if (rank != 0) return;
-        __shared__ bool last;
-        if (threadIdx.x == 0) {
-            __threadfence();
-            last = atomicAdd(p.ticket, 1u) == static_cast<uint32_t>(step) - 1u;
-        }
-        __syncthreads();
-        if (!last) return;
+    // the cluster that finishes last (a ticket in the workspace, which it takes back to zero) adds the rows' losses, or forms
+    // the pairs'
+    if constexpr (!kPolicy)
+        if (!p.fused) return;
+    if (rank != 0) return;
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
         __threadfence();
-        block_sum<kLongThreads>(p.row_loss, in.rows, p.scale, p.loss);
-        if (threadIdx.x == 0) *p.ticket = 0u;
+        last = atomicAdd(p.ticket, 1u) == static_cast<uint32_t>(step) - 1u;
     }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if constexpr (kPolicy) block_sum<kLongThreads>(p.row_loss, in.rows, p.scale, p.loss);
+    else pairs_by_warps(p, kLongThreads / 32);
+    if (threadIdx.x == 0) *p.ticket = 0u;
 }
 
 // Margins, losses and the rows' coefficients: a CTA a pair.
@@ -624,33 +687,13 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const __grid_c
         if (threadIdx.x == 0) *p.loss = 0.f;
         return;
     }
-    const PrefPair q = pairs.p[blockIdx.x];
-    const int rows = q.chosen_rows + q.rejected_rows;
-    const auto row_of = [&](int i) -> int64_t { return i < q.chosen_rows ? q.chosen + i : q.rejected + (i - q.chosen_rows); };
-    const auto counts = [&](int64_t r) { return p.in.labels[r] >= 0 && p.in.labels[r] < p.in.vocab; };
-    double sum = 0.0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < rows; i += kPairThreads) {
-        const int64_t r = row_of(i);
-        const double d = static_cast<double>(p.in.logp[r]) - (p.ref ? static_cast<double>(p.ref[r]) : 0.0);
-        if (counts(r)) sum += i < q.chosen_rows ? d : -d;
-    }
-    sum = cta_sum(sum, part);
-    const float h = static_cast<float>(static_cast<double>(p.beta) * sum);
-    const float e = p.smoothing;
-    // log sigmoid(h) = min(h, 0) - log1p(exp(-|h|)),  log sigmoid(-h) = log sigmoid(h) - h
-    const float small = expf(-fabsf(h)), tail = log1pf(small);
-    const float loss = h != h ? h : (1.f - e) * (tail - fminf(h, 0.f)) + e * (tail + fmaxf(h, 0.f));
-    const float s_neg = (h >= 0.f ? small : 1.f) / (1.f + small);   // sigmoid(-h)
-    const float s_pos = (h >= 0.f ? 1.f : small) / (1.f + small);
-    const float g = h != h ? h : p.scale * p.beta * (e * s_pos - (1.f - e) * s_neg);
-    for (int i = threadIdx.x; i < rows; i += kPairThreads) {
-        const int64_t r = row_of(i);
-        if (counts(r)) p.coef[r] = i < q.chosen_rows ? g : -g;
-    }
+    const PairRows pr{pairs.p[blockIdx.x]};
+    const double sum = cta_sum(margin_part(p, pr, threadIdx.x, kPairThreads), part);
+    const float2 lg = pair_loss(p, sum);
+    write_coefs(p, pr, lg.y, threadIdx.x, kPairThreads);
     if (threadIdx.x == 0) {
         p.margin[blockIdx.x] = static_cast<float>(sum);
-        p.pair_loss[blockIdx.x] = loss;
+        p.pair_loss[blockIdx.x] = lg.x;
         __threadfence();
         last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     }
@@ -769,23 +812,42 @@ int64_t row_vecs(const P& p) {
 }
 
 template <typename T, bool kPolicy, typename P>
-cudaError_t rows_of(const P& p, int sms, cudaStream_t stream) {
-    const int64_t vecs = row_vecs<T>(p);
-    if (vecs > kShortVecs) return run_long<T, kPolicy>(p, vecs, sms, stream);
+cudaError_t run_short(const P& p, int64_t vecs, cudaStream_t stream) {
     if (vecs <= kT) return run_short<T, 1, kPolicy>(p, stream);
     if (vecs <= 2 * kT) return run_short<T, 2, kPolicy>(p, stream);
     return run_short<T, 4, kPolicy>(p, stream);
 }
 
+template <typename T>
+cudaError_t stats(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, int sms, bool* paired, cudaStream_t stream) {
+    const int64_t vecs = row_vecs<T>(p);
+    if (vecs <= kShortVecs) return run_short<T, false>(p, vecs, stream);
+    PrefLong l;
+    static_cast<PrefParams&>(l) = p;
+    // one launch less: four pairs of some 80 rows of 32000 logits, 25 to 27 us a call against 27.6; larger batches keep a CTA
+    // a pair
+    l.fused = p.n_pairs <= kFewPairs && p.in.rows <= kFusedRows;
+    if (l.fused) std::copy(pairs.p, pairs.p + p.n_pairs, l.pairs.p);
+    *paired = l.fused != 0;
+    return run_long<T, false>(l, vecs, sms, stream);
+}
+
+template <typename T>
+cudaError_t policy_rows(const PolicyParams& p, int sms, bool* summed, cudaStream_t stream) {
+    const int64_t vecs = row_vecs<T>(p);
+    *summed = vecs > kShortVecs;
+    return *summed ? run_long<T, true>(p, vecs, sms, stream) : run_short<T, true>(p, vecs, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_loss_stats(const PrefParams& p, int sms, cudaStream_t stream) {
-    return p.in.f32 ? rows_of<float, false>(p, sms, stream) : rows_of<uint16_t, false>(p, sms, stream);
+cudaError_t launch_loss_stats(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, int sms, bool* paired, cudaStream_t stream) {
+    *paired = false;
+    return p.in.f32 ? stats<float>(p, pairs, sms, paired, stream) : stats<uint16_t>(p, pairs, sms, paired, stream);
 }
 
 cudaError_t launch_policy_rows(const PolicyParams& p, int sms, bool* summed, cudaStream_t stream) {
-    *summed = (p.in.f32 ? row_vecs<float>(p) : row_vecs<uint16_t>(p)) > kShortVecs;
-    return p.in.f32 ? rows_of<float, true>(p, sms, stream) : rows_of<uint16_t, true>(p, sms, stream);
+    return p.in.f32 ? policy_rows<float>(p, sms, summed, stream) : policy_rows<uint16_t>(p, sms, summed, stream);
 }
 
 cudaError_t launch_loss_pairs(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, cudaStream_t stream) {

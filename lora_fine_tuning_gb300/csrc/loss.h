@@ -48,6 +48,13 @@ struct PrefPairs {
 };
 constexpr int kFewPairs = 64;
 
+// For long rows: with few pairs and rows the pass over the logits also forms the pairs' losses (`fused`).
+struct PrefLong : PrefParams {
+    int32_t fused;
+    PrefPairs<kFewPairs> pairs;
+};
+constexpr int kFusedRows = 4096;
+
 struct PolicyParams {
     LossLogits in;
     const float *old_logp, *adv, *ref;   // rows; ref may be null
@@ -59,7 +66,8 @@ struct PolicyParams {
     DevCtl ctl;
 };
 
-cudaError_t launch_loss_stats(const PrefParams& p, int sms, cudaStream_t stream);
+// *paired: the kernel also formed the pairs' losses (launch_loss_pairs otherwise).
+cudaError_t launch_loss_stats(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, int sms, bool* paired, cudaStream_t stream);
 cudaError_t launch_loss_pairs(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, cudaStream_t stream);
 cudaError_t launch_loss_grad(const PrefParams& p, cudaStream_t stream);
 // *summed: the kernel also wrote the loss (launch_loss_sum otherwise).

@@ -113,8 +113,9 @@ lora_status pref_loss(const lora_logits* logits, const lora_pref_pair* pairs, in
     p.smoothing = label_smoothing;
     p.scale = scale;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
-    if (p.in.rows > 0) LORA_CUDA(timed(kLossRows, s, [&] { return launch_loss_stats(p, sms, s); }));
-    LORA_CUDA(timed(kLossPairs, s, [&] { return launch_loss_pairs(p, table, s); }));
+    bool paired = false;
+    if (p.in.rows > 0) LORA_CUDA(timed(kLossRows, s, [&] { return launch_loss_stats(p, table, sms, &paired, s); }));
+    if (!paired) LORA_CUDA(timed(kLossPairs, s, [&] { return launch_loss_pairs(p, table, s); }));
     if (p.in.rows > 0 && p.in.dz) LORA_CUDA(timed(kLossGrad, s, [&] { return launch_loss_grad(p, s); }));
     return LORA_OK;
 }

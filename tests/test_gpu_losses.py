@@ -311,3 +311,14 @@ def test_offsets_past_32_bits(vocab):
     got = api.policy_loss(z, y, old, adv, dlogits=z)                     # in place
     assert torch.allclose(got[0], want[0], rtol=1e-4)
     near(z[rows - n:], want[2].double().cpu(), grad_tol(torch.bfloat16))
+
+
+@pytest.mark.parametrize("n_pairs,rows", [(0, 9), (1, 300), (19, 200), (64, 200), (65, 200), (300, 700)])
+def test_long_rows_with_few_and_many_pairs(n_pairs, rows):
+    """Rows of a vocabulary beyond a CTA's registers: the pairs by the pass over the logits, or by a kernel of their own."""
+    z, y, noise = inputs(rows, 20001, torch.bfloat16, seed=n_pairs)
+    each = rows // max(1, 2 * n_pairs)
+    pairs = [(2 * i * each, (2 * i + 1) * each, each, each - (i % 2 if each > 1 else 0)) for i in range(n_pairs)]
+    first = check_pref(z, y, pairs, noise[0].contiguous())
+    again = check_pref(z, y, pairs, noise[0].contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
