@@ -477,7 +477,7 @@ const char* lora_status_string(lora_status s);
  * 1 finalize S, 2 forward GEMM, 3 dS/dB, 4 finalize dS/dB, 5 backward GEMM,
  * 6 dA, 7 finalize dA, 8 memset (gradients of adapters that own no rows),
  * 9-12 DoRA (U, norm, dZ, dmag), 13-17 attention
- * (forward, joining of split rows, dQ, dK and dV, unused rows),
+ * (forward, joining of what was split over SMs, dQ, dK and dV, unused rows),
  * 18-21 losses (rows, pairs, gradient, sum), 22 AdamW.  When kind 6 runs on the library's side
  * stream beside the backward GEMM, its event pair spans from the fork to its
  * end.
