@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -279,9 +280,15 @@ def dora_bwd(dY, X, W, A, B, S_saved, Y, mag, g_saved, alpha: float, p: float, s
 # packed causal attention
 # ---------------------------------------------------------------------------------------------------------------
 
-_STREAM_WS: dict = {}
+class _Workspaces(threading.local):
+    """A host thread's cached workspaces.  A call is several launches that hand results to each other through its
+    workspace, and the launches of two threads on one stream may interleave."""
+
+    def __init__(self):
+        self.cached = {}
 
 
+_WORKSPACES = _Workspaces()
 _GRAIN = 1 << 20   # bytes: a slightly larger batch then needs no new workspace
 
 
@@ -304,14 +311,14 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.index)
 
     def workspace(self, kind: str, size: int) -> torch.Tensor:
-        """A cached workspace of this stream (calls on different streams may overlap), zeroed when it is made."""
-        key = (kind, self.index, self.handle)
-        ws = _STREAM_WS.get(key)
+        """A workspace cached for the calls of this thread on this stream, zeroed when it is made."""
+        cached, key = _WORKSPACES.cached, (kind, self.index, self.handle)
+        ws = cached.get(key)
         if ws is None or ws.numel() < size:
             ws = self.empty(-(-size // _GRAIN) * _GRAIN, torch.uint8)
             with torch.cuda.stream(self.stream):
                 ws.zero_()
-            _STREAM_WS[key] = ws
+            cached[key] = ws
         return ws
 
 

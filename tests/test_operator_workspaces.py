@@ -1,0 +1,52 @@
+"""Which workspace a call of attention or a loss gets when none is given, without a GPU: memory and streams are stand-ins,
+and nothing is launched.
+
+A workspace is what several launches of one call hand each other, so no two calls that may overlap share one: not those of
+two host threads on one stream, whose launches may interleave.
+"""
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from lora_fine_tuning_gb300 import api  # noqa: E402
+
+
+@pytest.fixture
+def on():
+    """Stands for a call on stream 7 of device 0."""
+    class On(api._On):
+        def __init__(self, handle=7):
+            self.index, self.stream, self.handle = 0, None, handle
+
+        def empty(self, shape, dtype):
+            return torch.full((shape,) if isinstance(shape, int) else shape, 7, dtype=dtype)   # not zero by itself
+
+    return On
+
+
+def test_a_threads_calls_on_one_stream_share_one(on):
+    a = on().workspace("attn", 1000)
+    assert a.numel() >= 1000 and not a.count_nonzero()
+    assert on().workspace("attn", 900) is a and on(7).workspace("attn", 1000) is a
+    assert on(8).workspace("attn", 1000) is not a and on().workspace("loss", 1000) is not a
+    larger = on().workspace("attn", 5 << 20)
+    assert larger.numel() >= 5 << 20 and on().workspace("attn", 1000) is larger
+
+
+def test_threads_do_not_share(on):
+    mine, theirs, wait = on().workspace("attn", 1000), [], threading.Barrier(4)
+
+    def work():
+        wait.wait(10)   # all alive at once
+        theirs.append(on().workspace("attn", 1000))
+        wait.wait(10)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len({t.data_ptr() for t in theirs + [mine]}) == 5
+    assert on().workspace("attn", 1000) is mine
