@@ -290,6 +290,7 @@ class _Workspaces(threading.local):
 
 _WORKSPACES = _Workspaces()
 _GRAIN = 1 << 20   # bytes: a slightly larger batch then needs no new workspace
+_WS_HEAD = 256     # bytes that are zero before a workspace's first use; the rest is scratch
 
 
 class _On:
@@ -310,8 +311,21 @@ class _On:
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.index)
 
+    def capturing(self) -> bool:
+        if self.stream is None:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(self.stream):
+            return torch.cuda.is_current_stream_capturing()
+
     def workspace(self, kind: str, size: int) -> torch.Tensor:
-        """A workspace cached for the calls of this thread on this stream, zeroed when it is made."""
+        """The workspace of a call that was given none: cached for the calls of this thread on this stream.  A call that is
+        being captured gets memory of its graph's own pool instead, zeroed by the graph before each use: a cached
+        workspace may be replaced by a larger one while the graph lives, and calls outside the graph use it, too."""
+        if self.capturing():
+            ws = self.empty(size, torch.uint8)
+            with torch.cuda.stream(self.stream):
+                ws[:_WS_HEAD].zero_()
+            return ws
         cached, key = _WORKSPACES.cached, (kind, self.index, self.handle)
         ws = cached.get(key)
         if ws is None or ws.numel() < size:

@@ -2,7 +2,8 @@
 and nothing is launched.
 
 A workspace is what several launches of one call hand each other, so no two calls that may overlap share one: not those of
-two host threads on one stream, whose launches may interleave.
+two host threads on one stream (their launches may interleave), and not a captured call and a later one (the graph runs
+again whenever it is replayed).
 """
 import threading
 
@@ -14,15 +15,24 @@ from lora_fine_tuning_gb300 import api  # noqa: E402
 
 
 @pytest.fixture
-def on():
-    """Stands for a call on stream 7 of device 0."""
+def on(monkeypatch):
+    """Stands for a call on stream 7 of device 0; `on.captures` says whether that stream is being captured."""
     class On(api._On):
+        captures = False
+        made = []
+
         def __init__(self, handle=7):
             self.index, self.stream, self.handle = 0, None, handle
 
         def empty(self, shape, dtype):
-            return torch.full((shape,) if isinstance(shape, int) else shape, 7, dtype=dtype)   # not zero by itself
+            t = torch.full((shape,) if isinstance(shape, int) else shape, 7, dtype=dtype)   # memory is not zero by itself
+            On.made.append(t)
+            return t
 
+        def capturing(self):
+            return On.captures
+
+    On.made = []
     return On
 
 
@@ -50,3 +60,21 @@ def test_threads_do_not_share(on):
         t.join()
     assert len({t.data_ptr() for t in theirs + [mine]}) == 5
     assert on().workspace("attn", 1000) is mine
+
+
+def test_a_captured_call_has_its_own(on):
+    """Zeroed by the graph itself, whatever ran before; neither kept for later calls nor taken from earlier ones."""
+    eager = on().workspace("loss", 1000)
+    on.captures = True
+    first, second = on().workspace("loss", 1000), on().workspace("loss", 1000)
+    for ws in (first, second):
+        assert ws is not eager and ws.numel() >= 1000 and not ws[:256].count_nonzero()
+    assert first.data_ptr() != second.data_ptr()
+    on.captures = False
+    assert on().workspace("loss", 1000) is eager
+    other = on(9)
+    on.captures = True
+    other.workspace("loss", 1000)
+    on.captures = False
+    made = len(on.made)
+    assert on(9).workspace("loss", 1000) is not None and len(on.made) == made + 1   # the first outside capture
