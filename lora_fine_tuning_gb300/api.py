@@ -311,6 +311,17 @@ class _On:
         with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.index)
 
+    def check(self, name: str, t: torch.Tensor) -> None:
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{self.index}")
+
+    def given(self, ws: torch.Tensor) -> torch.Tensor:
+        """A workspace of the caller's."""
+        self.check("ws", ws)
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        return ws
+
     def capturing(self) -> bool:
         if self.stream is None:
             return torch.cuda.is_current_stream_capturing()
@@ -363,10 +374,11 @@ def attn_seqs(seqs) -> AttnSeqs:
     return AttnSeqs([(s[0], s[1], s[0], s[1]) if len(s) == 2 else s for s in seqs])
 
 
-def _heads(name: str, t: torch.Tensor, rows: int, heads: int, d: int):
+def _heads(on: _On, name: str, t: torch.Tensor, rows: int, heads: int, d: int):
     """Checks one rows x heads x head_dim operand.  Returns its strides (row, head)."""
     if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    on.check(name, t)
     if t.shape != (rows, heads, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
     row, head, inner = t.stride()
@@ -397,9 +409,10 @@ def _attn_sizes(Q, K):
     return rows, k_rows, heads, kv_heads, d
 
 
-def _check_lse(lse, q_rows: int, q_heads: int) -> None:
+def _check_lse(on: _On, lse, q_rows: int, q_heads: int) -> None:
     if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (q_rows, q_heads):
         raise ValueError(f"lse must be a contiguous CUDA float32 tensor of shape {(q_rows, q_heads)}")
+    on.check("lse", lse)
 
 
 def attn_fwd(Q, K, V, seqs, *, scale: Optional[float] = None, O=None, lse=None, ws=None, stream=None):
@@ -414,11 +427,10 @@ def attn_fwd(Q, K, V, seqs, *, scale: Optional[float] = None, O=None, lse=None, 
     if lse is None:
         lse = on.empty((rows, heads), torch.float32)
     else:
-        _check_lse(lse, rows, heads)
-    shape = _attn_shape(sizes, scale, _heads("Q", Q, rows, heads, d) + _heads("K", K, k_rows, kv_heads, d) +
-                        _heads("V", V, k_rows, kv_heads, d) + _heads("O", O, rows, heads, d) + _NO_STRIDES)
-    if ws is None:
-        ws = on.workspace("attn", attn_workspace_size(rows, heads))
+        _check_lse(on, lse, rows, heads)
+    shape = _attn_shape(sizes, scale, _heads(on, "Q", Q, rows, heads, d) + _heads(on, "K", K, k_rows, kv_heads, d) +
+                        _heads(on, "V", V, k_rows, kv_heads, d) + _heads(on, "O", O, rows, heads, d) + _NO_STRIDES)
+    ws = on.workspace("attn", attn_workspace_size(rows, heads)) if ws is None else on.given(ws)
     st = native.lib().attn_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, seqs.array, len(seqs.seqs), O.data_ptr(),
                                lse.data_ptr(), ws.data_ptr(), ws.numel(), on.handle)
     if st:
@@ -440,11 +452,11 @@ def attn_bwd(dO, Q, K, V, O, lse, seqs, *, scale: Optional[float] = None, dQ=Non
         dK = on.empty(kv, torch.bfloat16)
     if dV is None:
         dV = on.empty(kv, torch.bfloat16)
-    _check_lse(lse, rows, heads)
-    shape = _attn_shape(sizes, scale, _heads("Q", Q, *q) + _heads("K", K, *kv) + _heads("V", V, *kv) + _heads("O", O, *q) +
-                        _heads("dO", dO, *q) + _heads("dQ", dQ, *q) + _heads("dK", dK, *kv) + _heads("dV", dV, *kv))
-    if ws is None:
-        ws = on.workspace("attn", attn_workspace_size(rows, heads))
+    _check_lse(on, lse, rows, heads)
+    shape = _attn_shape(sizes, scale, _heads(on, "Q", Q, *q) + _heads(on, "K", K, *kv) + _heads(on, "V", V, *kv) +
+                        _heads(on, "O", O, *q) + _heads(on, "dO", dO, *q) + _heads(on, "dQ", dQ, *q) +
+                        _heads(on, "dK", dK, *kv) + _heads(on, "dV", dV, *kv))
+    ws = on.workspace("attn", attn_workspace_size(rows, heads)) if ws is None else on.given(ws)
     st = native.lib().attn_bwd(dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), shape,
                                seqs.array, len(seqs.seqs), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
                                ws.numel(), on.handle)
@@ -481,15 +493,17 @@ def pref_pairs(pairs) -> PrefPairs:
 _DTYPES = {torch.bfloat16: native.BF16, torch.float32: native.F32}
 
 
-def _check_rows(name: str, t, rows: int, dtype) -> None:
+def _check_rows(on: _On, name: str, t, rows: int, dtype) -> None:
     if t is None:
         return
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.shape != (rows,):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} vector of {rows}")
+    on.check(name, t)
 
 
-def _given_f32(name: str, t: torch.Tensor, n: int) -> torch.Tensor:
+def _given_f32(on: _On, name: str, t: torch.Tensor, n: int) -> torch.Tensor:
     _check_f32(name, t, n)
+    on.check(name, t)
     return t
 
 
@@ -500,12 +514,12 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
     rows, vocab = logits.shape
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of a row must be contiguous")
-    _check_rows("labels", labels, rows, torch.int64)
+    _check_rows(on, "labels", labels, rows, torch.int64)
     ld = d_ld = logits.stride(0) if rows > 1 else vocab
     if logp is None:
         logp = on.empty((rows,), torch.float32)
     else:
-        _check_rows("logp", logp, rows, torch.float32)
+        _check_rows(on, "logp", logp, rows, torch.float32)
     if dlogits is None and want_grad:
         # rows as far apart as the logits' own: whole 16-byte vectors are then stored as they were loaded
         if ld == vocab:
@@ -516,6 +530,7 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
         if dlogits.dtype != logits.dtype or not dlogits.is_cuda or dlogits.shape != logits.shape or \
                 (vocab > 1 and dlogits.stride(1) != 1):
             raise ValueError(f"dlogits must be a CUDA {logits.dtype} matrix of shape {tuple(logits.shape)}, rows contiguous")
+        on.check("dlogits", dlogits)
         if rows > 1:
             d_ld = dlogits.stride(0)
     g = native.Logits(logits.data_ptr(), _ptr(dlogits), rows, vocab, ld, d_ld, labels.data_ptr(), logp.data_ptr(),
@@ -538,10 +553,10 @@ def pref_loss(logits, labels, pairs, ref_logp=None, *, beta: float = 0.1, label_
     pairs = pref_pairs(pairs)
     on = _On(logits, stream)
     g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
-    _check_rows("ref_logp", ref_logp, logits.shape[0], torch.float32)
-    loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
-    margins = on.empty((len(pairs),), torch.float32) if margins is None else _given_f32("margins", margins, len(pairs))
-    ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
+    _check_rows(on, "ref_logp", ref_logp, logits.shape[0], torch.float32)
+    loss = on.empty((), torch.float32) if loss is None else _given_f32(on, "loss", loss, 1)
+    margins = on.empty((len(pairs),), torch.float32) if margins is None else _given_f32(on, "margins", margins, len(pairs))
+    ws = on.workspace("loss", loss_workspace_size(logits.shape[0])) if ws is None else on.given(ws)
     st = native.lib().pref_loss(g, pairs.array, len(pairs), _ptr(ref_logp), float(beta),
                                 float(label_smoothing), float(scale), _ptr(loss), _ptr(margins), _ptr(ws), ws.numel(),
                                 on.handle)
@@ -558,9 +573,9 @@ def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, *, clip_low
     on = _On(logits, stream)
     g, logp, dlogits = _logits(on, logits, labels, logp, dlogits, want_grad)
     for name, t in (("old_logp", old_logp), ("advantages", advantages), ("ref_logp", ref_logp)):
-        _check_rows(name, t, logits.shape[0], torch.float32)
-    loss = on.empty((), torch.float32) if loss is None else _given_f32("loss", loss, 1)
-    ws = ws if ws is not None else on.workspace("loss", loss_workspace_size(logits.shape[0]))
+        _check_rows(on, name, t, logits.shape[0], torch.float32)
+    loss = on.empty((), torch.float32) if loss is None else _given_f32(on, "loss", loss, 1)
+    ws = on.workspace("loss", loss_workspace_size(logits.shape[0])) if ws is None else on.given(ws)
     st = native.lib().policy_loss(g, _ptr(old_logp), _ptr(advantages), _ptr(ref_logp), float(clip_low),
                                   float(clip_high), float(kl_coef), float(scale), _ptr(loss), _ptr(ws), ws.numel(),
                                   on.handle)
@@ -654,6 +669,8 @@ def adamw_step(tensors, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
         raise ValueError(f"tensors are on cuda:{tensors.device}, the current device is cuda:{index}")
     if grad_scale is not None:
         _check_f32("grad_scale", grad_scale, 1)
+        if grad_scale.get_device() != index:
+            raise ValueError(f"grad_scale is on {grad_scale.device}, the call runs on cuda:{index}")
     st = native.lib().adamw_step(tensors.array, len(tensors), float(lr), float(beta1), float(beta2), float(eps),
                                  float(weight_decay), int(step), _ptr(grad_scale),
                                  _current_stream(index) if stream is None else stream.cuda_stream)

@@ -15,22 +15,22 @@ if not torch.cuda.is_available():  # pragma: no cover
 from tests.test_gpu_threads import attention, policy, preference  # noqa: E402
 
 
-def calls():
-    """name -> (two calls with inputs of their own, a larger one)"""
-    return {
-        "preference, long rows": (preference(40, 32001, torch.bfloat16, 2, 0), preference(24, 40000, torch.float32, 3, 1),
-                                  preference(4000, 33000, torch.bfloat16, 40, 2)),
-        "preference, short rows": (preference(40, 1000, torch.bfloat16, 2, 3), preference(24, 900, torch.float32, 3, 4),
-                                   preference(200000, 64, torch.bfloat16, 70, 5)),
-        "policy": (policy(40, 32001, torch.bfloat16, 6), policy(24, 50001, torch.float32, 7), policy(250000, 64, torch.bfloat16, 8)),
-        "attention": (attention([(0, 1, 0, 5000), (1, 20, 5000, 3000)], 8, 2, 64, 9), attention([(0, 2000, 0, 2000)], 8, 1, 64, 10),
-                      attention([(0, 30000, 0, 30000)], 16, 4, 64, 11)),
-    }
+# name -> two calls with inputs of their own, and a larger one
+CALLS = {
+    "preference, long rows": lambda: (preference(40, 32001, torch.bfloat16, 2, 0), preference(24, 40000, torch.float32, 3, 1),
+                                      preference(4000, 33000, torch.bfloat16, 40, 2)),
+    "preference, short rows": lambda: (preference(40, 1000, torch.bfloat16, 2, 3), preference(24, 900, torch.float32, 3, 4),
+                                       preference(200000, 64, torch.bfloat16, 70, 5)),
+    "policy": lambda: (policy(40, 32001, torch.bfloat16, 6), policy(24, 50001, torch.float32, 7),
+                       policy(250000, 64, torch.bfloat16, 8)),
+    "attention": lambda: (attention([(0, 1, 0, 5000), (1, 20, 5000, 3000)], 8, 2, 64, 9),
+                          attention([(0, 2000, 0, 2000)], 8, 1, 64, 10), attention([(0, 30000, 0, 30000)], 16, 4, 64, 11)),
+}
 
 
-@pytest.mark.parametrize("name", list(calls().keys()) if torch.cuda.is_available() else [])
+@pytest.mark.parametrize("name", list(CALLS))
 def test_two_graphs_without_a_workspace(name):
-    first, second, larger = calls()[name]
+    first, second, larger = CALLS[name]()
     want = [[x.clone() for x in f()] for f in (first, second)]
     graphs, outs = [], []
     for f in (first, second):
