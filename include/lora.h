@@ -387,7 +387,8 @@ lora_status policy_loss(const lora_logits* logits, const float* old_logp, const 
  *    parameter: it is updated and param is its rounding.  Without it a bf16 param is read, updated and rounded.
  *  - state_bits 32: m and v are fp32.  state_bits 8: m and sqrt(v) are e4m3 codes, one byte each, with an fp32 scale for
  *    every 256 consecutive values (m_scale, v_scale: ceil(n / 256) each; value = code * scale; scale = largest / 448, a
- *    block whose largest value is below 2^-100 is held as zeros; a positive sqrt(v) gets at least the smallest code).
+ *    block whose largest value is below 2^-100 is held as zeros; a positive sqrt(v) gets at least the smallest code; a
+ *    value that is infinite or NaN is held as NaN, and the scale is that of the block's finite values).
  *    States start as zeros (codes and scales) in either form.
  *  - tensors is a HOST array, read before the call returns; pointers are 16-byte aligned (scales: 4), tensors do not
  *    overlap.  grad_scale (optional): one fp32 on the device, for example a clipping factor.  step counts from 1, eps is

@@ -147,15 +147,26 @@ __device__ __forceinline__ float max_abs(float t, float2 x) {
     return r;
 }
 
-// One block (this warp's 256 values; x is 0 past the tensor's end) in 8 bits.  kPositive: x is not negative.
+// One block (this warp's 256 values; x is 0 past the tensor's end) in 8 bits.  kPositive: x is not negative.  An infinite
+// or NaN value gets the NaN code and has no part in the scale: the rest of its block keeps its states.
 template <bool kPositive>
-__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int64_t at, int left, const F2 (&x)[4]) {
+__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int64_t at, int left, F2 (&x)[4]) {
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) most = max_abs(most, parts(x[i]));
     // the sign is clear: values order like their bits, infinity and NaN above the rest
     float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
-    if (!(top >= kTiny)) top = 0.f;
+    if (__float_as_uint(top) >= 0x7F800000u) {   // in the whole warp alike; 1.3 us of the 94 of a model's adapters
+        most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = fma2(x[i], f2(0.f, 0.f), x[i]);   // infinities become NaN: their conversion is the largest code
+            const float2 q = parts(x[i]);
+            most = fmaxf(most, fmaxf(fabsf(q.x), fabsf(q.y)));   // a NaN counts for nothing
+        }
+        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+    }
+    if (top < kTiny) top = 0.f;
     const float f = top > 0.f ? __fmul_rn(__frcp_rn(top), kE4m3Max) : 0.f;
     float2 y[4];
     float least = kE4m3Max;

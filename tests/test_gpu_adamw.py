@@ -264,3 +264,41 @@ def test_offsets_past_32_bits(bits):
         # the first block after the small tensor's end shares its scale with zeros: the last whole block is compared
         assert torch.equal(x[:4096], getattr(small[0], name)[:4096]) and torch.equal(x[n - k:], getattr(small[1], name))
         assert not x[k:n - k].count_nonzero()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("pdtype,gdtype,master", [(torch.float32, torch.float32, False), (torch.bfloat16, torch.bfloat16, True)])
+def test_8_bit_states_beside_a_value_that_is_not_finite(bad, pdtype, gdtype, master):
+    """A gradient that is infinite or NaN spoils its own value, as with fp32 states: the others of its block keep the
+    states and parameters, bit by bit, that they have where that gradient is zero."""
+    n, at = 256 + 256 + 100, (9, 300, 600)
+    g = (torch.randn(4, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0)) * 1e-3).to(gdtype)
+    g[:, at] = 0
+    good, spoiled = (api.adamw_tensor(torch.ones(n, device="cuda").to(pdtype), torch.zeros(n, device="cuda").to(gdtype), bits=8,
+                                      master=master) for _ in range(2))
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[list(at)] = False
+    for step in range(4):
+        for t in (good, spoiled):
+            t.grad.copy_(g[step])
+        if step == 1:
+            spoiled.grad[list(at)] = bad
+        for t in (good, spoiled):
+            api.adamw_step([t], lr=1e-3, step=step + 1)
+        for name in ("param", "m", "v", "master"):
+            a, b = getattr(good, name), getattr(spoiled, name)
+            assert a is None or torch.equal(a[others], b[others]), (name, step)
+        assert torch.equal(good.m_scale, spoiled.m_scale) and torch.equal(good.v_scale, spoiled.v_scale)
+        if step:
+            assert bool(torch.isnan(spoiled.param[~others]).all())
+            for codes in (spoiled.m, spoiled.v):
+                assert bool(torch.isnan(codes.view(torch.float8_e4m3fn).float()[~others]).all())
+
+
+def test_8_bit_block_without_a_finite_value():
+    t = api.adamw_tensor(torch.ones(512, device="cuda"), torch.full((512,), 1e-3, device="cuda"), bits=8)
+    t.grad[:256] = math.nan
+    for step in (1, 2):
+        api.adamw_step([t], lr=1e-3, step=step)
+    assert bool(torch.isnan(t.param[:256]).all()) and bool(torch.isfinite(t.param[256:]).all())
+    assert bool(torch.isnan(t.m[:256].view(torch.float8_e4m3fn).float()).all()) and t.m_scale[:1].count_nonzero() == 0
