@@ -363,6 +363,7 @@ size_t loss_workspace_size(int64_t rows);
 /* Preference loss of paired log ratios:
  *   margin_i = sum_{t in chosen_i} (logp_t - ref_t) - sum_{t in rejected_i} (logp_t - ref_t),  h_i = beta margin_i
  *   *loss = scale * sum_i [ -(1 - label_smoothing) log sigmoid(h_i) - label_smoothing log sigmoid(-h_i) ]
+ * (a term whose weight is zero counts nothing, an infinite one too: the margin of a label of probability 0 is infinite).
  * ref_logp (rows, fp32): the reference policy's log p of each label, as this call returns logp when it runs on the
  * model without its adapters; NULL for none (zeros).  pairs is a HOST array, read before the call returns; no row may
  * belong to two responses (LORA_ETABLE).  margins receives margin_i (n_pairs, fp32). */

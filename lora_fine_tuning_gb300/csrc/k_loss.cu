@@ -353,7 +353,8 @@ __device__ __forceinline__ float2 pair_loss(const PrefParams& p, double margin) 
     const float e = p.smoothing;
     // log sigmoid(h) = min(h, 0) - log1p(exp(-|h|)),  log sigmoid(-h) = log sigmoid(h) - h
     const float small = expf(-fabsf(h)), tail = log1pf(small);
-    const float loss = h != h ? h : (1.f - e) * (tail - fminf(h, 0.f)) + e * (tail + fmaxf(h, 0.f));
+    // an infinite h (a label of probability 0) leaves out the term whose weight is zero: 0 infinity would be a NaN
+    const float loss = h != h ? h : (e < 1.f ? (1.f - e) * (tail - fminf(h, 0.f)) : 0.f) + (e > 0.f ? e * (tail + fmaxf(h, 0.f)) : 0.f);
     const float s_neg = (h >= 0.f ? small : 1.f) / (1.f + small);   // sigmoid(-h)
     const float s_pos = (h >= 0.f ? 1.f : small) / (1.f + small);
     const float g = h != h ? h : p.scale * p.beta * (e * s_pos - (1.f - e) * s_neg);

@@ -322,3 +322,27 @@ def test_long_rows_with_few_and_many_pairs(n_pairs, rows):
     first = check_pref(z, y, pairs, noise[0].contiguous())
     again = check_pref(z, y, pairs, noise[0].contiguous())
     assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("vocab,n_pairs", [(300, 3), (20001, 3), (20001, 70)])
+def test_labels_of_probability_zero(vocab, n_pairs):
+    """A label outside a restricted vocabulary has log p = -inf and its pair an infinite margin.  The loss is that of the limit:
+    a term whose weight is zero (no smoothing, or nothing but it) counts nothing, however large; nothing becomes NaN."""
+    z, y, noise = inputs(4 * n_pairs, vocab, torch.float32, seed=vocab, ignored=0.0)
+    pairs = [(4 * i, 4 * i + 2, 2, 2) for i in range(n_pairs)]
+    for side, sign in ((0, -1.0), (2, 1.0)):
+        x = z.clone()
+        x[4 + side, y[4 + side]] = -math.inf          # of the second pair
+        for eps in (0.0, 1.0, 0.25):
+            loss, logp, margin, dz = api.pref_loss(x, y, pairs, noise[0].contiguous(), beta=0.3, label_smoothing=eps)
+            assert float(margin[1]) == sign * math.inf and float(logp[4 + side]) == -math.inf
+            assert torch.isfinite(dz).all()
+            h = 0.3 * torch.cat([margin[:1], margin[2:]]).double().cpu()
+            sp = torch.nn.functional.softplus
+            rest = float(((1 - eps) * sp(-h) + eps * sp(h)).sum())
+            weight = eps if side else 1 - eps            # of the term that grows
+            if weight:
+                assert float(loss) == math.inf
+            else:
+                assert abs(float(loss) - rest) <= 1e-5 * rest + 1e-6
+                assert not dz[4:8].count_nonzero()
