@@ -203,15 +203,18 @@ int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
 
 AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
 
-// Unused rows that an item of the sequence before them is asked to fill at most; a batch with longer gaps between its
-// sequences gets a kernel of its own for them.
-constexpr int kMaxItemGap = 4096;
+// Unused rows, times the heads of an item, that an item fills at most; a batch with more of them gets a kernel for them.  The
+// items write them before their first turn, the kernel costs a launch.  us, by the items and by the kernel, 32/8 heads of
+// 128: 2000 tokens with 512, 1024, 2048 rows after them (33, 65, 130 an item) 44.3, 46.3, 51.8 and 44.3, 45.0, 46.1, backward
+// 131, 133, 138 and 130, 131, 133; 64 samples of 77 tokens every 128 rows (68) 50 and 44, backward 131 and 117; one token
+// over 300 keys in a buffer of 8192 rows (32768) 1120 and 23.
+constexpr int64_t kItemFill = 32;
 
 // Gives every unused row of an output with `rows` rows to the items of c (numbered already): the rows after a sequence
-// to its own, those before the first and after the last to all.  False if the rows need a launch of their own.  `first`
-// and `len` read a sequence's place.
+// to its own tiles, `tile` rows each, those before the first and after the last to all.  False if the rows need a launch of
+// their own.  `heads`: of an item; `first` and `len` read a sequence's place.
 template <class First, class Len>
-bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, First first, Len len) {
+bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, int tile, int heads, First first, Len len) {
     const auto none = [&c] {
         c.sh.lead = c.sh.trail0 = c.sh.trail = 0;
         for (int i = 0; i < c.n; ++i) c.order.s[i].gap = 0;
@@ -233,12 +236,14 @@ bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, Fir
             c.sh.trail0 = from;
             c.sh.trail = to - from;
         } else {
-            if (to - from > kMaxItemGap) return none();
             const auto e = std::lower_bound(ends, ends + m, std::make_pair(from, int32_t{-1}));
             if (e == ends + m || e->first != from) return none();
-            c.order.s[e->second].gap = to - from;
+            AttnSeq& q = c.order.s[e->second];
+            if (static_cast<int64_t>(to - from) * heads > kItemFill * tiles_of(len(q), tile)) return none();
+            q.gap = to - from;
         }
     }
+    if ((static_cast<int64_t>(c.sh.lead) + c.sh.trail) * heads > kItemFill * c.sh.items) return none();
     return true;
 }
 
@@ -287,7 +292,8 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, sms, &most, &split_tiles) : 0;
     if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q_items(q, c.sh, most) : attn_query_tiles(q, c.sh); })))
         return st;
-    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, [](const AttnSeq& q) { return q.q0; },
+                    [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
     }
     if (c.sh.items == 0) return LORA_OK;
@@ -360,7 +366,8 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     p.dV = mv;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }))) return st;
-    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, [](const AttnSeq& q) { return q.q0; }, [](const AttnSeq& q) { return q.ql; })) {
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, [](const AttnSeq& q) { return q.q0; },
+                    [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
     }
     p.sh = c.sh;
@@ -378,7 +385,8 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes + delta_bytes(a.q_rows, a.q_heads));
     if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? kv_items(q, c.sh, p.most) : key_tiles(q); })))
         return st;
-    if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, [](const AttnSeq& q) { return q.k0; }, [](const AttnSeq& q) { return q.kl; })) {
+    if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, kAttnTile, 1, [](const AttnSeq& q) { return q.k0; },
+                    [](const AttnSeq& q) { return q.kl; })) {
         if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
     }
     p.sh = c.sh;

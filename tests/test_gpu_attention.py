@@ -425,3 +425,36 @@ def test_long_rows_on_few_heads(lengths, hq, hkv, d, layout):
     assert off(O, got[0].double().cpu()) <= TOL and torch.equal(torch.isinf(lse), torch.isinf(got[1]))
     again = api.attn_fwd(Q, K, V, seqs)
     assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("rows,seqs,fills", [
+    (8192, [(0, 1, 0, 1)], 1), (5000, [(4999, 1, 4999, 1)], 1), (3000, [(1000, 300, 1000, 300)], 1),
+    (310, [(0, 300, 0, 300)], 0), (700, [(0, 1, 0, 1), (600, 1, 600, 1), (650, 50, 650, 50)], 1),
+    (600, [(0, 250, 0, 250), (256, 300, 256, 300)], 0)])
+def test_unused_rows_beside_few_tokens(rows, seqs, fills):
+    """Many unused rows are written by a kernel over all SMs, not by the few items of the sequences; a few cost no launch."""
+    Q, K, V, dO = inputs(rows, rows, 8, 2, 64, seed=rows)
+    O, dQ = torch.full_like(Q, 7), torch.full_like(Q, 7)
+    dK, dV = torch.full_like(K, 7), torch.full_like(V, 7)
+    lse = torch.full((rows, 8), 7.0, device="cuda")
+    native.timing_begin()
+    api.attn_fwd(Q, K, V, seqs, O=O, lse=lse)
+    torch.cuda.synchronize()
+    assert native.timing_end().get("attn_fill", (0, 0))[1] == fills
+    native.timing_begin()
+    api.attn_bwd(dO, Q, K, V, O, lse, seqs, dQ=dQ, dK=dK, dV=dV)
+    torch.cuda.synchronize()
+    assert native.timing_end().get("attn_fill", (0, 0))[1] == 2 * fills
+    check(Q, K, V, seqs, 0.125, dO, (O, lse, dQ, dK, dV))
+
+
+def test_no_sequence_in_a_large_buffer():
+    """Heads of 8 to 1024: a block of the kernel for unused rows has several rows at a time, or several rounds a row."""
+    for rows, hq, hkv, d in ((5000, 1, 1, 8), (700, 3, 1, 24), (40, 1024, 8, 16), (130, 40, 40, 128)):
+        Q, K, V, dO = inputs(rows, rows, hq, hkv, d)
+        O, dQ = torch.full_like(Q, 7), torch.full_like(Q, 7)
+        dK, dV = torch.full_like(K, 7), torch.full_like(V, 7)
+        lse = torch.full((rows, hq), 7.0, device="cuda")
+        api.attn_fwd(Q, K, V, [], O=O, lse=lse)
+        api.attn_bwd(dO, Q, K, V, O, lse, [], dQ=dQ, dK=dK, dV=dV)
+        assert bool((lse == -math.inf).all()) and not any(x.count_nonzero() for x in (O, dQ, dK, dV))
