@@ -367,7 +367,7 @@ __device__ __forceinline__ void write_coefs(const PrefParams& p, const PairRows&
     }
 }
 
-// All pairs by the warps of one CTA, a warp a pair, and the loss.
+// All pairs by the warps of one CTA, a warp a pair (there are no more pairs than warps), and the loss.
 __device__ __forceinline__ void pairs_by_warps(const PrefLong& p, int warps) {
     const int lane = threadIdx.x & 31;
     for (int q = threadIdx.x >> 5; q < p.n_pairs; q += warps) {
@@ -825,9 +825,13 @@ cudaError_t stats(const PrefParams& p, const PrefPairs<kLossMaxPairs>& pairs, in
     if (vecs <= kShortVecs) return run_short<T, false>(p, vecs, stream);
     PrefLong l;
     static_cast<PrefParams&>(l) = p;
-    // one launch less: four pairs of some 80 rows of 32000 logits, 25 to 27 us a call against 27.6; larger batches keep a CTA
-    // a pair
-    l.fused = p.n_pairs <= kFewPairs && p.in.rows <= kFusedRows;
+    // One launch less, but each pair is one warp's work, after the last row: it goes by the longest pair and by pairs a warp.  us of
+    // the statistics and the pairs' losses, fused and by a CTA a pair, rows of 32000 logits: 4 pairs of 20, 80, 128, 256, 512
+    // rows 15, 21, 23, 31, 48 and 19, 23, 26, 31, 44; one of 128, 512, 4096 17, 29, 128 and 19, 26, 78; 16 of 128 44 and 44;
+    // 64 of 8 29 and 25
+    int32_t longest = 0;
+    for (int i = 0; i < p.n_pairs; ++i) longest = std::max(longest, pairs.p[i].chosen_rows + pairs.p[i].rejected_rows);
+    l.fused = p.n_pairs <= kFusedPairs && longest <= kFusedPairRows;
     if (l.fused) std::copy(pairs.p, pairs.p + p.n_pairs, l.pairs.p);
     *paired = l.fused != 0;
     return run_long<T, false>(l, vecs, sms, stream);

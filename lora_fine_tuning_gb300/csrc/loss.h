@@ -48,12 +48,13 @@ struct PrefPairs {
 };
 constexpr int kFewPairs = 64;
 
-// For long rows: with few pairs and rows the pass over the logits also forms the pairs' losses (`fused`).
+// For long rows: with few and short pairs the pass over the logits also forms the pairs' losses (`fused`): a warp a pair.
+constexpr int kFusedPairs = 16;
+constexpr int kFusedPairRows = 128;
 struct PrefLong : PrefParams {
     int32_t fused;
-    PrefPairs<kFewPairs> pairs;
+    PrefPairs<kFusedPairs> pairs;
 };
-constexpr int kFusedRows = 4096;
 
 struct PolicyParams {
     LossLogits in;

@@ -346,3 +346,19 @@ def test_labels_of_probability_zero(vocab, n_pairs):
             else:
                 assert abs(float(loss) - rest) <= 1e-5 * rest + 1e-6
                 assert not dz[4:8].count_nonzero()
+
+
+@pytest.mark.parametrize("n_pairs,each,own", [(0, 0, 0), (1, 64, 0), (16, 64, 0), (16, 1, 0), (17, 5, 1), (1, 65, 1), (2, 700, 1),
+                                              (64, 3, 1)])
+def test_who_forms_the_pairs_of_long_rows(n_pairs, each, own):
+    """Few short pairs are formed by the pass over the logits, others by a kernel with a CTA a pair: a long pair is not left
+    to one warp.  The results are right either way."""
+    z, y, noise = inputs(max(2 * n_pairs * each, 5), 17000, torch.bfloat16, seed=n_pairs + each)
+    pairs = [(2 * i * each, (2 * i + 1) * each, each, each) for i in range(n_pairs)]
+    native.timing_begin()
+    got = check_pref(z, y, pairs, noise[0] * 0.3 - 5)
+    torch.cuda.synchronize()
+    launches = native.timing_end()
+    assert launches["loss_rows"][1] == 1 and launches.get("loss_pairs", (0, 0))[1] == own
+    again = api.pref_loss(z, y, pairs, noise[0] * 0.3 - 5, beta=0.3, label_smoothing=0.1, scale=0.5)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
