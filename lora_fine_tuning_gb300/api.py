@@ -521,11 +521,13 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
     else:
         _check_rows(on, "logp", logp, rows, torch.float32)
     if dlogits is None and want_grad:
-        # rows as far apart as the logits' own: whole 16-byte vectors are then stored as they were loaded
-        if ld == vocab:
+        # rows as far apart as the logits' own, and as far from a 16-byte boundary (a slice may start anywhere): whole
+        # vectors are then stored as they were loaded.  Else, 4096 rows of 50021 bf16 logits take 646 instead of 215 us.
+        skew = logits.data_ptr() % 16 // logits.element_size()
+        if ld == vocab and not skew:
             dlogits = on.empty((rows, vocab), logits.dtype)
         else:
-            dlogits = on.empty((max(rows, 1) * ld,), logits.dtype).as_strided((rows, vocab), (ld, 1))
+            dlogits = on.empty((max(rows, 1) * ld + skew,), logits.dtype).as_strided((rows, vocab), (ld, 1), skew)
     elif dlogits is not None:
         if dlogits.dtype != logits.dtype or not dlogits.is_cuda or dlogits.shape != logits.shape or \
                 (vocab > 1 and dlogits.stride(1) != 1):

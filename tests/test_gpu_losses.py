@@ -362,3 +362,18 @@ def test_who_forms_the_pairs_of_long_rows(n_pairs, each, own):
     assert launches["loss_rows"][1] == 1 and launches.get("loss_pairs", (0, 0))[1] == own
     again = api.pref_loss(z, y, pairs, noise[0] * 0.3 - 5, beta=0.3, label_smoothing=0.1, scale=0.5)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,ld", [(1003, 1003), (1003, 1009), (20001, 20001), (64, 64)])
+def test_gradients_lie_like_the_logits(vocab, ld, dtype):
+    """The gradient that a call allocates has the logits' strides and their place in a 16-byte vector, wherever a slice starts:
+    else it would be stored element by element."""
+    z, y, noise = inputs(20, vocab, dtype, seed=vocab, ld=ld)
+    for first in (0, 1, 3):
+        x, labels, n = z[first:], y[first:].contiguous(), noise[:, first:]
+        for dz in (check_policy(x, labels, n)[2], check_pref(x, labels, [(0, 8, 8, 8)], n[0].contiguous())[3]):
+            assert dz.stride() == x.stride() and dz.data_ptr() % 16 == x.data_ptr() % 16
+            assert dz.is_contiguous() == x.is_contiguous()
+    one = z[5:6]
+    assert check_policy(one, y[5:6].clamp(min=0).contiguous(), noise[:, 5:6])[2].shape == (1, vocab)
