@@ -298,10 +298,11 @@ class _On:
     memory to nobody else before that stream is done with it."""
     __slots__ = ("index", "stream", "handle")
 
-    def __init__(self, t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-        self.index = t.get_device()
-        if self.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    def __init__(self, t: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream]):
+        current = torch.cuda.current_device()
+        self.index = current if t is None else t.get_device()
+        if self.index != current:
+            raise ValueError(f"tensors are on {t.device}, the current device is cuda:{current}")
         self.stream = stream
         self.handle = _current_stream(self.index) if stream is None else stream.cuda_stream
 
@@ -337,6 +338,9 @@ class _On:
             with torch.cuda.stream(self.stream):
                 ws[:_WS_HEAD].zero_()
             return ws
+        return self.cached(kind, size)
+
+    def cached(self, kind: str, size: int) -> torch.Tensor:
         cached, key = _WORKSPACES.cached, (kind, self.index, self.handle)
         ws = cached.get(key)
         if ws is None or ws.numel() < size:
@@ -345,6 +349,11 @@ class _On:
                 ws.zero_()
             cached[key] = ws
         return ws
+
+    def public(self, kind: str, size: int) -> torch.Tensor:
+        if self.capturing():
+            raise RuntimeError("a captured call uses its graph's own workspace: make one before the capture and give it with ws=")
+        return self.cached(kind, size)
 
 
 # the handle of a device's current stream, without the objects of torch.cuda.current_stream (3 us of a call's 25)
@@ -469,6 +478,12 @@ def attn_workspace_size(q_rows: int, q_heads: int) -> int:
     return int(native.lib().attn_workspace_size(q_rows, q_heads))
 
 
+def attn_workspace(q_rows: int, q_heads: int, *, stream=None) -> torch.Tensor:
+    """The workspace of attn_fwd and attn_bwd calls that are given none: this thread's for the stream.  A kernel whose wait
+    ran out leaves its code there (lora_device_status).  A call with more rows or heads may replace it."""
+    return _On(None, stream).public("attn", attn_workspace_size(q_rows, q_heads))
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # losses on logits
 # ---------------------------------------------------------------------------------------------------------------
@@ -542,6 +557,11 @@ def _logits(on, logits, labels, logp, dlogits, want_grad):
 
 def loss_workspace_size(rows: int) -> int:
     return int(native.lib().loss_workspace_size(rows))
+
+
+def loss_workspace(rows: int, *, stream=None) -> torch.Tensor:
+    """The workspace of pref_loss and policy_loss calls that are given none, as attn_workspace() is attention's."""
+    return _On(None, stream).public("loss", loss_workspace_size(rows))
 
 
 def pref_loss(logits, labels, pairs, ref_logp=None, *, beta: float = 0.1, label_smoothing: float = 0.0,

@@ -78,3 +78,23 @@ def test_a_captured_call_has_its_own(on):
     on.captures = False
     made = len(on.made)
     assert on(9).workspace("loss", 1000) is not None and len(on.made) == made + 1   # the first outside capture
+
+
+def test_public_workspaces(on, monkeypatch):
+    """What a call without a workspace uses can be asked for its status; not during a capture, where each call has its own."""
+    class Sizes:
+        attn_workspace_size = staticmethod(lambda rows, heads: 4 * rows * heads)
+        loss_workspace_size = staticmethod(lambda rows: 4 * rows)
+
+    class On(on):
+        def __init__(self, t, stream):
+            super().__init__()
+
+    monkeypatch.setattr(api.native, "lib", lambda: Sizes)
+    monkeypatch.setattr(api, "_On", On)
+    assert api.attn_workspace(100, 8) is on().workspace("attn", 3200)
+    assert api.loss_workspace(100) is on().workspace("loss", 400)
+    on.captures = True
+    for f in (lambda: api.attn_workspace(100, 8), lambda: api.loss_workspace(100)):
+        with pytest.raises(RuntimeError, match="ws="):
+            f()
