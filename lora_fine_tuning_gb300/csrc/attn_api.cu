@@ -203,18 +203,20 @@ int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
 
 AttnMat mat(const lora_bf16* p, const lora_attn_strides& s) { return AttnMat{const_cast<uint16_t*>(p), s.row, s.head}; }
 
-// Unused rows, times the heads of an item, that an item fills at most; a batch with more of them gets a kernel for them.  The
-// items write them before their first turn, the kernel costs a launch.  us, by the items and by the kernel, 32/8 heads of
-// 128: 2000 tokens with 512, 1024, 2048 rows after them (33, 65, 130 an item) 44.3, 46.3, 51.8 and 44.3, 45.0, 46.1, backward
-// 131, 133, 138 and 130, 131, 133; 64 samples of 77 tokens every 128 rows (68) 50 and 44, backward 131 and 117; one token
-// over 300 keys in a buffer of 8192 rows (32768) 1120 and 23.
-constexpr int64_t kItemFill = 32;
+// Unused rows times heads that an item fills at most, and that an SM's two items of a moment fill at most over the call; a batch
+// with more of them gets a kernel for them.  The items write them before their first turn, eight in 0.27 us, the kernel
+// costs a launch of some 2 us.  us, by the items and by the kernel, 32/8 heads of 128: one sample of 77 tokens in 128 rows (68 an
+// item) 21 and 23; 14 samples of 152 to 1094 tokens on 128-row boundaries (91 of all) both directions 275 and 280; 2000 tokens with
+// 512, 1024, 2048 rows after them (54, 108, 216 of all) 43.7, 46.3, 51.8 and 43.2, 45.6, 46.4; 64 samples of 77 tokens every 128
+// rows (344 of all) 50 and 45, backward 132 and 121; one token over 300 keys in a buffer of 8192 rows 1116 and 23.
+constexpr int64_t kItemFill = 96;
 
 // Gives every unused row of an output with `rows` rows to the items of c (numbered already): the rows after a sequence
 // to its own tiles, `tile` rows each, those before the first and after the last to all.  False if the rows need a launch of
-// their own.  `heads`: of an item; `first` and `len` read a sequence's place.
+// their own.  `heads`: of an item, of `all_heads`; `first` and `len` read a sequence's place.
 template <class First, class Len>
-bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, int tile, int heads, First first, Len len) {
+bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, int tile, int heads, int all_heads, int sms,
+                First first, Len len) {
     const auto none = [&c] {
         c.sh.lead = c.sh.trail0 = c.sh.trail = 0;
         for (int i = 0; i < c.n; ++i) c.order.s[i].gap = 0;
@@ -228,8 +230,10 @@ bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, int
     for (int i = 0; i < c.n; ++i)
         if (len(c.order.s[i]) > 0) ends[m++] = {first(c.order.s[i]) + len(c.order.s[i]), i};
     std::sort(ends, ends + m);
+    int64_t unused = 0;
     for (int g = 0; g < n_gaps; ++g) {
         const int32_t from = gaps.from[g], to = gaps.to[g];
+        unused += to - from;
         if (from == 0) {
             c.sh.lead = to;
         } else if (to == rows) {
@@ -244,6 +248,7 @@ bool share_gaps(Prepared& c, const AttnGaps& gaps, int n_gaps, int64_t rows, int
         }
     }
     if ((static_cast<int64_t>(c.sh.lead) + c.sh.trail) * heads > kItemFill * c.sh.items) return none();
+    if (unused * all_heads > kItemFill * 2 * sms) return none();
     return true;
 }
 
@@ -292,7 +297,7 @@ lora_status attn_fwd(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V,
     const int split = workspace_bytes >= kStatusBytes + kSplitBytes ? split_keys(c, sms, &most, &split_tiles) : 0;
     if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? q_items(q, c.sh, most) : attn_query_tiles(q, c.sh); })))
         return st;
-    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, [](const AttnSeq& q) { return q.q0; },
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, a.q_heads, sms, [](const AttnSeq& q) { return q.q0; },
                     [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, mat(O, a.o), AttnMat{}, a.q_heads, a.head_dim, lse, s))) return st;
     }
@@ -366,7 +371,7 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     p.dV = mv;
     p.ctl = DevCtl{static_cast<int*>(workspace), wait_limit_ns()};
     if ((st = number_items(c, [&](const AttnSeq& q) { return tiles_of(q.ql, tokens); }))) return st;
-    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, [](const AttnSeq& q) { return q.q0; },
+    if (!share_gaps(c, c.q_gaps, c.nq_gaps, a.q_rows, tokens, c.sh.hp, a.q_heads, sms, [](const AttnSeq& q) { return q.q0; },
                     [](const AttnSeq& q) { return q.ql; })) {
         if ((st = fill(c.q_gaps, c.nq_gaps, p.dQ, AttnMat{}, a.q_heads, a.head_dim, nullptr, s))) return st;
     }
@@ -385,7 +390,7 @@ lora_status attn_bwd(const lora_bf16* dO, const lora_bf16* Q, const lora_bf16* K
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes + delta_bytes(a.q_rows, a.q_heads));
     if ((st = number_items(c, [&](const AttnSeq& q) { return q.split ? kv_items(q, c.sh, p.most) : key_tiles(q); })))
         return st;
-    if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, kAttnTile, 1, [](const AttnSeq& q) { return q.k0; },
+    if (!share_gaps(c, c.k_gaps, c.nk_gaps, a.k_rows, kAttnTile, 1, a.kv_heads, sms, [](const AttnSeq& q) { return q.k0; },
                     [](const AttnSeq& q) { return q.kl; })) {
         if ((st = fill(c.k_gaps, c.nk_gaps, mk, mv, a.kv_heads, a.head_dim, nullptr, s))) return st;
     }
