@@ -501,7 +501,8 @@ loss_long_rows_kernel(const __grid_constant__ P p, int32_t cluster, int32_t slic
                           reinterpret_cast<const uint8_t*>(rv.z + a * Vec<T>::n - rv.skew) + o, min(bytes - o, 8192u), &full[s]);
             ++n;
         }
-        if (!ok && lane == 0)
+        // every copy lands before the CTA exits, also when the warps that wait for it gave up
+        if (lane == 0)
             for (int i = max(0, n - slices); i < n; ++i) mbar_wait_drain(&full[i % slices], (i / slices) & 1, p.ctl.wait_ns);
     } else if (warp == kWarps + 1) {
         int n = 0;
@@ -640,6 +641,7 @@ loss_long_rows_kernel(const __grid_constant__ P p, int32_t cluster, int32_t slic
         }
     }
     __syncwarp();
+    if (*w.abort) __nanosleep(20000);   // messages that no peer waits for any more land, too
     cluster_sync();   // no CTA leaves while a peer may still write to it
     // the cluster that finishes last (a ticket in the workspace, which it takes back to zero) adds the rows' losses, or forms
     // the pairs'
