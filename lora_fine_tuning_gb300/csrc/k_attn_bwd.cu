@@ -7,11 +7,18 @@
 // query tiles of all heads of its group.  Each gradient element is summed by one CTA in a fixed order, in TMEM in fp32:
 // the results are the same from call to call, and no partial sum goes through memory.  The price is that S and dP are
 // formed twice (seven products instead of five).  dS and, for dV, P are rounded to bf16, the tensor cores' operand type;
-// dS comes from P and dP in fp32.
+// dS comes from P and dP in fp32.  P is formed with the approximate exponential (2^-22).
 //
-// Bound by the tensor cores on long sequences: four of 4096 tokens, 64/8 heads of 128, take 1095 to 1130 us for dQ (three
-// products, 880 us at the cuBLAS rate; a turn of 128 keys takes 1645 cycles, its products 1536) and 1274 to 1310 us for
-// dK and dV (four products, 1173 us).  On short ones by the start of a CTA, whose first tiles of 32 KB arrive together.
+// delta: the dQ pass starts from the O that it is given, in bf16.  Where P gathers on few keys, dP - delta cancels, and this
+// rounding of O grows: 0.006 of dQ and of dK (2-norm) for scores with a standard deviation of 12, where dS in bf16 alone gives
+// 0.0024.  But P sums to 1 over a row, so the row's sum of P (dP - delta), in fp32 before any rounding, is what delta lacks.
+// The dQ pass adds it up and hands the whole delta to the dK and dV pass: dK is off by 0.0024, at 3% of the dQ pass's time.
+// dQ itself keeps the first delta: its correction, the missing part times P K, would take a fourth product, and TMEM has no
+// room for its sums.
+//
+// Bound by the tensor cores on long sequences: four of 4096 tokens, 64/8 heads of 128, take 1140 us for dQ (three
+// products, 880 us at the cuBLAS rate) and 1270 to 1310 us for dK and dV (four products, 1173 us).  On short ones by the start
+// of a CTA, whose first tiles of 32 KB arrive together.
 #include "attn.cuh"
 #include "kernels.h"
 
@@ -85,6 +92,16 @@ __device__ __forceinline__ void store_scores(uint32_t taddr, const uint32_t (&x)
             o[e] = pack_bf16x2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
         tmem_st16(taddr + c * 16, o);
     }
+}
+
+// Adds a row's 64 gradients of scores, in fp32 before their rounding.
+__device__ __forceinline__ void add_row(F2 (&sum)[2], const uint32_t (&x)[2][32]) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) sum[e & 1] = add2(sum[e & 1], pair(x, e));
+}
+__device__ __forceinline__ float total(const F2 (&sum)[2]) {
+    const float2 q = parts(add2(sum[0], sum[1]));
+    return q.x + q.y;
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -328,7 +345,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
         const float lse2 = row_ok && limit >= 0 ? p.lse[at] * kLog2e : 0.f;
         bool ok = true;
         const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2);
-        F2 delta2 = f2(0.f, 0.f);
+        F2 delta2 = f2(0.f, 0.f), rest[2] = {delta2, delta2};
         for (int j = 0; j < n; ++j) {
             const uint32_t ts = t_s + (j & 1) * 128 + lanes + g * 64;
             ok = mbar_wait(&s_full[j & 1], (j >> 1) & 1, w, 9);
@@ -361,7 +378,6 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
                 score_sync<256>();
                 if (!ok) break;
                 const float delta = sDelta[r];
-                if (row_ok && g == 0) p.delta[at] = delta;   // for the next pass
                 delta2 = f2(-delta, -delta);
             }
             ok = mbar_wait(dp_full, j & 1, w, 10);
@@ -377,11 +393,19 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(ds_full);
+            add_row(rest, x);
         }
         if (ok && n > 0) {
             ok = mbar_wait(dq_full, 0, w, 11);
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
+        }
+        if (n > 0) {
+            // delta for the next pass (every thread has read its own: all arrived for the last product); all score warps
+            // come here, also after a wait that ran out
+            if (g == 1) sDelta[r] = total(rest);
+            score_sync<256>();
+            if (row_ok && g == 0) p.delta[at] = total(rest) + sDelta[r] - parts(delta2).x;
         }
         if (ok) {
             // group g features [64 g, 64 g + 64), through Q's shared memory: all products are done
@@ -405,7 +429,7 @@ attn_dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ 
 
 // The same pass with key tiles of 64, four score warps and half the shared memory and TMEM: two CTAs an SM, one of which
 // works while the other starts (its first tiles take 5000 cycles) or ends.  A product of 64 columns with both operands
-// in shared memory costs 3/4 of one of 128, so long ranges are slower.  us for 8192 tokens with 32/8 heads of 128 in
+// in shared memory costs 3/4 of one of 128, so long ranges are slower.  us (before the sums for delta, 1% here) for 8192 tokens with 32/8 heads of 128 in
 // samples of 77, 128, 256, 450, 1024, 2048, 4096 tokens: 86, 78, 83, 100, 135, 204, 343 against 119, 100, 100, 115, 136,
 // 186, 276 with tiles of 128; 32 heads of 64 the same way (58 against 83 at 128, 256 against 233 at 4096).
 constexpr int kShortKeys = 64;
@@ -666,8 +690,8 @@ attn_dq_short_kernel(const __grid_constant__ AttnBwdParams p, const __grid_const
             }
             score_sync<128>();
             delta = sDelta[r];
-            if (row_ok) p.delta[at] = delta;         // for the next pass
         }
+        F2 rest[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         const F2 sl2 = f2(sl, sl), lse22 = f2(-lse2, -lse2), delta2 = f2(-delta, -delta);
         for (int j = 0; ok && j < n; ++j) {
             const uint32_t ts = tmem + (j & 1) * 64 + lanes, tdp = tmem + ((j + 1) & 1) * 64 + lanes;
@@ -694,7 +718,9 @@ attn_dq_short_kernel(const __grid_constant__ AttnBwdParams p, const __grid_const
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(ds_full);
+            add_row(rest, x);
         }
+        if (row_ok && n > 0) p.delta[at] = delta + total(rest);   // for the next pass
         if (ok && n > 0) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(dq_full, 0, w, 11));
             tc_fence_after();
