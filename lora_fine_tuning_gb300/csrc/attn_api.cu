@@ -160,7 +160,7 @@ int split_keys(Prepared& c, int sms, int32_t* most, int* tiles) {
         const int t = attn_query_tiles(*q, c.sh);
         if (t == 0 || key_tiles(*q) < (t == 1 ? *most + 1 : 4 * static_cast<int64_t>(*most))) continue;
         const int64_t n = static_cast<int64_t>(t) * attn_pieces(*q, *most);
-        if ((slots + n) * c.sh.packs > kAttnMaxSlots) break;
+        if ((slots + n) * c.sh.packs > kAttnMaxSlots) continue;
         q->split = static_cast<int32_t>(slots + 1);
         slots += n;
         *tiles += t;
@@ -193,7 +193,7 @@ int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
     for (AttnSeq* q = c.order.s; q != end; ++q) {
         if (attn_turns(*q, c.sh, 0) * 2 <= *most * 3) continue;
         const int64_t n = kv_items(*q, c.sh, *most);
-        if ((slots + n) * c.sh.hkv > kMaxKvSlots || *tiles + key_tiles(*q) > 65535) break;
+        if ((slots + n) * c.sh.hkv > kMaxKvSlots || *tiles + key_tiles(*q) > 65535) continue;
         q->split = static_cast<int32_t>(slots + 1);
         slots += n;
         *tiles += key_tiles(*q);

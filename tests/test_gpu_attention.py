@@ -472,3 +472,15 @@ def test_dk_where_probability_gathers(rows, hq, hkv, d, spread):
     ref = reference(Q, K, V, seqs, d ** -0.5, dO)
     assert off(dK, ref[3]) <= 2.8e-3 and off(dV, ref[4]) <= 2.8e-3
     assert off(dQ, ref[2]) <= 1e-2
+
+
+def test_a_sequence_that_does_not_fit_the_slots():
+    """Few queries over many keys on one key head need more slots than there are: that sequence stays whole, the next ones are
+    split all the same."""
+    seqs = [(0, 890, 0, 14344), (890, 1169, 14344, 1169), (2059, 981, 15513, 981)]
+    Q, K, V, dO = inputs(3040, 16494, 10, 1, 64, seed=890)
+    native.timing_begin()
+    got = run(Q, K, V, dO, seqs, None)
+    torch.cuda.synchronize()
+    assert native.timing_end()["attn_join"][1] >= 1
+    check(Q, K, V, seqs, 0.125, dO, got)
