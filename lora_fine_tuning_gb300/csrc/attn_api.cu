@@ -142,6 +142,7 @@ int q_items(const AttnSeq& q, const AttnShape& sh, int most) {
 // the others: an item then has at most two thirds of what an SM gets of the call's work, but no fewer than four key tiles.
 // Sequences of one query tile are split from there on, longer ones, which a few long tiles do not hold up as much, from
 // four times that.  They come first in the table, as the join wants them.  Returns how many they are, and their query tiles.
+// (The slots hold them all on 152 SMs; one that did not fit would stay whole.)
 // 24 continuations of 1 to 22 tokens over up to 12000 keys, 32/8 heads of 128: 63 us with the join; pieces of all or half
 // an SM's share 71 and 77, none 121.  One token over 4096 keys: 12 us, with at least eight tiles a piece 14.  A prompt of
 // 8192 tokens with one head of 128: 25 us and 10 for the join, whole 82; with 8/1 heads, 4096 tokens (1.7 times): 45 and 10,
@@ -178,7 +179,9 @@ int kv_items(const AttnSeq& q, const AttnShape& sh, int most) {
 // work (few key/value heads, shared by many query heads): an item then has that share at most, but no fewer than four
 // query tiles.  These sequences come first in the table.  Returns how many they are, and their key tiles.  One sequence of
 // 2048 tokens with 8/1 heads of 128: 25 us and 8 for the join, pieces of half that length 33 and 15, none 177; of 4096
-// tokens 82 and 6, 74 and 10, 342.
+// tokens 82 and 6, 74 and 10, 342.  One that does not fit the slots (few queries over many keys: one batch in a thousand of those
+// that are split) stays whole, and the others are still looked at: 890 queries over 14344 keys before samples of 1169 and
+// 981 with 10/1 heads 117 us and 6, 155 without; where the whole one takes longest all the same, the join's 6 us more.
 int split_queries(Prepared& c, int sms, int32_t* most, int* tiles) {
     AttnSeq* const end = c.order.s + c.n;
     int64_t work = 0;

@@ -479,8 +479,9 @@ def test_a_sequence_that_does_not_fit_the_slots():
     split all the same."""
     seqs = [(0, 890, 0, 14344), (890, 1169, 14344, 1169), (2059, 981, 15513, 981)]
     Q, K, V, dO = inputs(3040, 16494, 10, 1, 64, seed=890)
+    O, lse = api.attn_fwd(Q, K, V, seqs)
     native.timing_begin()
-    got = run(Q, K, V, dO, seqs, None)
+    grads = api.attn_bwd(dO, Q, K, V, O, lse, seqs)
     torch.cuda.synchronize()
-    assert native.timing_end()["attn_join"][1] >= 1
-    check(Q, K, V, seqs, 0.125, dO, got)
+    assert native.timing_end()["attn_join"][1] == 1
+    check(Q, K, V, seqs, 0.125, dO, (O, lse, *grads))
