@@ -386,7 +386,8 @@ lora_status policy_loss(const lora_logits* logits, const float* old_logp, const 
 /* One AdamW step over many tensors (adapters, magnitudes, biases) in as few launches as the table allows:
  *   g = grad * (*grad_scale),  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
- * in fp32, with the states and the parameter written back in place.
+ * in fp32, with the states and the parameter written back in place.  lr, beta1, beta2, eps, weight_decay and step are values of
+ * the launch: a captured call is right for that step alone.
  *  - param and grad are bf16 or fp32 each; master (optional, bf16 parameters only) is an fp32 copy that holds the
  *    parameter: it is updated and param is its rounding.  Without it a bf16 param is read, updated and rounded.
  *  - state_bits 32: m and v are fp32.  state_bits 8: m and sqrt(v) are e4m3 codes, one byte each, with an fp32 scale for

@@ -362,8 +362,8 @@ _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda
 
 
 class AttnSeqs:
-    """The sequences of a packed batch: (q_start, q_rows, k_start, k_rows) each, in row order.  Made once and used by
-    every layer's attention."""
+    """The sequences of a packed batch: (q_start, q_rows, k_start, k_rows) each, in row order.  Made once (1 us a sequence) and
+    used by every layer's attention; a decoder whose keys grow makes one a token."""
 
     def __init__(self, seqs):
         self.seqs = [tuple(int(x) for x in s) for s in seqs]
@@ -641,7 +641,8 @@ def adamw_tensor(param, grad, *, bits: int = 32, master: bool = False) -> AdamWT
 
 
 class AdamWTensors:
-    """The optimiser's list of tensors, checked and laid out once for every step."""
+    """The optimiser's list of tensors, checked and laid out once for every step.  It holds their addresses: a program whose
+    gradients are new tensors in each step makes the list anew (4 us a tensor), or copies them into the old ones."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
