@@ -287,7 +287,7 @@ lora_status lora_fwd_static_scratch(const lora_bf16* X, const lora_bf16* W, cons
  *    rows that do not see it.
  *  - P and dS are rounded to bf16 for their products with V, K, Q and dO; everything else is fp32 until the outputs.
  *    dQ's sum of dO O is formed from the O given, in bf16 (dK's has what that rounding lacks): dQ is off by 0.0025 (2-norm) for
- *    scores with a standard deviation of 1, by 0.006 for 12.
+ *    scores with a standard deviation of 1, by 0.006 for 12, a single row by up to 0.01.
  *    Every sum has a fixed order: results are bit-identical from call to call in both reduction modes.
  *  - workspace: attn_workspace_size() bytes, 256-byte aligned, not shared by calls that may overlap.  Its first 256
  *    bytes (the device status word) are zero before the first use and stay so; the rest is scratch whose contents do
