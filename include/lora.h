@@ -415,6 +415,140 @@ typedef struct {
 lora_status adamw_step(const lora_adamw_tensor* tensors, int32_t n_tensors, double lr, double beta1, double beta2,
                        double eps, double weight_decay, int64_t step, const float* grad_scale, void* stream);
 
+/* Activations in 8 bits: what a backward pass needs of a layer's input, in 1.03 bytes a value instead of two.
+ *
+ * 32 consecutive values of a row share a power of two: with E = floor(log2 of the largest finite |x| of the block),
+ *   scale = 2^(E - 6) (at least 2^-126),  code = x / scale rounded to the nearest whole number (even on ties), at most 127
+ * so a value is off by half a scale at most (2^-7 of its block's largest), and code * scale is a bf16 value.  A value that
+ * is infinite or NaN has code -128 and is held as NaN; its block's scale is that of the finite values.
+ *  - codes: rows x (width rounded up to 32), contiguous, 16-byte aligned; scales: rows x 4 ceil(width / 128), contiguous,
+ *    4-byte aligned, the exponent of each block's scale plus 127.  Codes past the width are 0, scales past the last block 127.
+ *  - X has row stride ld >= width and its element's alignment; width up to LORA_MAX_ACT8_WIDTH, rows times the codes of
+ *    a row below 2^34.
+ * act8_load writes the values that codes and scales stand for, exactly.  norm_fwd writes the same codes on the way, norm_bwd,
+ * lora_bwd_act8 and multi_lora_bwd_act8 read them. */
+enum { LORA_MAX_ACT8_WIDTH = 1 << 22 };
+
+typedef struct {
+    int8_t* codes;
+    uint8_t* scales;
+} lora_act8;
+
+lora_status act8_store(const lora_bf16* X, int64_t rows, int64_t width, int64_t ld, const lora_act8* out, void* stream);
+lora_status act8_load(const lora_act8* in, int64_t rows, int64_t width, lora_bf16* X, int64_t ld, void* stream);
+
+/* The layer's backward from an input in 8 bits: multi_lora_bwd and lora_bwd with X8 (m x k) in the place of X.  Of X the backward
+ * needs dA = (X .* D)^T dS only, and code * scale is a bf16 value: the results are those of the bf16 call on
+ * what act8_load gives. */
+lora_status multi_lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_bf16* W,
+                                const lora_adapter* adapters, int32_t n_adapters, const lora_segment* segments,
+                                int32_t n_segments, uint64_t seed, int64_t m, int64_t k, int64_t n,
+                                const lora_bf16* S_saved, const uint8_t* mask_bits, lora_bf16* dX, void* workspace,
+                                size_t workspace_bytes, void* stream);
+lora_status lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_bf16* W, const lora_bf16* A,
+                          const lora_bf16* B, const lora_bf16* S_saved, const uint8_t* mask_bits, float alpha, float p,
+                          uint64_t seed, int64_t m, int64_t k, int64_t n, int32_t r, lora_bf16* dX, lora_bf16* dA,
+                          lora_bf16* dB, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norms around a block: the block's output y joins the stream h, normed, gated and scaled, and the stream is normed for the
+ * next block, in one pass:
+ *   rms(v) = sqrt(mean_j v_j^2 + eps)
+ *   u = y / rms(y) (w_offset + post_w)   (without post_w: u = y)
+ *   h' = h + res_scale gate_j row_gate_t u,   x = h' / rms(h') (w_offset + w)
+ * Every vector but w is optional (data NULL): post_w, w and gate have `width` values, row_gate `rows`.  y NULL: x only, from
+ * h as it is (h_out NULL, too).  w NULL: h' only (x NULL).
+ *  - h, h_out, dh, dh_out are the stream, bf16 or fp32 (stream_dtype); y, x, dx, dy are bf16.  Each has a row stride (in
+ *    elements, >= width) and its element's alignment; rows that start on 16-byte boundaries and whole eights of values are
+ *    read 16 bytes at a time.
+ *  - Everything is fp32 until the outputs, x is formed from h' before its rounding.  A row's results depend on that row only.
+ *    Rows of zeros give zeros.
+ *  - h_out may be h, dh_out may be dh (same strides); nothing else overlaps.
+ *  - x8, h8, y8 (optional) receive x, h' and y (each rounded to bf16) in 8 bits; with x8 x may be NULL.
+ * Backward, from dx and dh (the gradients of x and h'; dh NULL: zero): dh_out (of h), dy (optional), and where not NULL
+ * the sums over rows dw, dpost_w, dgate (width, fp32) and drow_gate (rows, fp32).  h is the forward's h' (bf16 or fp32 or, as h8,
+ * in 8 bits), y its y (or y8); rms is taken of these.  Sums have a fixed order: results are bit-identical from call to call.
+ * Without w: dx, h and h8 are NULL.
+ *  - workspace: norm_workspace_size() bytes, 256-byte aligned, for calls with dw, dpost_w or dgate; scratch whose contents do
+ *    not matter, not shared by calls that may overlap. */
+enum { LORA_MAX_NORM_WIDTH = 16384 };
+
+typedef struct {
+    const void* data;
+    int32_t dtype; /* LORA_BF16 or LORA_F32 */
+    int32_t reserved;
+} lora_vector;
+
+typedef struct {
+    int64_t rows, width;
+    int64_t h, y, h_out, x;       /* row strides of norm_fwd's matrices; norm_bwd has those of h and y, too */
+    int64_t dx, dh, dh_out, dy;   /* norm_bwd */
+    lora_vector w, post_w, gate, row_gate;
+    float eps;                    /* at least 1e-30 */
+    float w_offset, res_scale;
+    int32_t stream_dtype;
+} lora_norm;
+
+size_t norm_workspace_size(int64_t rows, int64_t width);
+
+lora_status norm_fwd(const lora_norm* norm, const void* h, const lora_bf16* y, void* h_out, lora_bf16* x,
+                     const lora_act8* x8, const lora_act8* h8, const lora_act8* y8, void* stream);
+
+lora_status norm_bwd(const lora_norm* norm, const lora_bf16* dx, const void* dh, const void* h, const lora_act8* h8,
+                     const lora_bf16* y, const lora_act8* y8, void* dh_out, lora_bf16* dy, float* dw, float* dpost_w,
+                     float* dgate, float* drow_gate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions: pairs of a head's first rot_dim features turned by the angle of their row's position.
+ *   pair i: (x_i, x_{i + rot_dim/2}), or interleaved (x_{2i}, x_{2i+1});  f_i = base^(-2 i / rot_dim), changed by the scaling
+ *   (a, b) -> magnitude (a cos(t f_i) - b sin(t f_i), b cos(t f_i) + a sin(t f_i));  other features stay
+ * rope_table (host only) fills a lora_rope: turn[i] is f_i / 2 pi modulo one in units of 2^-64, so the angle of position t is
+ * right to |t| 2^-65 of a turn, far positions included.  Scalings: LINEAR: f / factor; BASE: base factor^(rot / (rot - 2));
+ * PARTS: f keep + f / factor (1 - keep), keep rising from 0 to 1 while the turns over the original length, original f / 2 pi,
+ * go from low to high. */
+enum { LORA_ROPE_MAX_HEAD_DIM = 256 };
+enum { LORA_ROPE_NONE = 0, LORA_ROPE_LINEAR = 1, LORA_ROPE_BASE = 2, LORA_ROPE_PARTS = 3 };
+
+typedef struct {
+    int32_t kind;
+    float magnitude;
+    double factor, original, low, high;
+} lora_rope_scaling;
+
+typedef struct {
+    int32_t rot_dim, interleaved;
+    float magnitude;
+    int32_t reserved;
+    uint64_t turn[LORA_ROPE_MAX_HEAD_DIM / 2];
+} lora_rope;
+
+/* scaling NULL: none, magnitude 1. */
+lora_status rope_table(int32_t rot_dim, double base, int32_t interleaved, const lora_rope_scaling* scaling, lora_rope* out);
+
+/* Q is rows x q_heads x head_dim, K (and V) rows x kv_heads x head_dim, bf16, in the layouts of attn_fwd but with any strides
+ * and alignment (vectors of up to 16 bytes are used where everything allows them); either count of heads may be 0 in
+ * rope_fwd and rope_bwd. */
+typedef struct {
+    int64_t rows, cache_rows;
+    int32_t q_heads, kv_heads, head_dim;
+    int32_t positions_bits; /* positions are int64 (64) or int32 (32) */
+    lora_attn_strides q, k, v, q_out, k_out, v_out;
+} lora_rope_shape;
+
+/* Q_out and K_out receive Q and K turned by positions[row] (device, any values); they may be Q and K (same strides).
+ * rope_bwd turns gradients by the transposed rotation, the magnitude with it: the gradients of rope_fwd. */
+lora_status rope_fwd(const lora_bf16* Q, const lora_bf16* K, const void* positions, const lora_rope_shape* shape,
+                     const lora_rope* rope, lora_bf16* Q_out, lora_bf16* K_out, void* stream);
+lora_status rope_bwd(const lora_bf16* dQ, const lora_bf16* dK, const void* positions, const lora_rope_shape* shape,
+                     const lora_rope* rope, lora_bf16* dQ_out, lora_bf16* dK_out, void* stream);
+
+/* rope_fwd on the way into a cache: the row's turned K and its V go to row slots[row] (device, int64) of K_cache and V_cache
+ * (cache_rows x kv_heads x head_dim, strides k_out and v_out), the rows that attn_fwd reads.  A cache of pages is such
+ * a matrix, with slot = page * page rows + row of the page.  A row whose slot is outside [0, cache_rows) is not stored (its Q_out
+ * is written).  Slots inside it must differ from each other: of two rows with one slot, either may be left there, or parts
+ * of both. */
+lora_status rope_append(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const void* positions,
+                        const int64_t* slots, const lora_rope_shape* shape, const lora_rope* rope, lora_bf16* Q_out,
+                        lora_bf16* K_cache, lora_bf16* V_cache, void* stream);
+
 /* Host only, no GPU needed: the routing table.  tile_adapter[i] (i < ceil(m/128))
  * receives the adapter of tile i, -1 where no segment covers it. */
 lora_status lora_tile_table(const lora_segment* segments, int32_t n_segments, int32_t n_adapters, int64_t m,
@@ -484,11 +618,12 @@ const char* lora_status_string(lora_status s);
  * 6 dA, 7 finalize dA, 8 memset (gradients of adapters that own no rows),
  * 9-12 DoRA (U, norm, dZ, dmag), 13-17 attention
  * (forward, joining of what was split over SMs, dQ, dK and dV, unused rows),
- * 18-21 losses (rows, pairs, gradient, sum), 22 AdamW.  When kind 6 runs on the library's side
+ * 18-21 losses (rows, pairs, gradient, sum), 22 AdamW, 23-24 activations in 8 bits (store, load), 25-27 norms (forward,
+ * backward, the weights' sums), 28-29 rotary positions (alone, into a cache).  When kind 6 runs on the library's side
  * stream beside the backward GEMM, its event pair spans from the fork to its
  * end.
  * Host-side cost: two event records per launch. */
-enum { LORA_KERNEL_KINDS = 23 };
+enum { LORA_KERNEL_KINDS = 30 };
 lora_status lora_timing_begin(void);
 lora_status lora_timing_end(float* total_ms, int32_t* launches, int32_t n_kinds);
 const char* lora_kernel_name(int32_t kind);

@@ -9,7 +9,7 @@ import ctypes
 import struct
 import threading
 from dataclasses import dataclass
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -85,25 +85,34 @@ def lora_fwd(X, W, A, B, alpha: float, p: float, seed: int, *, Y=None, S_saved=N
 
 def lora_bwd(dY, X, W, A, B, S_saved, alpha: float, p: float, seed: int, *, dX=None, dA=None, dB=None, ws=None,
              stream=None, mask_bits=None):
-    """Gradients of lora_fwd with W frozen.  Returns (dX, dA, dB).  mask_bits: optional, the keep bits
-    lora_fwd wrote for the same inputs (read instead of regenerating the mask)."""
+    """Gradients of lora_fwd with W frozen.  Returns (dX, dA, dB).  X: the forward's, or what act8_store or norm_fwd kept of it
+    in 8 bits (Act8).  mask_bits: optional, the keep bits lora_fwd wrote for the same inputs (read instead of regenerating the mask)."""
     m, k = X.shape
     n = W.shape[1]
     r = A.shape[1]
-    for name, t, shp in (("dY", dY, (m, n)), ("X", X, (m, k)), ("W", W, (k, n)), ("A", A, (k, r)),
-                         ("B", B, (r, n)), ("S_saved", S_saved, (m, r))):
+    for name, t, shp in (("dY", dY, (m, n)), ("W", W, (k, n)), ("A", A, (k, r)), ("B", B, (r, n)), ("S_saved", S_saved, (m, r))):
         _check_bf16(name, t, shp)
+    X_arg, act8_form = _layer_input(X, m, k)
     dX = dX if dX is not None else torch.empty((m, k), dtype=torch.bfloat16, device=X.device)
     dA = dA if dA is not None else torch.empty((k, r), dtype=torch.bfloat16, device=X.device)
     dB = dB if dB is not None else torch.empty((r, n), dtype=torch.bfloat16, device=X.device)
     _check_bits(mask_bits, m, k)
     ws = ws if ws is not None else workspace(m, k, n, r)
-    st = native.lib().lora_bwd(_ptr(dY), _ptr(X), _ptr(W), _ptr(A), _ptr(B), _ptr(S_saved), _ptr(mask_bits),
-                               float(alpha), float(p),
-                               int(seed) & (2**64 - 1), m, k, n, r, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
-                               ws.numel(), _stream(stream))
-    native.check("lora_bwd", st)
+    name = "lora_bwd" + act8_form
+    st = getattr(native.lib(), name)(_ptr(dY), X_arg, _ptr(W), _ptr(A), _ptr(B), _ptr(S_saved), _ptr(mask_bits),
+                                     float(alpha), float(p),
+                                     int(seed) & (2**64 - 1), m, k, n, r, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws),
+                                     ws.numel(), _stream(stream))
+    native.check(name, st)
     return dX, dA, dB
+
+
+def _layer_input(X, m: int, k: int):
+    """The input of a layer's backward, bf16 or in 8 bits.  Returns what the library takes and how that form's calls end."""
+    if isinstance(X, Act8):
+        return _act8_arg(_On(X.codes, None), "X", X, m, k), "_act8"
+    _check_bf16("X", X, (m, k))
+    return _ptr(X), ""
 
 
 @dataclass
@@ -164,11 +173,11 @@ def multi_lora_fwd(X, W, adapters: Sequence[Adapter], segments, seed: int, *, Y=
 def multi_lora_bwd(dY, X, W, adapters: Sequence[Adapter], segments, seed: int, S_saved, *, dX=None, ws=None,
                    stream=None, mask_bits=None):
     """Packed multi-adapter backward.  Fills each adapter's dA / dB (allocated if missing); returns dX.
-    mask_bits: optional, the keep bits multi_lora_fwd wrote for the same batch."""
+    X: the forward's, or what act8_store or norm_fwd kept of it in 8 bits (Act8).  mask_bits: optional, the keep bits multi_lora_fwd wrote for the same batch."""
     m, k = X.shape
     n = W.shape[1]
     _check_bf16("dY", dY, (m, n))
-    _check_bf16("X", X, (m, k))
+    X_arg, act8_form = _layer_input(X, m, k)
     _check_bf16("W", W, (k, n))
     for a in adapters:
         if a.dA is None:
@@ -181,10 +190,11 @@ def multi_lora_bwd(dY, X, W, adapters: Sequence[Adapter], segments, seed: int, S
     seg = native.segments_array(segments)
     ad = _adapter_array(adapters, True)
     _check_bits(mask_bits, m, k)
-    st = native.lib().multi_lora_bwd(_ptr(dY), _ptr(X), _ptr(W), ad, len(adapters), seg, len(segments),
+    name = "multi_lora_bwd" + act8_form
+    st = getattr(native.lib(), name)(_ptr(dY), X_arg, _ptr(W), ad, len(adapters), seg, len(segments),
                                      int(seed) & (2**64 - 1), m, k, n, _ptr(S_saved), _ptr(mask_bits), _ptr(dX),
                                      _ptr(ws), ws.numel(), _stream(stream))
-    native.check("multi_lora_bwd", st)
+    native.check(name, st)
     return dX
 
 
@@ -698,6 +708,329 @@ def adamw_step(tensors, *, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
                                  float(weight_decay), int(step), _ptr(grad_scale),
                                  _current_stream(index) if stream is None else stream.cuda_stream)
     native.check("adamw_step", st)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# activations in 8 bits
+# ---------------------------------------------------------------------------------------------------------------
+
+@dataclass
+class Act8:
+    """A rows x width matrix in 8 bits (include/lora.h): int8 codes, rows of the width rounded up to 32, and uint8 scales, four
+    for each 128 values of a row.  Slices of whole rows of both are such a matrix, too."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    width: int
+
+    @property
+    def shape(self):
+        return torch.Size((self.codes.shape[0], self.width))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def get_device(self) -> int:
+        return self.codes.get_device()
+
+
+def act8(rows: int, width: int, *, stream=None) -> Act8:
+    """Room for a rows x width matrix in 8 bits, on the current device."""
+    on = _On(None, stream)
+    return Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
+
+
+def _act8_arg(on: _On, name: str, a: Optional[Act8], rows: int, width: int):
+    """Checks one matrix in 8 bits.  Returns what the library takes for it."""
+    if a is None:
+        return None
+    if a.width != width or a.codes.dtype is not torch.int8 or not a.codes.is_cuda or not a.codes.is_contiguous() or \
+            a.codes.shape != (rows, -(-width // 32) * 32):
+        raise ValueError(f"{name}.codes must be a contiguous CUDA int8 tensor of shape {(rows, -(-width // 32) * 32)}, its width {width}")
+    if a.scales.dtype is not torch.uint8 or not a.scales.is_cuda or not a.scales.is_contiguous() or \
+            a.scales.shape != (rows, -(-width // 128) * 4):
+        raise ValueError(f"{name}.scales must be a contiguous CUDA uint8 tensor of shape {(rows, -(-width // 128) * 4)}")
+    on.check(name, a.codes)
+    on.check(name, a.scales)
+    return native.Act8(a.codes.data_ptr(), a.scales.data_ptr())
+
+
+def _matrix(on: _On, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> int:
+    """Checks one rows x width operand whose rows may lie apart.  Returns its row stride."""
+    if t.dtype is not dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    on.check(name, t)
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
+    row, inner = t.stride()
+    if inner != 1 and width != 1:
+        raise ValueError(f"the values of a row of {name} must be contiguous")
+    return row if rows > 1 else width
+
+
+def act8_store(X, out: Optional[Act8] = None, *, stream=None) -> Act8:
+    """X (rows x width, bf16, rows may lie apart) in 8 bits: 32 values of a row share a power of two, codes are whole numbers up
+    to 127 (include/lora.h).  Kept for a backward pass in the place of X: lora_bwd, multi_lora_bwd and norm_bwd take it."""
+    on = _On(X, stream)
+    if X.dim() != 2:
+        raise ValueError("X is rows x width")
+    rows, width = X.shape
+    ld = _matrix(on, "X", X, rows, width, torch.bfloat16)
+    if out is None:
+        out = Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
+    st = native.lib().act8_store(X.data_ptr(), rows, width, ld, _act8_arg(on, "out", out, rows, width), on.handle)
+    if st:
+        native.check("act8_store", st)
+    return out
+
+
+def act8_load(a: Act8, out=None, *, stream=None):
+    """The bf16 values that a matrix in 8 bits stands for, exactly."""
+    on = _On(a.codes, stream)
+    rows, width = a.shape
+    if out is None:
+        out = on.empty((rows, width), torch.bfloat16)
+    ld = _matrix(on, "out", out, rows, width, torch.bfloat16)
+    st = native.lib().act8_load(_act8_arg(on, "a", a, rows, width), rows, width, out.data_ptr(), ld, on.handle)
+    if st:
+        native.check("act8_load", st)
+    return out
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# norms around a block
+# ---------------------------------------------------------------------------------------------------------------
+
+# lora_norm in one go
+_NORM = struct.Struct("10qqiiqiiqiiqiifffi")
+
+
+def _vector(on: _On, name: str, t, n: int):
+    """Checks one optional vector of weights.  Returns (address, type, 0)."""
+    if t is None:
+        return 0, 0, 0
+    if t.dtype not in _DTYPES or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
+        raise ValueError(f"{name} must be a contiguous CUDA bfloat16 or float32 vector of {n}")
+    on.check(name, t)
+    return t.data_ptr(), _DTYPES[t.dtype], 0
+
+
+def _norm(on, rows, width, strides, w, post_w, gate, row_gate, eps, w_offset, res_scale, stream_dtype):
+    packed = _NORM.pack(rows, width, *strides, *_vector(on, "w", w, width), *_vector(on, "post_w", post_w, width),
+                        *_vector(on, "gate", gate, width), *_vector(on, "row_gate", row_gate, rows), eps, w_offset, res_scale,
+                        _DTYPES[stream_dtype])
+    return native.Norm.from_buffer_copy(packed)
+
+
+def norm_fwd(h, w=None, *, y=None, post_w=None, gate=None, row_gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+             w_offset: float = 0.0, h_out=None, x=None, x8: Optional[Act8] = None, h8: Optional[Act8] = None,
+             y8: Optional[Act8] = None, stream=None):
+    """A block's output joins the stream, and the stream is normed for the next block (include/lora.h):
+    u = y / rms(y) (w_offset + post_w) (y itself without post_w), h' = h + res_scale gate row_gate u,
+    x = h' / rms(h') (w_offset + w).  h: rows x width, bf16 or fp32; y: bf16, without it x is h's norm; w, post_w, gate: width,
+    row_gate: rows, each bf16 or fp32.  x8, h8, y8 (act8(rows, width)) also receive x, h' and y in 8 bits, for the backward.
+    Returns (x, h'): x None without w, h' h itself without y.  h_out=h adds in place."""
+    on = _On(h, stream)
+    if h.dim() != 2 or h.dtype not in _DTYPES:
+        raise TypeError("h must be a CUDA bfloat16 or float32 matrix")
+    rows, width = h.shape
+    h_ld = _matrix(on, "h", h, rows, width, h.dtype)
+    y_ld = h_out_ld = x_ld = 0
+    if y is not None:
+        y_ld = _matrix(on, "y", y, rows, width, torch.bfloat16)
+        if h_out is None:
+            h_out = on.empty((rows, width), h.dtype)
+            h_out_ld = width
+        else:
+            h_out_ld = _matrix(on, "h_out", h_out, rows, width, h.dtype)
+    if x is not None:
+        x_ld = _matrix(on, "x", x, rows, width, torch.bfloat16)
+    elif w is not None:
+        x = on.empty((rows, width), torch.bfloat16)
+        x_ld = width
+    norm = _norm(on, rows, width, (h_ld, y_ld, h_out_ld, x_ld, 0, 0, 0, 0), w, post_w, gate, row_gate, eps, w_offset, res_scale,
+                 h.dtype)
+    st = native.lib().norm_fwd(norm, h.data_ptr(), _ptr(y), _ptr(h_out), _ptr(x), _act8_arg(on, "x8", x8, rows, width),
+                               _act8_arg(on, "h8", h8, rows, width), _act8_arg(on, "y8", y8, rows, width), on.handle)
+    if st:
+        native.check("norm_fwd", st)
+    return x, h if h_out is None else h_out
+
+
+class NormGrads(NamedTuple):
+    """norm_bwd's results; None where the call has none."""
+    dh: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dw: Optional[torch.Tensor]
+    dpost_w: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    drow_gate: Optional[torch.Tensor]
+
+
+def norm_workspace_size(rows: int, width: int) -> int:
+    return int(native.lib().norm_workspace_size(rows, width))
+
+
+def norm_bwd(dx, h, w=None, *, dh=None, y=None, post_w=None, gate=None, row_gate=None, res_scale: float = 1.0,
+             eps: float = 1e-6, w_offset: float = 0.0, want_weights: bool = True, dh_out=None, dy=None, dw=None, dpost_w=None,
+             dgate=None, drow_gate=None, ws=None, stream=None) -> NormGrads:
+    """Gradients of norm_fwd from dx and dh, those of x and h' (dh None: zero; dx and h None without w).  h: the forward's h', y its
+    y, each a tensor or what act8_store or the forward kept of it in 8 bits (Act8).  Returns NormGrads: dh (of h, like
+    dh or h), dy, and with want_weights the gradients of w, post_w, gate and row_gate that were given, fp32."""
+    ref = h if h is not None else dh
+    if ref is None:
+        raise ValueError("the gradient of x or of the stream is needed")
+    on = _On(ref.codes if isinstance(ref, Act8) else ref, stream)
+    rows, width = ref.shape
+    # the stream's type: that of its gradient or of itself, bf16 where only 8 bits are given
+    stream_dtype = dh.dtype if dh is not None else torch.bfloat16 if isinstance(ref, Act8) else ref.dtype
+    if stream_dtype not in _DTYPES:
+        raise TypeError("the stream is bfloat16 or float32")
+    dx_ld = dh_ld = h_ld = y_ld = dy_ld = 0
+    h_ptr = h8 = y_ptr = y8 = None
+    if dx is not None:
+        dx_ld = _matrix(on, "dx", dx, rows, width, torch.bfloat16)
+    if dh is not None:
+        dh_ld = _matrix(on, "dh", dh, rows, width, stream_dtype)
+    if isinstance(h, Act8):
+        h8 = _act8_arg(on, "h", h, rows, width)
+    elif h is not None:
+        h_ld, h_ptr = _matrix(on, "h", h, rows, width, stream_dtype), h.data_ptr()
+    if dh_out is None:
+        dh_out, dh_out_ld = on.empty((rows, width), stream_dtype), width
+    else:
+        dh_out_ld = _matrix(on, "dh_out", dh_out, rows, width, stream_dtype)
+    if y is not None:
+        if isinstance(y, Act8):
+            y8 = _act8_arg(on, "y", y, rows, width)
+        else:
+            y_ld, y_ptr = _matrix(on, "y", y, rows, width, torch.bfloat16), y.data_ptr()
+        if dy is None:
+            dy, dy_ld = on.empty((rows, width), torch.bfloat16), width
+        else:
+            dy_ld = _matrix(on, "dy", dy, rows, width, torch.bfloat16)
+    norm = _norm(on, rows, width, (h_ld, y_ld, 0, 0, dx_ld, dh_ld, dh_out_ld, dy_ld), w, post_w, gate, row_gate, eps, w_offset,
+                 res_scale, stream_dtype)
+
+    def grad(name, given, param, n):
+        if given is not None:
+            return _given_f32(on, name, given, n)
+        return on.empty((n,), torch.float32) if want_weights and param is not None else None
+
+    dw, dpost_w, dgate = grad("dw", dw, w, width), grad("dpost_w", dpost_w, post_w, width), grad("dgate", dgate, gate, width)
+    drow_gate = grad("drow_gate", drow_gate, row_gate, rows)
+    size = 0
+    if ws is not None:
+        size = on.given(ws).numel()
+    elif dw is not None or dpost_w is not None or dgate is not None:
+        ws = on.workspace("norm", norm_workspace_size(rows, width))
+        size = ws.numel()
+    st = native.lib().norm_bwd(norm, _ptr(dx), _ptr(dh), h_ptr, h8, y_ptr, y8, dh_out.data_ptr(), _ptr(dy), _ptr(dw), _ptr(dpost_w),
+                               _ptr(dgate), _ptr(drow_gate), _ptr(ws), size, on.handle)
+    if st:
+        native.check("norm_bwd", st)
+    return NormGrads(dh_out, dy, dw, dpost_w, dgate, drow_gate)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------------------------------------------
+
+class Rope:
+    """The turns a position of each pair of features (include/lora.h).  Made once for a model."""
+
+    def __init__(self, table: native.Rope):
+        self.table, self.address = table, ctypes.addressof(table)
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, *, interleaved: bool = False, scaling: Optional[str] = None,
+               factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 32.0,
+               magnitude: float = 1.0) -> Rope:
+    """Frequencies base^(-2 i / rot_dim) of the first rot_dim features of a head, in pairs (i, i + rot_dim / 2) or, interleaved,
+    (2 i, 2 i + 1).  scaling for contexts longer than the trained ones: "linear" (over factor), "base" (a larger base) or "parts"
+    (over factor where a pair makes fewer than `low` turns over `original` positions, as they are from `high` turns on)."""
+    if scaling not in native.ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {list(native.ROPE_SCALINGS)}")
+    table = native.Rope()
+    s = native.RopeScaling(native.ROPE_SCALINGS[scaling], magnitude, factor, original, low, high)
+    native.check("rope_table", native.lib().rope_table(rot_dim, base, int(interleaved), ctypes.byref(s), ctypes.byref(table)))
+    return Rope(table)
+
+
+# lora_rope_shape in one go
+_ROPE_SHAPE = struct.Struct("qqiiii12q")
+_NO_MAT = (0, 0)
+
+
+def _positions(on: _On, positions, rows: int) -> int:
+    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_cuda or not positions.is_contiguous() or \
+            positions.shape != (rows,):
+        raise ValueError(f"positions must be a contiguous CUDA int64 or int32 vector of {rows}")
+    on.check("positions", positions)
+    return 64 if positions.dtype is torch.int64 else 32
+
+
+def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
+    on = _On(Q if Q is not None else K, stream)
+    if any(t is not None and t.dim() != 3 for t in (Q, K)):
+        raise ValueError("Q and K are rows x heads x head_dim")
+    rows, _, d = (Q if Q is not None else K).shape
+    bits = _positions(on, positions, rows)
+    hq = hk = 0
+    q = qo = k = ko = _NO_MAT
+    if Q is not None:
+        hq = Q.shape[1]
+        q = _heads(on, "Q", Q, rows, hq, d)
+        if Q_out is None:
+            Q_out = on.empty((rows, hq, d), torch.bfloat16)
+        qo = _heads(on, "Q_out", Q_out, rows, hq, d)
+    if K is not None:
+        hk = K.shape[1]
+        k = _heads(on, "K", K, rows, hk, d)
+        if K_out is None:
+            K_out = on.empty((rows, hk, d), torch.bfloat16)
+        ko = _heads(on, "K_out", K_out, rows, hk, d)
+    shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(rows, 0, hq, hk, d, bits, *q, *k, 0, 0, *qo, *ko, 0, 0))
+    st = getattr(native.lib(), name)(_ptr(Q), _ptr(K), positions.data_ptr(), shape, rope.address, _ptr(Q_out), _ptr(K_out), on.handle)
+    if st:
+        native.check(name, st)
+    return Q_out, K_out
+
+
+def rope_fwd(Q, K, positions, rope: Rope, *, Q_out=None, K_out=None, stream=None):
+    """Q (rows x q_heads x head_dim) and K (rows x kv_heads x head_dim; either may be None) turned by the positions of their rows
+    (int64 or int32, on the device).  rope: rope_table(...).  Strided slices of a fused projection are fine; Q_out=Q and K_out=K turn
+    in place.  Returns (Q_out, K_out)."""
+    return _rope("rope_fwd", Q, K, positions, rope, Q_out, K_out, stream)
+
+
+def rope_bwd(dQ, dK, positions, rope: Rope, *, dQ_out=None, dK_out=None, stream=None):
+    """Gradients of rope_fwd's Q and K from those of its outputs: the transposed rotation.  Returns (dQ_out, dK_out)."""
+    return _rope("rope_bwd", dQ, dK, positions, rope, dQ_out, dK_out, stream)
+
+
+def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_out=None, stream=None):
+    """rope_fwd on the way into a cache: each row's turned K and its V go to row slots[row] (int64, on the device) of K_cache and
+    V_cache (cache rows x kv_heads x head_dim, what attn_fwd reads; pages are runs of such rows).  A row whose slot is outside
+    the cache, -1 for example, is not stored; slots inside it must differ.  Returns the turned Q."""
+    on = _On(Q, stream)
+    if any(t.dim() != 3 for t in (Q, K, V, K_cache, V_cache)):
+        raise ValueError("Q, K, V and the caches are rows x heads x head_dim")
+    rows, hq, d = Q.shape
+    hk, cache_rows = K.shape[1], K_cache.shape[0]
+    bits = _positions(on, positions, rows)
+    _check_rows(on, "slots", slots, rows, torch.int64)
+    if Q_out is None:
+        Q_out = on.empty((rows, hq, d), torch.bfloat16)
+    shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(
+        rows, cache_rows, hq, hk, d, bits, *_heads(on, "Q", Q, rows, hq, d), *_heads(on, "K", K, rows, hk, d),
+        *_heads(on, "V", V, rows, hk, d), *_heads(on, "Q_out", Q_out, rows, hq, d),
+        *_heads(on, "K_cache", K_cache, cache_rows, hk, d), *_heads(on, "V_cache", V_cache, cache_rows, hk, d)))
+    st = native.lib().rope_append(Q.data_ptr(), K.data_ptr(), V.data_ptr(), positions.data_ptr(), slots.data_ptr(), shape,
+                                  rope.address, Q_out.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), on.handle)
+    if st:
+        native.check("rope_append", st)
+    return Q_out
 
 
 def lora_device_status(ws: torch.Tensor, stream=None) -> int:

@@ -10,6 +10,7 @@
 #include <mutex>
 #include <vector>
 
+#include "act8.h"
 #include "attn.h"
 #include "host.h"
 #include "kernels.h"
@@ -66,7 +67,8 @@ const char* const kKindNames[kKinds] = {"down_proj", "finalize_s", "gemm_fwd", "
                                         "gemm_bwd", "da", "finalize_da", "memset",
                                         "dora_u", "dora_norm", "dora_dz", "dora_dmag",
                                         "attn_fwd", "attn_join", "attn_dq", "attn_dkdv", "attn_fill",
-                                        "loss_rows", "loss_pairs", "loss_grad", "loss_sum", "adamw"};
+                                        "loss_rows", "loss_pairs", "loss_grad", "loss_sum", "adamw",
+                                        "act8_store", "act8_load", "norm_fwd", "norm_bwd", "norm_sums", "rope", "rope_append"};
 
 struct TimingRec {
     int kind;
@@ -203,13 +205,13 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
 
 // 2-D byte tensor map (keep bits): `inner` bytes per row, `outer` rows, `ld` bytes between rows, no swizzle.
 bool make_map_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
-                 uint32_t box_outer) {
+                 uint32_t box_outer, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
     cuuint64_t dims[2] = {inner, outer};
     cuuint64_t strides[1] = {ld};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) g_last_error = "cuTensorMapEncodeTiled rejected a tensor map";
     return r == CUDA_SUCCESS;
@@ -556,7 +558,7 @@ int bwd_tile_width(int64_t m, int64_t k, int64_t n) {
 // read it before waiting on its predecessor.
 lora_status run_bwd(const Call& c, const uint16_t* dY, const uint16_t* X, const uint16_t* W, const lora_adapter* ads,
                     uint64_t seed, int64_t m, int64_t k, int64_t n, const uint16_t* S_saved, const uint8_t* mask_bits,
-                    uint16_t* dX, bool dy_from_call = false) {
+                    uint16_t* dX, bool dy_from_call = false, const lora_act8* X8 = nullptr) {
     const uint32_t seed_lo = static_cast<uint32_t>(seed), seed_hi = static_cast<uint32_t>(seed >> 32);
     const int nad = c.rt.n_adapters;
     uint16_t* dsq = reinterpret_cast<uint16_t*>(c.ws + c.L.dsq);
@@ -695,7 +697,8 @@ lora_status run_bwd(const Call& c, const uint16_t* dY, const uint16_t* X, const 
     if (fork_da || gemm_bits) {
         thread_local DaParams p;
         std::memset(&p, 0, sizeof(p));
-        if (!make_map(&p.mapX, X, k, m, k, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return LORA_ECUDA;
+        if (!X8 && !make_map(&p.mapX, X, k, m, k, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return LORA_ECUDA;
+        if (X8 && !make_map_u8(&p.mapX, X8->codes, k, m, act8_codes_ld(k), 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)) return LORA_ECUDA;
         for (int a = 0; a < nad; ++a) {
             const int rp = c.rpads[a];
             if (!make_map(&p.mapD[a], dsq, c.s_ld, m, c.s_ld, std::min(rp, 64), 128, rank_swizzle_host(rp)))
@@ -729,6 +732,12 @@ lora_status run_bwd(const Call& c, const uint16_t* dY, const uint16_t* X, const 
             if (!make_map_u8(&p.mapBits, gemm_bits ? ws_bits : mask_bits, k / 8, m, k / 8, 16, 128)) return LORA_ECUDA;
             p.off_bits = p.stage_bytes;
             p.stage_bytes += 2048;
+        }
+        if (X8) {
+            p.scales = X8->scales;
+            p.scales_ld = act8_scales_ld(k);
+            p.off_codes = p.stage_bytes;
+            p.stage_bytes += 128 * 128;
         }
         // three mask groups where the ring holds three stages (as the down-projection), else two
         p.groups = mask_ring_stages(p.stage_bytes, 8, 3) >= 3 ? 3 : 2;
@@ -883,10 +892,16 @@ lora_status multi_lora_fwd(const lora_bf16* X, const lora_bf16* W, const lora_ad
     return run_fwd(c, X, W, adapters, seed, m, k, n, Y, S_saved, mask_bits);
 }
 
-lora_status multi_lora_bwd(const lora_bf16* dY, const lora_bf16* X, const lora_bf16* W, const lora_adapter* adapters,
-                           int32_t n_adapters, const lora_segment* segments, int32_t n_segments, uint64_t seed,
-                           int64_t m, int64_t k, int64_t n, const lora_bf16* S_saved, const uint8_t* mask_bits,
-                           lora_bf16* dX, void* workspace, size_t workspace_bytes, void* stream) {
+static lora_status multi_bwd(const lora_bf16* dY, const lora_bf16* X, const lora_act8* X8, const lora_bf16* W,
+                             const lora_adapter* adapters, int32_t n_adapters, const lora_segment* segments,
+                             int32_t n_segments, uint64_t seed, int64_t m, int64_t k, int64_t n, const lora_bf16* S_saved,
+                             const uint8_t* mask_bits, lora_bf16* dX, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    if (X8) {
+        if (m > 0 && (!X8->codes || !X8->scales)) return LORA_EINVAL;
+        if (!aligned16(X8->codes) || reinterpret_cast<uintptr_t>(X8->scales) % 4) return LORA_EALIGN;
+        X = reinterpret_cast<const lora_bf16*>(X8->codes);   // for the checks that both forms make
+    }
     if (!W || (m > 0 && (!X || !dY || !dX))) return LORA_EINVAL;
     if (!aligned16(dY) || !aligned16(X) || !aligned16(W) || !aligned16(dX) || !aligned16(S_saved) ||
         !aligned16(mask_bits))
@@ -896,7 +911,35 @@ lora_status multi_lora_bwd(const lora_bf16* dY, const lora_bf16* X, const lora_b
     lora_status st = prepare(c, adapters, n_adapters, segments, n_segments, m, k, n, true, workspace,
                              workspace_bytes, stream);
     if (st) return st;
-    return run_bwd(c, dY, X, W, adapters, seed, m, k, n, S_saved, mask_bits, dX);
+    return run_bwd(c, dY, X, W, adapters, seed, m, k, n, S_saved, mask_bits, dX, false, X8);
+}
+
+lora_status multi_lora_bwd(const lora_bf16* dY, const lora_bf16* X, const lora_bf16* W, const lora_adapter* adapters,
+                           int32_t n_adapters, const lora_segment* segments, int32_t n_segments, uint64_t seed,
+                           int64_t m, int64_t k, int64_t n, const lora_bf16* S_saved, const uint8_t* mask_bits,
+                           lora_bf16* dX, void* workspace, size_t workspace_bytes, void* stream) {
+    return multi_bwd(dY, X, nullptr, W, adapters, n_adapters, segments, n_segments, seed, m, k, n, S_saved, mask_bits, dX,
+                     workspace, workspace_bytes, stream);
+}
+
+lora_status multi_lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_bf16* W,
+                                const lora_adapter* adapters, int32_t n_adapters, const lora_segment* segments,
+                                int32_t n_segments, uint64_t seed, int64_t m, int64_t k, int64_t n,
+                                const lora_bf16* S_saved, const uint8_t* mask_bits, lora_bf16* dX, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    if (!X8) return LORA_EINVAL;
+    return multi_bwd(dY, nullptr, X8, W, adapters, n_adapters, segments, n_segments, seed, m, k, n, S_saved, mask_bits, dX,
+                     workspace, workspace_bytes, stream);
+}
+
+lora_status lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_bf16* W, const lora_bf16* A,
+                          const lora_bf16* B, const lora_bf16* S_saved, const uint8_t* mask_bits, float alpha, float p,
+                          uint64_t seed, int64_t m, int64_t k, int64_t n, int32_t r, lora_bf16* dX, lora_bf16* dA,
+                          lora_bf16* dB, void* workspace, size_t workspace_bytes, void* stream) {
+    lora_adapter ad{r, alpha, p, A, B, dA, dB};
+    lora_segment seg{0, m, 0, 0};
+    return multi_lora_bwd_act8(dY, X8, W, &ad, 1, &seg, m > 0 ? 1 : 0, seed, m, k, n, S_saved, mask_bits, dX, workspace,
+                               workspace_bytes, stream);
 }
 
 lora_status lora_fwd(const lora_bf16* X, const lora_bf16* W, const lora_bf16* A, const lora_bf16* B, float alpha,

@@ -29,7 +29,7 @@ enum Kind : int {
     kDownProj = 0, kFinalizeS, kGemmFwd, kDsDb, kFinalize, kGemmBwd, kDa, kFinalizeDa, kMemset,
     kDoraU, kDoraNorm, kDoraDz, kDoraDmag,
     kAttnFwd, kAttnJoin, kAttnDq, kAttnDkDv, kAttnFill, kLossRows, kLossPairs, kLossGrad, kLossSum,
-    kAdamW, kKinds
+    kAdamW, kAct8Store, kAct8Load, kNormFwd, kNormBwd, kNormSums, kRope, kRopeAppend, kKinds
 };
 static_assert(static_cast<int>(kKinds) == static_cast<int>(LORA_KERNEL_KINDS), "the header counts the kinds");
 

@@ -12,8 +12,11 @@
 // MN-major (M = 128 features, N = rank, K = 128 tokens) accumulating over a
 // CTA's run of tiles of one (adapter, feature block), and the run's partial is
 // added into the adapter's fp32 accumulator with vector reductions.
+// With X in 8 bits (k8) a stage also holds the tile's codes (one TMA box of 128 bytes a row), and the same warps turn
+// them into the two bf16 boxes, masked on the way: code * scale is a bf16 value, so the product is that of the bf16 X.
 // finalize_da then writes dA in bf16 and clears the accumulators and dSq
 // (dA is dSq's last reader), so the workspace ends the call all zeros.
+#include "act8.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -28,6 +31,7 @@ constexpr int kChunks = 16;                        // 16-byte chunks of a token 
 constexpr int kBatch = 8;                          // Philox calls computed before their chunks are masked
 static_assert(kGroupThreads == 128, "a group is four warps: one thread per token row, one warp per TMEM lane quadrant");
 constexpr uint32_t kXBytes = 2u * 128u * 128u;   // 128 tokens x 128 features
+constexpr uint32_t kCodeBytes = 128u * 128u;      // the same in 8 bits
 
 struct DaUnit {
     int a, fb, ti, tile, n_a;
@@ -64,8 +68,16 @@ __device__ __forceinline__ void da_next(DaUnit& d, const DaParams& p) {
     d.tile = p.rt.active_tiles[p.rt.adapter_begin[d.a] + d.ti];
 }
 
-// G mask groups take the ring's stages in turn (S % G == 0).
-template <int G>
+// The 16-byte chunk of eight values (columns 8 i ..) of a row from codes and their block's scale.
+__device__ __forceinline__ uint4 decode_chunk(uint32_t lo, uint32_t hi, float scale) {
+    float a[4], b[4];
+    act8_decode4(lo, scale, a);
+    act8_decode4(hi, scale, b);
+    return make_uint4(exact_bf16x2(a[0], a[1]), exact_bf16x2(a[2], a[3]), exact_bf16x2(b[0], b[1]), exact_bf16x2(b[2], b[3]));
+}
+
+// G mask groups take the ring's stages in turn (S % G == 0).  k8: X comes in 8 bits.
+template <int G, bool k8>
 __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_constant__ DaParams p) {
     constexpr int kGroups = G;
     extern __shared__ uint8_t smem_raw[];
@@ -138,10 +150,14 @@ __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_const
                 const int rpad = p.rt.ad[d.a].rpad;
                 if (!mbar_wait(&empty[s], ph ^ 1u, w, 1)) { ok = false; break; }
                 uint8_t* st = smem + s * p.stage_bytes;
-                mbar_arrive_expect_tx(&full[s], kXBytes + 256u * static_cast<uint32_t>(rpad) + (p.use_bits ? 2048u : 0u));
+                mbar_arrive_expect_tx(&full[s], (k8 ? kCodeBytes : kXBytes) + 256u * static_cast<uint32_t>(rpad) + (p.use_bits ? 2048u : 0u));
                 if (p.use_bits) tma_load_2d(st + p.off_bits, &p.mapBits, &full[s], d.fb * 16, d.tile * kTileM);
-                tma_load_2d(st, &p.mapX, &full[s], d.fb * 128, d.tile * kTileM);
-                tma_load_2d(st + 16384, &p.mapX, &full[s], d.fb * 128 + 64, d.tile * kTileM);
+                if (k8) {
+                    tma_load_2d(st + p.off_codes, &p.mapX, &full[s], d.fb * 128, d.tile * kTileM);
+                } else {
+                    tma_load_2d(st, &p.mapX, &full[s], d.fb * 128, d.tile * kTileM);
+                    tma_load_2d(st + 16384, &p.mapX, &full[s], d.fb * 128 + 64, d.tile * kTileM);
+                }
                 tma_load_2d(st + p.off_d, &p.mapD[d.a], &full[s], 0, d.tile * kTileM);
                 if (rpad > 64) tma_load_2d(st + p.off_d + 16384, &p.mapD[d.a], &full[s], 64, d.tile * kTileM);
                 ++issued;
@@ -227,6 +243,9 @@ __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_const
                 const uint32_t t = static_cast<uint32_t>(static_cast<int64_t>(d.tile) * kTileM + row);
                 const uint32_t g0 = static_cast<uint32_t>(d.fb * 16);
                 const KeepForm kf = keep_form(ad.T);
+                // the row's four scales of this feature block (rows past the last have no codes: zeros)
+                uint32_t scales = 0x7F7F7F7Fu;
+                if (k8 && t < p.m) scales = *reinterpret_cast<const uint32_t*>(p.scales + t * p.scales_ld + d.fb * 4);
                 // The first batch of keep masks depends only on (seed, row, feature): it is computed before
                 // the wait on the stage's data, so that the Philox arithmetic overlaps the TMA load.
                 uint4 km[kBatch];
@@ -249,7 +268,46 @@ __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_const
                 if (p.bits_clear != nullptr && t < p.m)
                     stg128(p.bits_clear + static_cast<int64_t>(t) * (p.k >> 3) + static_cast<int64_t>(d.fb) * 16,
                            make_uint4(0u, 0u, 0u, 0u));
-                if (ad.T != 0u && p.use_bits) {
+                if (k8) {
+                    const uint32_t sbase = smem_u32(smem + s * p.stage_bytes);
+                    const uint32_t xrow = sbase + row * 128, crow = sbase + p.off_codes + row * 128;
+                    uint32_t kw[4] = {0u, 0u, 0u, 0u};
+                    const bool bits = ad.T != 0u && p.use_bits;
+                    if (bits) {
+                        const uint4 kb4 = lds128(sbase + p.off_bits + row * 16);
+                        kw[0] = kb4.x, kw[1] = kb4.y, kw[2] = kb4.z, kw[3] = kb4.w;
+                    }
+#pragma unroll
+                    for (int c0 = 0; c0 < kChunks; c0 += kBatch) {
+                        if (regen && c0 > 0) {
+                            if (kf.half) {
+#pragma unroll
+                                for (int i = 0; i < kBatch; ++i) km[i] = keep_chunk_mask<true>(prow, g0 + c0 + i, keys, kf);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kBatch; ++i) km[i] = keep_chunk_mask<false>(prow, g0 + c0 + i, keys, kf);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kBatch; i += 2) {
+                            const int cc = c0 + i;   // this chunk of eight features and the next are sixteen codes
+                            const uint4 codes = lds128(crow + (((cc >> 1) ^ (row & 7)) << 4));
+                            const float scale = act8_scale((scales >> (8 * (cc >> 2))) & 0xFFu);
+                            uint4 v[2] = {decode_chunk(codes.x, codes.y, scale), decode_chunk(codes.z, codes.w, scale)};
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                if (bits) {
+                                    const uint32_t byte = kw[(cc + j) >> 2] >> (8 * ((cc + j) & 3));
+                                    v[j] = and4(v[j], make_uint4(keep_mask_word(byte, 0), keep_mask_word(byte, 1),
+                                                                 keep_mask_word(byte, 2), keep_mask_word(byte, 3)));
+                                } else if (regen) {
+                                    v[j] = and4(v[j], km[i + j]);
+                                }
+                                sts128(xrow + ((cc + j) >> 3) * 16384 + ((((cc + j) & 7) ^ (row & 7)) << 4), v[j]);
+                            }
+                        }
+                    }
+                } else if (ad.T != 0u && p.use_bits) {
                     // the forward's keep bits: byte cc of the row's 16 covers chunk cc (bit e = feature 8 cc + e)
                     const uint32_t sbase = smem_u32(smem + s * p.stage_bytes);
                     const uint32_t xrow = sbase + row * 128;
@@ -400,14 +458,19 @@ __global__ void stuck_wait_kernel(DevCtl ctl) {
 size_t da_smem_bytes(const DaParams& p) { return 1024 + p.stages * p.stage_bytes + (3 * p.stages + 2 * p.groups + 1) * 8 + 16; }
 
 cudaError_t da_configure() {
-    cudaError_t e = cudaFuncSetAttribute(da_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(da_kernel<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
-    return e;
+    for (auto* k : {da_kernel<2, false>, da_kernel<3, false>, da_kernel<2, true>, da_kernel<3, true>}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_da(const DaParams& p, int grid, cudaStream_t stream, bool pdl) {
-    if (p.groups == 3) return launch_k(pdl, da_kernel<3>, dim3(grid), dim3(threads_of(3)), da_smem_bytes(p), stream, p);
-    if (p.groups == 2) return launch_k(pdl, da_kernel<2>, dim3(grid), dim3(threads_of(2)), da_smem_bytes(p), stream, p);
+    const bool k8 = p.scales != nullptr;
+    if (p.groups == 3)
+        return launch_k(pdl, k8 ? da_kernel<3, true> : da_kernel<3, false>, dim3(grid), dim3(threads_of(3)), da_smem_bytes(p), stream, p);
+    if (p.groups == 2)
+        return launch_k(pdl, k8 ? da_kernel<2, true> : da_kernel<2, false>, dim3(grid), dim3(threads_of(2)), da_smem_bytes(p), stream, p);
     return cudaErrorInvalidValue;
 }
 

@@ -243,7 +243,7 @@ struct UnitBegin {
 
 // dA = (X .* D)^T dSq per adapter: per (adapter, 128-feature block, tile) unit.
 struct DaParams {
-    CUtensorMap mapX;                  // X {k, m}, box {64, 128}, 128B swizzle
+    CUtensorMap mapX;                  // X {k, m}, box {64, 128}, 128B swizzle; in 8 bits: codes, box {128, 128}
     CUtensorMap mapD[kMaxAdapters];    // dSq {s_ld, m}, box {min(rpad,64), 128}, swizzle by rpad (MN-major)
     Routing rt;
     DevCtl ctl;
@@ -262,6 +262,9 @@ struct DaParams {
     int32_t use_bits;                  // 1: the stage's keep bits come with X (at off_bits) instead of from Philox
     uint32_t off_bits;
     uint8_t* bits_clear;               // optional: the bits tensor of mapBits, whose bytes this pass zeroes once read
+    const uint8_t* scales;             // X in 8 bits: its blocks' scales (rows of scales_ld bytes); null: X is bf16
+    int64_t scales_ld;
+    uint32_t off_codes;                // and where a stage has its codes (a multiple of 1024: the swizzle's period)
     int32_t groups;                    // mask groups of four warps (2 or 3); stages % groups == 0
     Slots sl;                          // deterministic mode: dA partials per (adapter * nfb + feature block, CTA) slot
 };

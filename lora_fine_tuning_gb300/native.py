@@ -20,7 +20,9 @@ STATUS_NAMES = {0: "LORA_OK", 1: "LORA_EINVAL", 2: "LORA_EALIGN", 3: "LORA_ESHAP
 EXPORTED = ["lora_workspace_size", "lora_set_deterministic", "lora_get_deterministic", "lora_fwd", "lora_bwd", "multi_lora_fwd", "multi_lora_bwd",
             "dora_workspace_size", "dora_weight_norm2", "dora_fwd", "dora_bwd",
             "lora_fwd_static_scratch", "attn_workspace_size", "attn_fwd", "attn_bwd",
-            "loss_workspace_size", "pref_loss", "policy_loss", "adamw_step", "lora_tile_table",
+            "loss_workspace_size", "pref_loss", "policy_loss", "adamw_step",
+            "act8_store", "act8_load", "multi_lora_bwd_act8", "lora_bwd_act8", "norm_workspace_size", "norm_fwd", "norm_bwd",
+            "rope_table", "rope_fwd", "rope_bwd", "rope_append", "lora_tile_table",
             "lora_keep_threshold", "lora_pack_greedy", "lora_device_status", "lora_set_wait_limit_ns", "lora_debug_stuck_wait",
             "lora_debug_gemm_runs",
             "lora_status_string", "lora_timing_begin", "lora_timing_end", "lora_kernel_name",
@@ -75,6 +77,42 @@ class AdamWTensor(ctypes.Structure):
                 ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Vector(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("h", ctypes.c_int64), ("y", ctypes.c_int64),
+                ("h_out", ctypes.c_int64), ("x", ctypes.c_int64), ("dx", ctypes.c_int64), ("dh", ctypes.c_int64),
+                ("dh_out", ctypes.c_int64), ("dy", ctypes.c_int64), ("w", Vector), ("post_w", Vector), ("gate", Vector),
+                ("row_gate", Vector), ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("stream_dtype", ctypes.c_int32)]
+
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("magnitude", ctypes.c_float), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 128)]
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cache_rows", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("positions_bits", ctypes.c_int32),
+                ("q", AttnStrides), ("k", AttnStrides), ("v", AttnStrides), ("q_out", AttnStrides),
+                ("k_out", AttnStrides), ("v_out", AttnStrides)]
+
+
 class LoraError(RuntimeError):
     def __init__(self, fn: str, status: int):
         detail = ""
@@ -100,6 +138,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, u64, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
                                            ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
+        a8 = ctypes.POINTER(Act8)
         sig = {
             "lora_workspace_size": (sz, [i64, i64, i64, i32, i32]),
             "lora_set_deterministic": (i32, [i32]),
@@ -124,6 +163,18 @@ def lib() -> ctypes.CDLL:
             "pref_loss": (i32, [ctypes.POINTER(Logits), vp, i32, vp, f32, f32, f32, vp, vp, vp, sz, vp]),
             "policy_loss": (i32, [ctypes.POINTER(Logits), vp, vp, vp, f32, f32, f32, f32, vp, vp, sz, vp]),
             "adamw_step": (i32, [vp, i32, f64, f64, f64, f64, f64, i64, vp, vp]),
+            "act8_store": (i32, [vp, i64, i64, i64, a8, vp]),
+            "act8_load": (i32, [a8, i64, i64, vp, i64, vp]),
+            "multi_lora_bwd_act8": (i32, [vp, a8, vp, ctypes.POINTER(LoraAdapter), i32, ctypes.POINTER(LoraSegment), i32,
+                                          u64, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
+            "lora_bwd_act8": (i32, [vp, a8, vp, vp, vp, vp, vp, f32, f32, u64, i64, i64, i64, i32, vp, vp, vp, vp, sz, vp]),
+            "norm_workspace_size": (sz, [i64, i64]),
+            "norm_fwd": (i32, [ctypes.POINTER(Norm), vp, vp, vp, vp, a8, a8, a8, vp]),
+            "norm_bwd": (i32, [ctypes.POINTER(Norm), vp, vp, vp, a8, vp, a8, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "rope_table": (i32, [i32, f64, i32, vp, vp]),
+            "rope_fwd": (i32, [vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp]),
+            "rope_bwd": (i32, [vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp]),
+            "rope_append": (i32, [vp, vp, vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp, vp]),
             "lora_tile_table": (i32, [ctypes.POINTER(LoraSegment), i32, i32, i64, ctypes.POINTER(ctypes.c_int32),
                                       i64]),
             "lora_keep_threshold": (i32, [f32, ctypes.POINTER(ctypes.c_uint32)]),
@@ -247,7 +298,7 @@ def gemm_runs(M: int, N: int, bn: int, stages: int, max_pairs: int, allow_split:
     return pairs.value, split.value, runs
 
 
-KERNEL_KINDS = 23
+KERNEL_KINDS = 30
 
 
 def timing_begin() -> None:
