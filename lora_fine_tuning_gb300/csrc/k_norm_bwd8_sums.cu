@@ -1,0 +1,10 @@
+// The backward of the norms around a block from what was kept in 8 bits, with the weights' gradients.
+#include "norm_bwd.cuh"
+
+namespace lora {
+
+cudaError_t norm_bwd8_sums_configure() { return configure_form<true, true>(); }
+
+cudaError_t launch_norm_bwd8_sums(NormBwd& p, int sms, cudaStream_t stream) { return launch_norm_bwd_form<true, true>(p, sms, stream); }
+
+}  // namespace lora

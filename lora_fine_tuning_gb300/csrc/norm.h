@@ -21,7 +21,8 @@ struct NormAct8 {
 // What the forward and the backward have in common.
 struct NormShape {
     int32_t rows, width;
-    int32_t vector;                     // rows start on 16-byte boundaries and are whole vectors of eight values
+    int32_t ragged;                     // some matrix has rows that do not start on 16 bytes or are not whole units of eight values
+    int32_t vectors;                    // w, post and gate are whole vectors of eight values on 16-byte boundaries
     int32_t f32;                        // the stream is fp32
     NormVec w, post, gate, row_gate;
     float eps, offset, res, inv_width;
@@ -34,8 +35,10 @@ struct NormFwd {
     const uint16_t* y;                  // may be null
     void* h_out;                        // null where y is
     uint16_t* x;                        // null where w is
-    int64_t h_ld, y_ld, h_out_ld, x_ld;
+    int64_t h_ld, y_ld, h_out_ld, x_ld;   // bytes
     NormAct8 x8, h8, y8;
+    int32_t stages;                     // of a row group's ring in shared memory, and their bytes (the launch sets them)
+    uint32_t stage_bytes, at_y;
 };
 
 struct NormBwd {
@@ -46,20 +49,28 @@ struct NormBwd {
     const uint16_t* y;                  // may be null (or y8)
     void* dh_out;
     uint16_t* dy;                       // may be null
-    int64_t dx_ld, dh_ld, h_ld, y_ld, dh_out_ld, dy_ld;
+    int64_t dx_ld, dh_ld, h_ld, y_ld, dh_out_ld, dy_ld;   // bytes
     NormAct8 h8, y8;
     float* part;                        // sums over each group's rows: groups x 2 x width; null: no weights' gradients
     float *dw, *dpost, *dgate, *drow;   // each may be null
-    int32_t groups;
+    // set by the launch
+    int32_t groups, stages;
+    uint32_t stage_bytes, at_dx, at_h, at_dh, at_y;
 };
 
-// Threads that share a row, and how many rows a CTA works on at once (one, or a warp a row).
-int norm_threads(int width);
-// Groups of rows that the backward sums over: the partial sums' first extent.
+// The most groups of rows that the backward sums over: the partial sums' first extent.
 int norm_bwd_groups(int rows, int width, int sms);
 
+cudaError_t norm_fwd_configure();
+cudaError_t norm_bwd_configure();
+cudaError_t norm_bwd_sums_configure();
+cudaError_t norm_bwd8_configure();
+cudaError_t norm_bwd8_sums_configure();
 cudaError_t launch_norm_fwd(const NormFwd& p, int sms, cudaStream_t stream);
-cudaError_t launch_norm_bwd(const NormBwd& p, int sms, cudaStream_t stream);
+cudaError_t launch_norm_bwd(NormBwd& p, int sms, cudaStream_t stream);        // without the weights' gradients
+cudaError_t launch_norm_bwd_sums(NormBwd& p, int sms, cudaStream_t stream);   // with their sums over each CTA's rows
+cudaError_t launch_norm_bwd8(NormBwd& p, int sms, cudaStream_t stream);       // the same where h or y is in 8 bits
+cudaError_t launch_norm_bwd8_sums(NormBwd& p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_sums(const NormBwd& p, cudaStream_t stream);
 
 }  // namespace lora

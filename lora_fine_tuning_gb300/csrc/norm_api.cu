@@ -18,7 +18,7 @@ bool aligned(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>
 struct Checker {
     int64_t rows, width;
     lora_status st = LORA_OK;
-    bool vector = true;
+    bool vectors = true, ragged = false;
     void fail(lora_status s) {
         if (!st) st = s;
     }
@@ -29,13 +29,13 @@ struct Checker {
         }
         if (ld < width || ld >= (int64_t{1} << 38)) fail(LORA_ESHAPE);
         if (!aligned(p, size)) fail(LORA_EALIGN);
-        vector = vector && aligned16(p) && (ld * size) % 16 == 0;
+        ragged = ragged || !aligned16(p) || (ld * size) % 16;
     }
     NormVec vec(const lora_vector& v, bool whole) {
         if (!v.data) return NormVec{nullptr, 0};
         if (v.dtype != LORA_BF16 && v.dtype != LORA_F32) fail(LORA_EINVAL);
         if (!aligned(v.data, v.dtype == LORA_F32 ? 4 : 2)) fail(LORA_EALIGN);
-        if (whole) vector = vector && aligned16(v.data);
+        if (whole) vectors = vectors && aligned16(v.data);
         return NormVec{v.data, v.dtype == LORA_F32};
     }
     NormAct8 act8(const lora_act8* a) {
@@ -53,7 +53,8 @@ lora_status check_shape(const lora_norm* n, Checker& c, NormShape& s) {
     if (!(n->eps >= 1e-30f) || !std::isfinite(n->eps) || !std::isfinite(n->w_offset) || !std::isfinite(n->res_scale)) return LORA_EINVAL;
     c.rows = n->rows;
     c.width = n->width;
-    c.vector = n->width % 8 == 0;
+    c.vectors = n->width % 8 == 0;
+    c.ragged = !c.vectors;
     s.rows = static_cast<int32_t>(n->rows);
     s.width = static_cast<int32_t>(n->width);
     s.f32 = n->stream_dtype == LORA_F32;
@@ -64,6 +65,7 @@ lora_status check_shape(const lora_norm* n, Checker& c, NormShape& s) {
     s.eps = n->eps;
     s.offset = n->w_offset;
     s.res = n->res_scale;
+    s.vectors = c.vectors;
     s.inv_width = static_cast<float>(1.0 / static_cast<double>(n->width));
     s.codes_ld = act8_codes_ld(n->width);
     s.scales_ld = act8_scales_ld(n->width);
@@ -110,9 +112,9 @@ lora_status norm_fwd(const lora_norm* norm, const void* h, const lora_bf16* y, v
     int sms = 0;
     if ((st = device_setup(&sms))) return st;
     if (norm->rows == 0) return LORA_OK;
-    p.s.vector = c.vector;
+    p.s.ragged = c.ragged;
     p.h = h, p.y = y, p.h_out = h_out, p.x = x;
-    p.h_ld = norm->h, p.y_ld = norm->y, p.h_out_ld = norm->h_out, p.x_ld = norm->x;
+    p.h_ld = norm->h * size, p.y_ld = norm->y * 2, p.h_out_ld = norm->h_out * size, p.x_ld = norm->x * 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LORA_CUDA(timed(kNormFwd, s, [&] { return launch_norm_fwd(p, sms, s); }));
     return LORA_OK;
@@ -151,13 +153,13 @@ lora_status norm_bwd(const lora_norm* norm, const lora_bf16* dx, const void* dh,
     if ((st = device_setup(&sms))) return st;
     sms = std::min(sms, kMaxSms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    p.s.vector = c.vector;
     p.dx = dx, p.dh = dh, p.h = h, p.y = y, p.dh_out = dh_out, p.dy = dy;
-    p.dx_ld = norm->dx, p.dh_ld = norm->dh, p.h_ld = norm->h, p.y_ld = norm->y, p.dh_out_ld = norm->dh_out, p.dy_ld = norm->dy;
+    p.s.ragged = c.ragged;
+    p.dx_ld = norm->dx * 2, p.dh_ld = norm->dh * size, p.h_ld = norm->h * size, p.y_ld = norm->y * 2, p.dh_out_ld = norm->dh_out * size, p.dy_ld = norm->dy * 2;
     p.dw = dw, p.dpost = dpost_w, p.dgate = dgate, p.drow = drow_gate;
-    p.groups = norm->rows > 0 ? norm_bwd_groups(p.s.rows, p.s.width, sms) : 0;
     p.part = sums ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256) : nullptr;
-    if (norm->rows > 0) LORA_CUDA(timed(kNormBwd, s, [&] { return launch_norm_bwd(p, sms, s); }));
+    auto* launch = h8 || y8 ? (sums ? launch_norm_bwd8_sums : launch_norm_bwd8) : (sums ? launch_norm_bwd_sums : launch_norm_bwd);
+    if (norm->rows > 0) LORA_CUDA(timed(kNormBwd, s, [&] { return launch(p, sms, s); }));
     if (sums) LORA_CUDA(timed(kNormSums, s, [&] { return launch_norm_sums(p, s); }));
     return LORA_OK;
 }
