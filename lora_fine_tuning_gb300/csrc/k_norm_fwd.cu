@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
     const Mat<T, V, false, kRagged, false> Y(p.y, p.y_ld, none, s, p.at_y, t);
     pdl_wait();
     pdl_trigger();
+    const int mine = kRagged ? units_of<T, V>(t, s.width) : V;
     const int step = gridDim.x * R, row0 = blockIdx.x * R + sub;
     const auto fetch = [&](int row, int slot) {
         if (row < s.rows) {
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
         if (s.post.p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                if (kRagged && i >= mine) break;
                 F2 y[4];
                 Y.read(y, stage, row, i, t);
 #pragma unroll
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
         F2 q = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if (kRagged && i >= mine) break;
             H.read(h[i], stage, row, i, t);
             if (p.y) {
                 F2 y[4], f[4];
@@ -112,13 +115,14 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
 #pragma unroll
             for (int i = 0; i < V; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) a = fma2(mul(h[i][k], both(kSmall)), mul(h[i][k], both(kSmall)), a);
+                for (int k = 0; k < 4; ++k) if (!kRagged || i < mine) a = fma2(mul(h[i][k], both(kSmall)), mul(h[i][k], both(kSmall)), a);
             float q[4] = {total(a), 0.f, 0.f, 0.f};
             sums.add(q);
             r = inverse_rms_small(q[0], s) * kSmall;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if (kRagged && i >= mine) break;
             F2 f[4];
             if (!kKept) main_factors<T>(f, s, i, t);
 #pragma unroll

@@ -422,6 +422,16 @@ struct RowAt {
     }
 };
 
+// How many of a thread's units its warp needs for a row: those of which some lane's is inside it.
+template <int T, int V>
+__device__ __forceinline__ int units_of(int t, int width) {
+    const int first = __shfl_sync(0xFFFFFFFFu, t, 0) * 8;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += i * T * 8 + first < width;
+    return n;
+}
+
 // Where V units of a thread leave the registers for it, factors are kept; wider rows form them anew.
 template <int T, int V>
 constexpr bool kept() { return V <= 2; }
@@ -454,7 +464,7 @@ struct RingPlan {
 };
 RingPlan ring_plan(int cta_bytes, int most) {
     for (int n = most; n > 1; --n)
-        for (int stages = 4; stages >= 3; --stages)
+        for (int stages = 4; stages >= 2; --stages)
             if (n * stages * cta_bytes <= kRingBudget) return RingPlan{n, stages};
     return RingPlan{1, std::max(1, std::min(4, kRingBudget / cta_bytes))};
 }

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
     const Mat<T, V, false, kRagged, kCodes> Y(p.y, p.y_ld, p.y8, s, p.at_y, t);
     pdl_wait();
     pdl_trigger();
+    const int mine = kRagged ? units_of<T, V>(t, s.width) : V;
     const auto fetch = [&](int row, int slot) {
         if (row < s.rows) {
             uint8_t* const a = ring + slot * p.stage_bytes;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
         F2 hh = both(0.f), th = both(0.f), yy = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if (kRagged && i >= mine) break;
             if (s.w.p) {
                 F2 h[4], dx[4], f[4];
                 H.read(h, stage, row, i, t);
@@ -127,6 +129,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
         F2 along = both(0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if (kRagged && i >= mine) break;
             Dh.read(d[i], stage, row, i, t);
             if (s.w.p) {
                 F2 h[4], dx[4], f[4];
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
         const float m = s.post.p ? along * rg * s.inv_width : 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if (kRagged && i >= mine) break;
             F2 f[4];
             if (s.post.p) {
                 F2 y[4];
