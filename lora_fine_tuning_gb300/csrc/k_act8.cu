@@ -6,6 +6,7 @@
 #include "act8.cuh"
 #include "act8.h"
 #include "kernels.h"
+#include "rows.cuh"
 
 namespace lora {
 
@@ -14,47 +15,42 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnits = 4;
 
-// Eight values of a row from column c on; those past the row's end are zero.
-template <bool kVec>
-__device__ __forceinline__ uint4 load_unit(const uint16_t* row, int c, int width) {
-    if (kVec && c + 8 <= width) return __ldcs(reinterpret_cast<const uint4*>(row + c));
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < width) w[i / 2] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <bool kVec>
-__device__ __forceinline__ void store_unit(uint16_t* row, int c, int width, uint4 x) {
-    if (kVec && c + 8 <= width) {
-        *reinterpret_cast<uint4*>(row + c) = x;
-        return;
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < width) row[c + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-}
-
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads) act8_store_kernel(const Act8Params p) {
     pdl_wait();
     pdl_trigger();
     const uint32_t u0 = blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    uint4 x[kUnits];
-    uint32_t row[kUnits], at[kUnits];
+    const int bytes = p.width * 2;
+    const bool end_lane = (threadIdx.x & 31) == 31;
+    uint4 x[kUnits], more[kVec ? 1 : kUnits];
+    uint32_t row[kUnits], at[kUnits], shift[kVec ? 1 : kUnits];
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t u = u0 + i * kThreads;
         row[i] = u / p.per_row;
         at[i] = u - row[i] * p.per_row;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (u < p.units) x[i] = load_unit<kVec>(p.x + row[i] * p.ld, static_cast<int>(at[i]) * 8, p.width);
+        if (!kVec) more[kVec ? 0 : i] = x[i], shift[kVec ? 0 : i] = 0;
+        if (u >= p.units) continue;
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(p.x + row[i] * p.ld);
+        const int b = static_cast<int>(at[i]) * 16;
+        if (kVec) {
+            x[i] = load_block<2>(src, b, bytes);
+        } else {
+            const int s = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u);
+            shift[kVec ? 0 : i] = s;
+            x[i] = load_block<2>(src, b - s, bytes);
+            if (s && (end_lane || at[i] + 1 == p.per_row)) more[kVec ? 0 : i] = load_block<2>(src, b - s + 16, bytes);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t u = u0 + i * kThreads;
+        if (!kVec) {
+            uint4 next = shuffle_down(x[i]);
+            if (end_lane || at[i] + 1 == p.per_row) next = more[kVec ? 0 : i];
+            x[i] = shifted(x[i], next, shift[kVec ? 0 : i]);
+        }
         uint32_t e;
         const uint2 c = act8_encode8(x[i], e);
         if (u >= p.units) continue;
@@ -92,14 +88,20 @@ __global__ void __launch_bounds__(kThreads) act8_load_kernel(const Act8Params p)
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        if (u0 + i * kThreads >= p.units) continue;
         const float scale = act8_scale(e[i]);
         float a[4], b[4];
         act8_decode4(c[i].x, scale, a);
         act8_decode4(c[i].y, scale, b);
-        store_unit<kVec>(p.x + row[i] * p.ld, static_cast<int>(at[i]) * 8, p.width,
-                         make_uint4(exact_bf16x2(a[0], a[1]), exact_bf16x2(a[2], a[3]), exact_bf16x2(b[0], b[1]),
-                                    exact_bf16x2(b[2], b[3])));
+        const uint4 x = make_uint4(exact_bf16x2(a[0], a[1]), exact_bf16x2(a[2], a[3]), exact_bf16x2(b[0], b[1]), exact_bf16x2(b[2], b[3]));
+        const uint4 before = kVec ? x : shuffle_up(x);
+        if (u0 + i * kThreads >= p.units) continue;
+        const int lane = threadIdx.x & 31;
+        const bool first = lane == 0 || at[i] == 0, last = lane == 31 || at[i] + 1 == p.per_row;
+        uint8_t* to = reinterpret_cast<uint8_t*>(p.x + row[i] * p.ld);
+        const int from = static_cast<int>(at[i]) * 16, left = p.width * 2 - from;
+        if (!kVec) store16<2>(to, from, p.width * 2, x, before, first, last);
+        else if (left >= 16) __stcs(reinterpret_cast<uint4*>(to + from), x);
+        else if (left > 0) store_parts<2>(to + from, x, 0, left / 2);
     }
 }
 

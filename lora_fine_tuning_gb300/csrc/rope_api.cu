@@ -107,15 +107,19 @@ lora_status run(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, cons
     p.rows = static_cast<int32_t>(g.rows), p.q_heads = hq, p.kv_heads = hk, p.d = d, p.rot = rot;
     p.interleaved = rope->interleaved;
     p.back = back;
-    p.q_copies = Qo != Q, p.k_copies = Ko != K;
+    // a unit is two vectors
     p.units = rot / 2 / W;
-    p.copies = p.q_copies || p.k_copies ? (d - rot) / W : 0;
-    p.v_units = append ? d / W : 0;
-    const uint32_t each = static_cast<uint32_t>(p.units + p.copies);
-    p.head_magic = each == 1 ? 0u : static_cast<uint32_t>(((uint64_t{1} << 32) + each - 1) / each);
-    // a row's heads go to several warps where the rows alone would give an SM fewer than sixteen
-    const int64_t want = (static_cast<int64_t>(sms) * 16 + g.rows - 1) / g.rows;
-    p.chunks = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(want, std::max(1, (hq + hk) / 2))));
+    p.q_copies = Qo != Q ? ((d - rot) / W + 1) / 2 : 0;
+    p.k_copies = Ko != K ? ((d - rot) / W + 1) / 2 : 0;
+    p.v_units = append ? (d / W + 1) / 2 : 0;
+    p.each = std::max({hq ? p.units + p.q_copies : 0, hk ? p.units + p.k_copies : 0, p.v_units});
+    p.g = std::max(1, 32 / p.each);
+    // an item has as many heads as its lanes take; fewer where the rows would give an SM fewer than sixteen items
+    const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    const int64_t least = std::max<int64_t>({1, up(hq, kRopeQHeads * p.g), up(hk, kRopeKHeads * p.g)}), most = std::max<int64_t>(least, up(std::max(hq, hk), p.g));
+    p.items = static_cast<int32_t>(std::min(std::max(least, up(static_cast<int64_t>(sms) * 16, g.rows)), most));
+    p.q_each = static_cast<int32_t>(up(hq, p.items));
+    p.k_each = static_cast<int32_t>(up(hk, p.items));
     p.positions = positions;
     p.positions64 = g.positions_bits == 64;
     p.slots = append ? slots : nullptr;
