@@ -9,6 +9,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace lora {
 
@@ -30,10 +31,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// The code of one bf16 value (its bits in the upper half of `x`), in the low byte; the other bytes are undefined.
+// The code of one bf16 value (its bits in the upper half of `x`), in the low byte; the other bytes are undefined.  The product is exact, the
+// sum with 1.5 * 2^23 rounds it to a whole number, even on ties, whose bits are the sum's last.
+constexpr float kAct8Magic = 12582912.f;
 __device__ __forceinline__ uint32_t act8_code(uint32_t x, float inverse) {
     const float v = fminf(fmaxf(__uint_as_float(x) * inverse, -127.f), 127.f);
-    return __float_as_uint(v + 12582912.f);   // 1.5 * 2^23: the sum's last bits are the whole number, rounded to even
+    return __float_as_uint(v + kAct8Magic);
 }
 
 // A finite value's largest |x| counts; the rest of a block is what holds an infinity or NaN.
@@ -61,8 +64,18 @@ __device__ __forceinline__ uint2 act8_encode8(uint4 x, uint32_t& exponent) {
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        c[2 * i] = act8_code(w[i] << 16, inverse);
-        c[2 * i + 1] = act8_code(w[i] & 0xFFFF0000u, inverse);
+        const float2 v = parts(fma2(f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), f2(inverse, inverse),
+                                    f2(kAct8Magic, kAct8Magic)));
+        c[2 * i] = __float_as_uint(v.x);
+        c[2 * i + 1] = __float_as_uint(v.y);
+    }
+    // only a block whose largest value has all fraction bits set holds 127.5 scales, which would round to 128
+    if (__any_sync(0xFFFFFFFFu, (top & 0x7Fu) == 0x7Fu)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[2 * i] = act8_code(w[i] << 16, inverse);
+            c[2 * i + 1] = act8_code(w[i] & 0xFFFF0000u, inverse);
+        }
     }
     if (odd) {
 #pragma unroll

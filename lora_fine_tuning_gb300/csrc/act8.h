@@ -18,6 +18,7 @@ struct Act8Params {
     uint32_t per_row;      // units of eight codes in a row of codes
     uint32_t units;        // rows * per_row
     int32_t vector;        // whole units of x are 16-byte aligned
+    uint32_t magic, shift; // u / per_row = high word of (u magic) >> shift, for u below 2^31
 };
 
 cudaError_t launch_act8_store(const Act8Params& p, cudaStream_t stream);

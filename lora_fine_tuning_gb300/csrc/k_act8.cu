@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kThreads) act8_store_kernel(const Act8Params p
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t u = u0 + i * kThreads;
-        row[i] = u / p.per_row;
+        row[i] = __umulhi(u, p.magic) >> p.shift;
         at[i] = u - row[i] * p.per_row;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (!kVec) more[kVec ? 0 : i] = x[i], shift[kVec ? 0 : i] = 0;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) act8_load_kernel(const Act8Params p)
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
         const uint32_t u = u0 + i * kThreads;
-        row[i] = u / p.per_row;
+        row[i] = __umulhi(u, p.magic) >> p.shift;
         at[i] = u - row[i] * p.per_row;
         c[i] = make_uint2(0u, 0u);
         e[i] = 127;
