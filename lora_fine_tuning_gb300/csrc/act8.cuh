@@ -116,6 +116,40 @@ __device__ __forceinline__ float act8_decode1(uint32_t code, float scale) {
     return c == -128 ? __int_as_float(0x7FC00000) : static_cast<float>(c) * scale;
 }
 
+// Sixteen codes -> sixteen bf16 values, exact, without fp32 in between: a byte's low seven bits are the fraction of 128 + low (0x43..) and its
+// top bit that of 128 or 256, whose difference is the code.  `scale2`: the blocks' scale in bf16, twice.
+__device__ __forceinline__ uint32_t act8_scale2(uint32_t exponent) { return exponent * 0x00800080u; }
+__device__ __forceinline__ uint32_t code_pair(uint32_t bytes, uint32_t scale2) {
+    uint32_t r;
+    asm("{\n.reg .b32 d;\nsub.rn.bf16x2 d, %1, %2;\nmul.rn.bf16x2 %0, d, %3;\n}"
+        : "=r"(r) : "r"(bytes & 0xFF7FFF7Fu), "r"(bytes & 0xFF80FF80u), "r"(scale2));
+    return r;
+}
+__device__ __forceinline__ void act8_decode16(uint4 codes, uint32_t scale2, uint4 (&v)[2]) {
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t w[8], none = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[2 * i] = code_pair(__byte_perm(c[i], 0x43434343u, 0x4140), scale2);
+        w[2 * i + 1] = code_pair(__byte_perm(c[i], 0x43434343u, 0x4342), scale2);
+        const uint32_t u = c[i] ^ 0x80808080u;
+        none |= (u - 0x01010101u) & ~u & 0x80808080u;   // not zero where a code is -128
+    }
+    if (none) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t two = c[i / 2] >> (16 * (i & 1));
+            if ((two & 0xFFu) == 0x80u) w[i] = (w[i] & 0xFFFF0000u) | 0x7FC0u;
+            if ((two & 0xFF00u) == 0x8000u) w[i] = (w[i] & 0xFFFFu) | 0x7FC00000u;
+        }
+    }
+    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Four bits -> a mask of four bytes.
+__device__ __forceinline__ uint32_t byte_mask(uint32_t bits) { return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu; }
+
 // Two fp32 values whose lower halves are zero -> two bf16, exact.
 __device__ __forceinline__ uint32_t exact_bf16x2(float lo, float hi) {
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);

@@ -744,6 +744,7 @@ lora_status run_bwd(const Call& c, const uint16_t* dY, const uint16_t* X, const 
         }
         // three mask groups where the ring holds three stages (as the down-projection), else two
         p.groups = mask_ring_stages(p.stage_bytes, 8, 3) >= 3 ? 3 : 2;
+        if (X8 && mask_ring_stages(p.stage_bytes, 8, 4) >= 4) p.groups = 4;   // the codes' arithmetic wants the warps
         p.stages = mask_ring_stages(p.stage_bytes, 8, p.groups);
         const int grid = static_cast<int>(std::min<int64_t>(p.units, c.sms));
         if (c.det) p.sl = Slots{reinterpret_cast<float*>(c.ws + c.L.slots), p.units, grid, static_cast<int32_t>(rpm)};

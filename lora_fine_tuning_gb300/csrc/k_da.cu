@@ -68,14 +68,6 @@ __device__ __forceinline__ void da_next(DaUnit& d, const DaParams& p) {
     d.tile = p.rt.active_tiles[p.rt.adapter_begin[d.a] + d.ti];
 }
 
-// The 16-byte chunk of eight values (columns 8 i ..) of a row from codes and their block's scale.
-__device__ __forceinline__ uint4 decode_chunk(uint32_t lo, uint32_t hi, float scale) {
-    float a[4], b[4];
-    act8_decode4(lo, scale, a);
-    act8_decode4(hi, scale, b);
-    return make_uint4(exact_bf16x2(a[0], a[1]), exact_bf16x2(a[2], a[3]), exact_bf16x2(b[0], b[1]), exact_bf16x2(b[2], b[3]));
-}
-
 // G mask groups take the ring's stages in turn (S % G == 0).  k8: X comes in 8 bits.
 template <int G, bool k8>
 __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_constant__ DaParams p) {
@@ -291,18 +283,16 @@ __global__ void __launch_bounds__(threads_of(G), 1) da_kernel(const __grid_const
 #pragma unroll
                         for (int i = 0; i < kBatch; i += 2) {
                             const int cc = c0 + i;   // this chunk of eight features and the next are sixteen codes
-                            const uint4 codes = lds128(crow + (((cc >> 1) ^ (row & 7)) << 4));
-                            const float scale = act8_scale((scales >> (8 * (cc >> 2))) & 0xFFu);
-                            uint4 v[2] = {decode_chunk(codes.x, codes.y, scale), decode_chunk(codes.z, codes.w, scale)};
+                            uint4 codes = lds128(crow + (((cc >> 1) ^ (row & 7)) << 4));
+                            if (bits) {   // a dropped value's code is zero
+                                const uint32_t two = kw[cc >> 2] >> (8 * (cc & 3));
+                                codes = and4(codes, make_uint4(byte_mask(two), byte_mask(two >> 4), byte_mask(two >> 8), byte_mask(two >> 12)));
+                            }
+                            uint4 v[2];
+                            act8_decode16(codes, act8_scale2((scales >> (8 * (cc >> 2))) & 0xFFu), v);
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                if (bits) {
-                                    const uint32_t byte = kw[(cc + j) >> 2] >> (8 * ((cc + j) & 3));
-                                    v[j] = and4(v[j], make_uint4(keep_mask_word(byte, 0), keep_mask_word(byte, 1),
-                                                                 keep_mask_word(byte, 2), keep_mask_word(byte, 3)));
-                                } else if (regen) {
-                                    v[j] = and4(v[j], km[i + j]);
-                                }
+                                if (regen) v[j] = and4(v[j], km[i + j]);
                                 sts128(xrow + ((cc + j) >> 3) * 16384 + ((((cc + j) & 7) ^ (row & 7)) << 4), v[j]);
                             }
                         }
@@ -458,7 +448,7 @@ __global__ void stuck_wait_kernel(DevCtl ctl) {
 size_t da_smem_bytes(const DaParams& p) { return 1024 + p.stages * p.stage_bytes + (3 * p.stages + 2 * p.groups + 1) * 8 + 16; }
 
 cudaError_t da_configure() {
-    for (auto* k : {da_kernel<2, false>, da_kernel<3, false>, da_kernel<2, true>, da_kernel<3, true>}) {
+    for (auto* k : {da_kernel<2, false>, da_kernel<3, false>, da_kernel<2, true>, da_kernel<3, true>, da_kernel<4, true>}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
         if (e != cudaSuccess) return e;
     }
@@ -467,6 +457,7 @@ cudaError_t da_configure() {
 
 cudaError_t launch_da(const DaParams& p, int grid, cudaStream_t stream, bool pdl) {
     const bool k8 = p.scales != nullptr;
+    if (p.groups == 4 && k8) return launch_k(pdl, da_kernel<4, true>, dim3(grid), dim3(threads_of(4)), da_smem_bytes(p), stream, p);
     if (p.groups == 3)
         return launch_k(pdl, k8 ? da_kernel<3, true> : da_kernel<3, false>, dim3(grid), dim3(threads_of(3)), da_smem_bytes(p), stream, p);
     if (p.groups == 2)
