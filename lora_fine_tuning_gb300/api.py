@@ -740,28 +740,28 @@ def act8(rows: int, width: int, *, stream=None) -> Act8:
     return Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
 
 
-def _act8_arg(on: _On, name: str, a: Optional[Act8], rows: int, width: int):
+def _act8_arg(on: _On, name: str, a: Act8, rows: int, width: int):
     """Checks one matrix in 8 bits.  Returns what the library takes for it."""
-    if a is None:
-        return None
-    if a.width != width or a.codes.dtype is not torch.int8 or not a.codes.is_cuda or not a.codes.is_contiguous() or \
-            a.codes.shape != (rows, -(-width // 32) * 32):
+    codes, scales = a.codes, a.scales
+    if a.width != width or codes.dtype is not torch.int8 or not codes.is_contiguous() or codes.shape != (rows, -(-width // 32) * 32):
         raise ValueError(f"{name}.codes must be a contiguous CUDA int8 tensor of shape {(rows, -(-width // 32) * 32)}, its width {width}")
-    if a.scales.dtype is not torch.uint8 or not a.scales.is_cuda or not a.scales.is_contiguous() or \
-            a.scales.shape != (rows, -(-width // 128) * 4):
+    if scales.dtype is not torch.uint8 or not scales.is_contiguous() or scales.shape != (rows, -(-width // 128) * 4):
         raise ValueError(f"{name}.scales must be a contiguous CUDA uint8 tensor of shape {(rows, -(-width // 128) * 4)}")
-    on.check(name, a.codes)
-    on.check(name, a.scales)
-    return native.Act8(a.codes.data_ptr(), a.scales.data_ptr())
+    on.check(name, codes)
+    on.check(name, scales)
+    return native.Act8(codes.data_ptr(), scales.data_ptr())
 
 
 def _matrix(on: _On, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> int:
     """Checks one rows x width operand whose rows may lie apart.  Returns its row stride."""
-    if t.dtype is not dtype or not t.is_cuda:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    on.check(name, t)
+    if t.get_device() != on.index:
+        on.check(name, t)
     if t.shape != (rows, width):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
+    if t.is_contiguous():
+        return width
     row, inner = t.stride()
     if inner != 1 and width != 1:
         raise ValueError(f"the values of a row of {name} must be contiguous")
@@ -778,7 +778,10 @@ def act8_store(X, out: Optional[Act8] = None, *, stream=None) -> Act8:
     ld = _matrix(on, "X", X, rows, width, torch.bfloat16)
     if out is None:
         out = Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
-    st = native.lib().act8_store(X.data_ptr(), rows, width, ld, _act8_arg(on, "out", out, rows, width), on.handle)
+        arg = native.Act8(out.codes.data_ptr(), out.scales.data_ptr())
+    else:
+        arg = _act8_arg(on, "out", out, rows, width)
+    st = native.lib().act8_store(X.data_ptr(), rows, width, ld, arg, on.handle)
     if st:
         native.check("act8_store", st)
     return out
@@ -787,10 +790,12 @@ def act8_store(X, out: Optional[Act8] = None, *, stream=None) -> Act8:
 def act8_load(a: Act8, out=None, *, stream=None):
     """The bf16 values that a matrix in 8 bits stands for, exactly."""
     on = _On(a.codes, stream)
-    rows, width = a.shape
+    rows, width = a.codes.shape[0], a.width
+    ld = width
     if out is None:
         out = on.empty((rows, width), torch.bfloat16)
-    ld = _matrix(on, "out", out, rows, width, torch.bfloat16)
+    else:
+        ld = _matrix(on, "out", out, rows, width, torch.bfloat16)
     st = native.lib().act8_load(_act8_arg(on, "a", a, rows, width), rows, width, out.data_ptr(), ld, on.handle)
     if st:
         native.check("act8_load", st)
@@ -805,19 +810,24 @@ def act8_load(a: Act8, out=None, *, stream=None):
 _NORM = struct.Struct("10qqiiqiiqiiqiifffi")
 
 
+_NO_VECTOR = (0, 0, 0)
+
+
 def _vector(on: _On, name: str, t, n: int):
-    """Checks one optional vector of weights.  Returns (address, type, 0)."""
-    if t is None:
-        return 0, 0, 0
-    if t.dtype not in _DTYPES or not t.is_cuda or not t.is_contiguous() or t.shape != (n,):
+    """Checks one vector of weights.  Returns (address, type, 0)."""
+    dtype = t.dtype
+    if (dtype is not torch.bfloat16 and dtype is not torch.float32) or not t.is_contiguous() or t.shape != (n,):
         raise ValueError(f"{name} must be a contiguous CUDA bfloat16 or float32 vector of {n}")
-    on.check(name, t)
-    return t.data_ptr(), _DTYPES[t.dtype], 0
+    if t.get_device() != on.index:
+        on.check(name, t)
+    return t.data_ptr(), _DTYPES[dtype], 0
 
 
 def _norm(on, rows, width, strides, w, post_w, gate, row_gate, eps, w_offset, res_scale, stream_dtype):
-    packed = _NORM.pack(rows, width, *strides, *_vector(on, "w", w, width), *_vector(on, "post_w", post_w, width),
-                        *_vector(on, "gate", gate, width), *_vector(on, "row_gate", row_gate, rows), eps, w_offset, res_scale,
+    packed = _NORM.pack(rows, width, *strides, *(_NO_VECTOR if w is None else _vector(on, "w", w, width)),
+                        *(_NO_VECTOR if post_w is None else _vector(on, "post_w", post_w, width)),
+                        *(_NO_VECTOR if gate is None else _vector(on, "gate", gate, width)),
+                        *(_NO_VECTOR if row_gate is None else _vector(on, "row_gate", row_gate, rows)), eps, w_offset, res_scale,
                         _DTYPES[stream_dtype])
     return native.Norm.from_buffer_copy(packed)
 
@@ -834,7 +844,7 @@ def norm_fwd(h, w=None, *, y=None, post_w=None, gate=None, row_gate=None, res_sc
     if h.dim() != 2 or h.dtype not in _DTYPES:
         raise TypeError("h must be a CUDA bfloat16 or float32 matrix")
     rows, width = h.shape
-    h_ld = _matrix(on, "h", h, rows, width, h.dtype)
+    h_ld = width if h.is_contiguous() else _matrix(on, "h", h, rows, width, h.dtype)
     y_ld = h_out_ld = x_ld = 0
     if y is not None:
         y_ld = _matrix(on, "y", y, rows, width, torch.bfloat16)
@@ -850,8 +860,14 @@ def norm_fwd(h, w=None, *, y=None, post_w=None, gate=None, row_gate=None, res_sc
         x_ld = width
     norm = _norm(on, rows, width, (h_ld, y_ld, h_out_ld, x_ld, 0, 0, 0, 0), w, post_w, gate, row_gate, eps, w_offset, res_scale,
                  h.dtype)
-    st = native.lib().norm_fwd(norm, h.data_ptr(), _ptr(y), _ptr(h_out), _ptr(x), _act8_arg(on, "x8", x8, rows, width),
-                               _act8_arg(on, "h8", h8, rows, width), _act8_arg(on, "y8", y8, rows, width), on.handle)
+    if x8 is not None:
+        x8 = _act8_arg(on, "x8", x8, rows, width)
+    if h8 is not None:
+        h8 = _act8_arg(on, "h8", h8, rows, width)
+    if y8 is not None:
+        y8 = _act8_arg(on, "y8", y8, rows, width)
+    st = native.lib().norm_fwd(norm, h.data_ptr(), None if y is None else y.data_ptr(), None if h_out is None else h_out.data_ptr(),
+                               None if x is None else x.data_ptr(), x8, h8, y8, on.handle)
     if st:
         native.check("norm_fwd", st)
     return x, h if h_out is None else h_out
@@ -963,11 +979,11 @@ _NO_MAT = (0, 0)
 
 
 def _positions(on: _On, positions, rows: int) -> int:
-    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_cuda or not positions.is_contiguous() or \
-            positions.shape != (rows,):
+    dtype = positions.dtype
+    if (dtype is not torch.int64 and dtype is not torch.int32) or not positions.is_contiguous() or positions.shape != (rows,):
         raise ValueError(f"positions must be a contiguous CUDA int64 or int32 vector of {rows}")
     on.check("positions", positions)
-    return 64 if positions.dtype is torch.int64 else 32
+    return 64 if dtype is torch.int64 else 32
 
 
 def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
@@ -982,14 +998,16 @@ def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
         hq = Q.shape[1]
         q = _heads(on, "Q", Q, rows, hq, d)
         if Q_out is None:
-            Q_out = on.empty((rows, hq, d), torch.bfloat16)
-        qo = _heads(on, "Q_out", Q_out, rows, hq, d)
+            Q_out, qo = on.empty((rows, hq, d), torch.bfloat16), (hq * d, d)
+        else:
+            qo = _heads(on, "Q_out", Q_out, rows, hq, d)
     if K is not None:
         hk = K.shape[1]
         k = _heads(on, "K", K, rows, hk, d)
         if K_out is None:
-            K_out = on.empty((rows, hk, d), torch.bfloat16)
-        ko = _heads(on, "K_out", K_out, rows, hk, d)
+            K_out, ko = on.empty((rows, hk, d), torch.bfloat16), (hk * d, d)
+        else:
+            ko = _heads(on, "K_out", K_out, rows, hk, d)
     shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(rows, 0, hq, hk, d, bits, *q, *k, 0, 0, *qo, *ko, 0, 0))
     st = getattr(native.lib(), name)(_ptr(Q), _ptr(K), positions.data_ptr(), shape, rope.address, _ptr(Q_out), _ptr(K_out), on.handle)
     if st:
@@ -1021,10 +1039,12 @@ def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_ou
     bits = _positions(on, positions, rows)
     _check_rows(on, "slots", slots, rows, torch.int64)
     if Q_out is None:
-        Q_out = on.empty((rows, hq, d), torch.bfloat16)
+        Q_out, qo = on.empty((rows, hq, d), torch.bfloat16), (hq * d, d)
+    else:
+        qo = _heads(on, "Q_out", Q_out, rows, hq, d)
     shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(
         rows, cache_rows, hq, hk, d, bits, *_heads(on, "Q", Q, rows, hq, d), *_heads(on, "K", K, rows, hk, d),
-        *_heads(on, "V", V, rows, hk, d), *_heads(on, "Q_out", Q_out, rows, hq, d),
+        *_heads(on, "V", V, rows, hk, d), *qo,
         *_heads(on, "K_cache", K_cache, cache_rows, hk, d), *_heads(on, "V_cache", V_cache, cache_rows, hk, d)))
     st = native.lib().rope_append(Q.data_ptr(), K.data_ptr(), V.data_ptr(), positions.data_ptr(), slots.data_ptr(), shape,
                                   rope.address, Q_out.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), on.handle)
