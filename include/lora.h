@@ -458,8 +458,8 @@ lora_status lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_b
  * Every vector but w is optional (data NULL): post_w, w and gate have `width` values, row_gate `rows`.  y NULL: x only, from
  * h as it is (h_out NULL, too).  w NULL: h' only (x NULL).
  *  - h, h_out, dh, dh_out are the stream, bf16 or fp32 (stream_dtype); y, x, dx, dy are bf16.  Each has a row stride (in
- *    elements, >= width) and its element's alignment; rows that start on 16-byte boundaries and whole eights of values are
- *    read 16 bytes at a time.
+ *    elements, >= width) and its element's alignment.  Rows that start on 16 bytes and have whole eights of values are
+ *    fastest; others may be read from up to 15 bytes before their first value on, inside the same aligned 16 bytes.
  *  - Everything is fp32 until the outputs, x is formed from h' before its rounding.  A row's results depend on that row only.
  *    Rows of zeros give zeros.
  *  - h_out may be h, dh_out may be dh (same strides); nothing else overlaps.

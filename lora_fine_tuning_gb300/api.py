@@ -23,7 +23,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _check_bf16(name: str, t: torch.Tensor, shape) -> None:
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major)")

@@ -413,11 +413,12 @@ constexpr int kRingBudget = 216 * 1024;   // shared memory of an SM's rings
 struct RingPlan {
     int per_sm, stages;
 };
-RingPlan ring_plan(int cta_bytes, int most) {
+RingPlan ring_plan(int cta_bytes, int most, bool kept) {
+    if (!kept) return RingPlan{1, 1};   // wide rows are worked on one at a time
     for (int n = most; n > 1; --n)
         for (int stages = 4; stages >= 2; --stages)
             if (n * stages * cta_bytes <= kRingBudget) return RingPlan{n, stages};
-    return RingPlan{1, std::max(1, std::min(4, kRingBudget / cta_bytes))};
+    return RingPlan{1, std::max(2, std::min(4, kRingBudget / cta_bytes))};   // two of the largest, 8192 fp32 values, fit
 }
 
 // Bytes of a stage that a matrix takes: its units and, for ragged rows, 16 for each warp's last lane.

@@ -277,7 +277,7 @@ cudaError_t launch_norm_bwd_form(NormBwd& p, int sms, cudaStream_t stream) {
     return by_width(p.s.width, p.s.ragged, [&](auto t, auto v, auto r) {
         constexpr int T = decltype(t)::value, V = decltype(v)::value, R = rows_of(T);
         constexpr bool K = decltype(r)::value;
-        const int wide = stage_bytes_of(T, V, p.s.f32 ? 4 : 2, K), half = stage_bytes_of(T, V, 2, K), kept = T * V * 12;
+        const int wide = stage_bytes_of(T, V, p.s.f32 ? 4 : 2, K), half = stage_bytes_of(T, V, 2, K), codes = T * V * 12;
         uint32_t at = 0;
         const auto place = [&at](bool there, int bytes) {
             const uint32_t was = at;
@@ -285,11 +285,11 @@ cudaError_t launch_norm_bwd_form(NormBwd& p, int sms, cudaStream_t stream) {
             return was;
         };
         p.at_dx = place(p.dx, half);
-        p.at_h = place(p.h || p.h8.codes, p.h8.codes ? kept : wide);
+        p.at_h = place(p.h || p.h8.codes, p.h8.codes ? codes : wide);
         p.at_dh = place(true, wide);
-        p.at_y = place(p.y || p.y8.codes, p.y8.codes ? kept : half);
+        p.at_y = place(p.y || p.y8.codes, p.y8.codes ? codes : half);
         p.stage_bytes = at;
-        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(kSums ? kSumsThreads : kBwdThreads, T));
+        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(kSums ? kSumsThreads : kBwdThreads, T), kept<T, V>());
         p.stages = plan.stages;
         const int grid = std::min((p.s.rows + R - 1) / R, sms * plan.per_sm);
         p.groups = grid;

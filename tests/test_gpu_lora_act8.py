@@ -102,6 +102,10 @@ def test_refusals():
     for kept in (api.act8(256, 480), api.act8(255, 512)):
         with pytest.raises(ValueError):
             api.lora_bwd(dY, kept, W, A, B, S, 1.0, 0.0, 0)
+    with pytest.raises(TypeError):          # the forward's products need X itself, and so does DoRA's backward
+        api.lora_fwd(api.act8_store(X), W, A, B, 1.0, 0.0, 0)
+    with pytest.raises(TypeError):
+        api.dora_bwd(dY, api.act8_store(X), W, A, B, S, dY, None, None, 1.0, 0.0, 0)
     kept = api.act8_store(X)
     kept.scales = kept.scales[:, :8]
     with pytest.raises(ValueError):

@@ -212,7 +212,7 @@ def test_rows_apart_and_in_place(width, start, ld):
             assert bool((w[:, rest] == 7).all())
 
 
-@pytest.mark.parametrize("width", [128, 200, 97, 4096, 2050, 8192])
+@pytest.mark.parametrize("width", [128, 200, 97, 4096, 2050, 8192, 9000, 16381])
 @pytest.mark.parametrize("stream", [BF, F32])
 def test_what_is_kept_in_8_bits(width, stream):
     """The forward's codes are act8_store's, and the backward from codes is the backward from what they stand for."""
@@ -230,6 +230,13 @@ def test_what_is_kept_in_8_bits(width, stream):
     a = api.norm_bwd(dx, h8, dh=dh, y=y8, **after)
     b = api.norm_bwd(dx, api.act8_load(h8).to(stream), dh=dh, y=api.act8_load(y8), **after)
     assert all(torch.equal(p, q) for p, q in zip(a, b) if p is not None)
+    bad = st["h"].clone()       # a row of NaN, and one that becomes infinite, spoil their own values only: padding stays zero
+    bad[3], bad[4, 0] = float("nan"), float("inf")
+    api.norm_fwd(**{**st, "h": bad}, x8=x8, h8=h8)
+    x, h = api.norm_fwd(**{**st, "h": bad})
+    for kept, t in ((x8, x), (h8, h.bfloat16())):
+        want = api.act8_store(t)
+        assert torch.equal(kept.codes, want.codes) and torch.equal(kept.scales, want.scales)
     only = api.act8(rows, width)
     norm = {**st, "y": None, "post_w": None, "gate": None}
     api.norm_fwd(**norm, x8=only)

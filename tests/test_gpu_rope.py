@@ -169,6 +169,23 @@ def test_rows_into_a_cache(rows, hq, hkv, d, rot, inter, page):
     assert torch.equal(q, want_q) and torch.equal(kh, want_kc) and torch.equal(vh, want_vc)
 
 
+def test_rows_with_one_slot():
+    """Of two rows with one slot something of either is left there, and everything else is right."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    q, k, v = heads(40, 4, 64, g), heads(40, 2, 64, g), heads(40, 2, 64, g)
+    kc, vc = heads(60, 2, 64, g), heads(60, 2, 64, g)
+    slots = torch.arange(40, device="cuda") + 10
+    slots[30] = slots[5]
+    t, rope = torch.arange(40, device="cuda"), api.rope_table(64)
+    before = vc.clone()
+    out, want = api.rope_append(q, k, v, t, slots, kc, vc, rope), api.rope_fwd(q, k, t, rope)
+    rest = [i for i in range(40) if i not in (5, 30)]
+    assert torch.equal(out, want[0]) and torch.equal(kc[slots[rest]], want[1][rest]) and torch.equal(vc[slots[rest]], v[rest])
+    assert bool(((vc[15] == v[5]) | (vc[15] == v[30])).all()) and bool(((kc[15] == want[1][5]) | (kc[15] == want[1][30])).all())
+    untouched = [i for i in range(60) if i < 10 or i == 40 or i >= 50]
+    assert torch.equal(vc[untouched], before[untouched])
+
+
 def test_an_empty_cache_and_no_rows():
     g = torch.Generator(device="cuda").manual_seed(6)
     q, k = heads(3, 4, 64, g), heads(3, 2, 64, g)
