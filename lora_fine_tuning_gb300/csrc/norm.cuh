@@ -15,6 +15,10 @@
 // over a row (its squares, t h, q v) is added up together with the first sums of the next row.
 // Sums over a row are fp32, by pairs; the sum of squares is formed anew on values 2^-80 their size where it leaves fp32's range.
 // The CTAs' sums over rows are added by a second kernel in a fixed order.
+//
+// Measured, 16384 x 8192 in bf16 with norms before and after and gates: forward 170 us (6.3 TB/s), backward with all
+// gradients 276 us (5.8 TB/s; 499 with loads into registers and two barriers a row, 310 with the ring and two barriers).
+// 8192 x 4096 without them: 48 and 67 us.
 #pragma once
 
 #include "act8.cuh"
@@ -77,7 +81,7 @@ __device__ __forceinline__ void copies_wait(int left) {
 // One matrix that is read: where its rows are, and where a stage has a row's copies (both from thread t's first unit on).
 // kRagged: its rows need not start on 16 bytes or be whole units.  A row is then copied by the aligned 16 bytes that it lies in, its first ones
 // from before the row (inside the same 16); a warp's last lane also copies the 16 bytes after its unit, the other lanes get them
-// from their neighbour.  The forms without it have none of the arithmetic for that (1112 instead of 480 instructions a row of the backward).
+// from their neighbour.  The forms without it have none of the arithmetic for that (1112 instead of 750 instructions a row of 16 warps of the backward).
 // kCodes: it may be in 8 bits.
 template <int T, int V, bool kF32, bool kRagged, bool kCodes>
 struct Mat {
@@ -409,7 +413,8 @@ auto by_width(int width, bool ragged, F&& f) {
 
 constexpr int kRingBudget = 216 * 1024;   // shared memory of an SM's rings
 
-// CTAs of an SM and the stages of their rings (four at most), from the shared memory that a CTA's stage takes.
+// CTAs of an SM and the stages of their rings (four at most), from the shared memory that a CTA's stage takes.  A second CTA is worth more
+// than a third stage: 8192 x 4096 with an fp32 stream and all gradients 148 us with two CTAs of two stages, 205 with one of four.
 struct RingPlan {
     int per_sm, stages;
 };
