@@ -746,6 +746,9 @@ def act8(rows: int, width: int, *, stream=None) -> Act8:
     return Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
 
 
+_ACT8 = struct.Struct("PP")   # lora_act8; ctypes takes the bytes for its address
+
+
 def _act8_arg(on: _On, name: str, a: Act8, rows: int, width: int):
     """Checks one matrix in 8 bits.  Returns what the library takes for it."""
     codes, scales = a.codes, a.scales
@@ -755,7 +758,7 @@ def _act8_arg(on: _On, name: str, a: Act8, rows: int, width: int):
         raise ValueError(f"{name}.scales must be a contiguous CUDA uint8 tensor of shape {(rows, -(-width // 128) * 4)}")
     on.check(name, codes)
     on.check(name, scales)
-    return native.Act8(codes.data_ptr(), scales.data_ptr())
+    return _ACT8.pack(codes.data_ptr(), scales.data_ptr())
 
 
 def _matrix(on: _On, name: str, t: torch.Tensor, rows: int, width: int, dtype) -> int:
@@ -784,7 +787,7 @@ def act8_store(X, out: Optional[Act8] = None, *, stream=None) -> Act8:
     ld = _matrix(on, "X", X, rows, width, torch.bfloat16)
     if out is None:
         out = Act8(on.empty((rows, -(-width // 32) * 32), torch.int8), on.empty((rows, -(-width // 128) * 4), torch.uint8), width)
-        arg = native.Act8(out.codes.data_ptr(), out.scales.data_ptr())
+        arg = _ACT8.pack(out.codes.data_ptr(), out.scales.data_ptr())
     else:
         arg = _act8_arg(on, "out", out, rows, width)
     st = native.lib().act8_store(X.data_ptr(), rows, width, ld, arg, on.handle)
@@ -812,7 +815,7 @@ def act8_load(a: Act8, out=None, *, stream=None):
 # norms around a block
 # ---------------------------------------------------------------------------------------------------------------
 
-# lora_norm in one go
+# lora_norm in one go; ctypes takes the bytes for its address
 _NORM = struct.Struct("10qqiiqiiqiiqiifffi")
 
 
@@ -830,12 +833,11 @@ def _vector(on: _On, name: str, t, n: int):
 
 
 def _norm(on, rows, width, strides, w, post_w, gate, row_gate, eps, w_offset, res_scale, stream_dtype):
-    packed = _NORM.pack(rows, width, *strides, *(_NO_VECTOR if w is None else _vector(on, "w", w, width)),
-                        *(_NO_VECTOR if post_w is None else _vector(on, "post_w", post_w, width)),
-                        *(_NO_VECTOR if gate is None else _vector(on, "gate", gate, width)),
-                        *(_NO_VECTOR if row_gate is None else _vector(on, "row_gate", row_gate, rows)), eps, w_offset, res_scale,
-                        _DTYPES[stream_dtype])
-    return native.Norm.from_buffer_copy(packed)
+    return _NORM.pack(rows, width, *strides, *(_NO_VECTOR if w is None else _vector(on, "w", w, width)),
+                      *(_NO_VECTOR if post_w is None else _vector(on, "post_w", post_w, width)),
+                      *(_NO_VECTOR if gate is None else _vector(on, "gate", gate, width)),
+                      *(_NO_VECTOR if row_gate is None else _vector(on, "row_gate", row_gate, rows)), eps, w_offset, res_scale,
+                      _DTYPES[stream_dtype])
 
 
 def norm_fwd(h, w=None, *, y=None, post_w=None, gate=None, row_gate=None, res_scale: float = 1.0, eps: float = 1e-6,
@@ -932,13 +934,26 @@ def norm_bwd(dx, h, w=None, *, dh=None, y=None, post_w=None, gate=None, row_gate
     norm = _norm(on, rows, width, (h_ld, y_ld, 0, 0, dx_ld, dh_ld, dh_out_ld, dy_ld), w, post_w, gate, row_gate, eps, w_offset,
                  res_scale, stream_dtype)
 
-    def grad(name, given, param, n):
-        if given is not None:
-            return _given_f32(on, name, given, n)
-        return on.empty((n,), torch.float32) if want_weights and param is not None else None
-
-    dw, dpost_w, dgate = grad("dw", dw, w, width), grad("dpost_w", dpost_w, post_w, width), grad("dgate", dgate, gate, width)
-    drow_gate = grad("drow_gate", drow_gate, row_gate, rows)
+    if dw is not None:
+        _given_f32(on, "dw", dw, width)
+    if dpost_w is not None:
+        _given_f32(on, "dpost_w", dpost_w, width)
+    if dgate is not None:
+        _given_f32(on, "dgate", dgate, width)
+    if drow_gate is not None:
+        _given_f32(on, "drow_gate", drow_gate, rows)
+    if want_weights:
+        new = (w is not None and dw is None) + (post_w is not None and dpost_w is None) + (gate is not None and dgate is None)
+        if new:   # in one piece of memory
+            pieces = iter((on.empty((width,), torch.float32),) if new == 1 else on.empty((new, width), torch.float32).unbind(0))
+            if w is not None and dw is None:
+                dw = next(pieces)
+            if post_w is not None and dpost_w is None:
+                dpost_w = next(pieces)
+            if gate is not None and dgate is None:
+                dgate = next(pieces)
+        if row_gate is not None and drow_gate is None:
+            drow_gate = on.empty((rows,), torch.float32)
     size = 0
     if ws is not None:
         size = on.given(ws).numel()
@@ -1005,10 +1020,11 @@ def _positions(on: _On, positions, rows: int) -> int:
 
 
 def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
-    on = _On(Q if Q is not None else K, stream)
-    if any(t is not None and t.dim() != 3 for t in (Q, K)):
+    ref = Q if Q is not None else K
+    on = _On(ref, stream)
+    if ref.dim() != 3:
         raise ValueError("Q and K are rows x heads x head_dim")
-    rows, _, d = (Q if Q is not None else K).shape
+    rows, _, d = ref.shape
     bits = _positions(on, positions, rows)
     hq = hk = 0
     q = qo = k = ko = _NO_MAT
@@ -1026,7 +1042,7 @@ def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
             K_out, ko = on.empty((rows, hk, d), torch.bfloat16), (hk * d, d)
         else:
             ko = _turned(on, "K_out", K_out, rows, hk, d)
-    shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(rows, 0, hq, hk, d, bits, *q, *k, 0, 0, *qo, *ko, 0, 0))
+    shape = _ROPE_SHAPE.pack(rows, 0, hq, hk, d, bits, *q, *k, 0, 0, *qo, *ko, 0, 0)
     st = getattr(native.lib(), name)(_ptr(Q), _ptr(K), positions.data_ptr(), shape, rope.address, _ptr(Q_out), _ptr(K_out), on.handle)
     if st:
         native.check(name, st)
@@ -1050,7 +1066,7 @@ def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_ou
     V_cache (cache rows x kv_heads x head_dim, what attn_fwd reads; pages are runs of such rows).  A row whose slot is outside
     the cache, -1 for example, is not stored; slots inside it must differ.  Returns the turned Q."""
     on = _On(Q, stream)
-    if any(t.dim() != 3 for t in (Q, K, V, K_cache, V_cache)):
+    if Q.dim() != 3 or K.dim() != 3:
         raise ValueError("Q, K, V and the caches are rows x heads x head_dim")
     rows, hq, d = Q.shape
     hk, cache_rows = K.shape[1], K_cache.shape[0]
@@ -1060,10 +1076,10 @@ def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_ou
         Q_out, qo = on.empty((rows, hq, d), torch.bfloat16), (hq * d, d)
     else:
         qo = _turned(on, "Q_out", Q_out, rows, hq, d)
-    shape = native.RopeShape.from_buffer_copy(_ROPE_SHAPE.pack(
+    shape = _ROPE_SHAPE.pack(
         rows, cache_rows, hq, hk, d, bits, *_turned(on, "Q", Q, rows, hq, d), *_turned(on, "K", K, rows, hk, d),
         *_turned(on, "V", V, rows, hk, d), *qo,
-        *_turned(on, "K_cache", K_cache, cache_rows, hk, d), *_turned(on, "V_cache", V_cache, cache_rows, hk, d)))
+        *_turned(on, "K_cache", K_cache, cache_rows, hk, d), *_turned(on, "V_cache", V_cache, cache_rows, hk, d))
     st = native.lib().rope_append(Q.data_ptr(), K.data_ptr(), V.data_ptr(), positions.data_ptr(), slots.data_ptr(), shape,
                                   rope.address, Q_out.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), on.handle)
     if st:

@@ -403,6 +403,7 @@ auto by_width(int width, bool ragged, F&& f) {
         if (width <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), Yes());
         return f(integral_constant<int, 512>(), integral_constant<int, 4>(), Yes());
     }
+    if (width <= 256) return f(integral_constant<int, 32>(), integral_constant<int, 1>(), No());
     if (width <= 512) return f(integral_constant<int, 32>(), integral_constant<int, 2>(), No());
     if (width <= 1024) return f(integral_constant<int, 64>(), integral_constant<int, 2>(), No());
     if (width <= 2048) return f(integral_constant<int, 128>(), integral_constant<int, 2>(), No());
@@ -436,7 +437,7 @@ cudaError_t configure(F&& kernels) {
     const auto set = [&e](auto* k) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBudget);
     };
-    for (const int width : {512, 1024, 2048, 4096, 8192, kNormMaxWidth})
+    for (const int width : {256, 512, 1024, 2048, 4096, 8192, kNormMaxWidth})
         for (const bool ragged : {false, true})
             by_width(width, ragged, [&](auto t, auto v, auto r) {
                 kernels(t, v, r, set);

@@ -138,7 +138,6 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, u64, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64,
                                            ctypes.c_float, ctypes.c_double, ctypes.c_size_t)
-        a8 = ctypes.POINTER(Act8)
         sig = {
             "lora_workspace_size": (sz, [i64, i64, i64, i32, i32]),
             "lora_set_deterministic": (i32, [i32]),
@@ -163,18 +162,18 @@ def lib() -> ctypes.CDLL:
             "pref_loss": (i32, [ctypes.POINTER(Logits), vp, i32, vp, f32, f32, f32, vp, vp, vp, sz, vp]),
             "policy_loss": (i32, [ctypes.POINTER(Logits), vp, vp, vp, f32, f32, f32, f32, vp, vp, sz, vp]),
             "adamw_step": (i32, [vp, i32, f64, f64, f64, f64, f64, i64, vp, vp]),
-            "act8_store": (i32, [vp, i64, i64, i64, a8, vp]),
-            "act8_load": (i32, [a8, i64, i64, vp, i64, vp]),
-            "multi_lora_bwd_act8": (i32, [vp, a8, vp, ctypes.POINTER(LoraAdapter), i32, ctypes.POINTER(LoraSegment), i32,
+            "act8_store": (i32, [vp, i64, i64, i64, vp, vp]),
+            "act8_load": (i32, [vp, i64, i64, vp, i64, vp]),
+            "multi_lora_bwd_act8": (i32, [vp, vp, vp, ctypes.POINTER(LoraAdapter), i32, ctypes.POINTER(LoraSegment), i32,
                                           u64, i64, i64, i64, vp, vp, vp, vp, sz, vp]),
-            "lora_bwd_act8": (i32, [vp, a8, vp, vp, vp, vp, vp, f32, f32, u64, i64, i64, i64, i32, vp, vp, vp, vp, sz, vp]),
+            "lora_bwd_act8": (i32, [vp, vp, vp, vp, vp, vp, vp, f32, f32, u64, i64, i64, i64, i32, vp, vp, vp, vp, sz, vp]),
             "norm_workspace_size": (sz, [i64, i64]),
-            "norm_fwd": (i32, [ctypes.POINTER(Norm), vp, vp, vp, vp, a8, a8, a8, vp]),
-            "norm_bwd": (i32, [ctypes.POINTER(Norm), vp, vp, vp, a8, vp, a8, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "norm_fwd": (i32, [vp] * 9),
+            "norm_bwd": (i32, [vp] * 14 + [sz, vp]),
             "rope_table": (i32, [i32, f64, i32, vp, vp]),
-            "rope_fwd": (i32, [vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp]),
-            "rope_bwd": (i32, [vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp]),
-            "rope_append": (i32, [vp, vp, vp, vp, vp, ctypes.POINTER(RopeShape), vp, vp, vp, vp, vp]),
+            "rope_fwd": (i32, [vp] * 8),
+            "rope_bwd": (i32, [vp] * 8),
+            "rope_append": (i32, [vp] * 11),
             "lora_tile_table": (i32, [ctypes.POINTER(LoraSegment), i32, i32, i64, ctypes.POINTER(ctypes.c_int32),
                                       i64]),
             "lora_keep_threshold": (i32, [f32, ctypes.POINTER(ctypes.c_uint32)]),

@@ -3,6 +3,8 @@
 Every step but the rounding to a whole number is exact (the scale is a power of two), so nothing here has a tolerance but
 the format's own: half a scale, 2^-7 of the block's largest value.
 """
+import ctypes
+
 import pytest
 
 from tests.gpu_helpers import torch
@@ -164,4 +166,4 @@ def test_refusals():
     with pytest.raises(ValueError):
         api.act8_load(api.Act8(kept.codes[:, :32], kept.scales, 32))
     with pytest.raises(native.LoraError):
-        native.check("act8_store", native.lib().act8_store(x.data_ptr(), 4, 40, 39, native.Act8(256, 256), None))
+        native.check("act8_store", native.lib().act8_store(x.data_ptr(), 4, 40, 39, ctypes.byref(native.Act8(256, 256)), None))

@@ -22,7 +22,7 @@ NAN, INF = float("nan"), float("inf")
 
 
 def kept(codes=256, scales=256):
-    return native.Act8(codes, scales)
+    return ctypes.byref(native.Act8(codes, scales))
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -40,7 +40,7 @@ def norm(rows=10, width=96, w=(256, 0), post=(None, 0), gate=(None, 0), row_gate
     n = native.Norm(rows, width, *(ld.get(x, 96) for x in ("h", "y", "h_out", "x", "dx", "dh", "dh_out", "dy")))
     n.w, n.post_w, n.gate, n.row_gate = (native.Vector(p, t, 0) for p, t in (w, post, gate, row_gate))
     n.eps, n.w_offset, n.res_scale, n.stream_dtype = eps, offset, res, stream
-    return n
+    return ctypes.byref(n)
 
 
 def fwd(lib, n, h=256, y=512, h_out=1024, x=2048, x8=None, h8=None, y8=None):
@@ -145,7 +145,7 @@ def rope_shape(rows=10, cache=100, hq=8, hk=2, d=64, bits=64, **s):
     for f in ("q", "k", "v", "q_out", "k_out", "v_out"):
         m = getattr(g, f)
         m.row, m.head = s.get(f, ((hq if f.startswith("q") else hk) * d, d))
-    return g
+    return ctypes.byref(g)
 
 
 def turn(lib, g, r, q=256, k=512, pos=256, qo=1024, ko=2048):
@@ -178,7 +178,6 @@ def test_rope_pointers(lib):
                      (dict(vc=768), 1), (dict(vc=2048), 1)):
         assert append(lib, g, r, **kw) == code, kw
     assert append(lib, rope_shape(hk=0), r) == 3 and append(lib, rope_shape(cache=-1), r) == 3
-    bad = table()[1]
     for name, value in (("rot_dim", 0), ("rot_dim", 7), ("rot_dim", 66)):
         bad = table()[1]
         setattr(bad, name, value)
