@@ -337,12 +337,12 @@ struct RowSums {
             turn ^= 1;
             if ((lane & 7) == 0) to[(lane >> 3) * kWarps + threadIdx.x % T / 32] = x;
             wait();
-            constexpr int kLanes = kWarps < 8 ? kWarps : 8;
-            x = to[(lane >> 3) * kWarps + (lane & (kLanes - 1))];
+            x = 0.f;
 #pragma unroll
-            for (int i = kLanes; i < kWarps; i += kLanes) x += to[(lane >> 3) * kWarps + (lane & (kLanes - 1)) + i];
+            for (int i = 0; i < kWarps; i += 8)
+                if (i + 8 <= kWarps || (lane & 7) + i < kWarps) x += to[(lane >> 3) * kWarps + (lane & 7) + i];
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+            for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(0xFFFFFFFFu, x, 8 * k);
@@ -399,6 +399,7 @@ auto by_width(int width, bool ragged, F&& f) {
     using No = std::false_type;
     if (ragged) {
         if (width <= 512) return f(integral_constant<int, 32>(), integral_constant<int, 2>(), Yes());
+        if (width <= 2560) return f(integral_constant<int, 160>(), integral_constant<int, 2>(), Yes());
         if (width <= 4096) return f(integral_constant<int, 256>(), integral_constant<int, 2>(), Yes());
         if (width <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), Yes());
         return f(integral_constant<int, 512>(), integral_constant<int, 4>(), Yes());
@@ -407,6 +408,7 @@ auto by_width(int width, bool ragged, F&& f) {
     if (width <= 512) return f(integral_constant<int, 32>(), integral_constant<int, 2>(), No());
     if (width <= 1024) return f(integral_constant<int, 64>(), integral_constant<int, 2>(), No());
     if (width <= 2048) return f(integral_constant<int, 128>(), integral_constant<int, 2>(), No());
+    if (width <= 2560) return f(integral_constant<int, 160>(), integral_constant<int, 2>(), No());
     if (width <= 4096) return f(integral_constant<int, 256>(), integral_constant<int, 2>(), No());
     if (width <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), No());
     return f(integral_constant<int, 512>(), integral_constant<int, 4>(), No());
@@ -437,7 +439,7 @@ cudaError_t configure(F&& kernels) {
     const auto set = [&e](auto* k) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBudget);
     };
-    for (const int width : {256, 512, 1024, 2048, 4096, 8192, kNormMaxWidth})
+    for (const int width : {256, 512, 1024, 2048, 2560, 4096, 8192, kNormMaxWidth})
         for (const bool ragged : {false, true})
             by_width(width, ragged, [&](auto t, auto v, auto r) {
                 kernels(t, v, r, set);
