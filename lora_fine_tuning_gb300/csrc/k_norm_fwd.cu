@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
             if (s.post.p) {
                 float r = inverse_rms(squares, s);
                 if (too_large(squares)) {
-                    const RowAt<false> at{reinterpret_cast<const uint8_t*>(p.y) + row * p.y_ld, nullptr};
+                    const RowAt<false> at{reinterpret_cast<const uint8_t*>(p.y) + static_cast<uint64_t>(p.y_ld) * static_cast<uint32_t>(row), nullptr};
                     float q[4] = {small_sums(at, nullptr, s.w, 0.f, t, T, s.width).x, 0.f, 0.f, 0.f};
                     sums.add(q);
                     r = inverse_rms_small(q[0], s) * kSmall;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
                 for (int k = 0; k < 4; ++k) h[i][k] = fma2(mul(y[k], both(c)), kKept ? fc[kKept ? i : 0][k] : f[k], h[i][k]);
                 Unit<kF32> out;
                 out.put(h[i]);
-                store_unit<T, kF32, kRagged>(out, static_cast<uint8_t*>(p.h_out) + row * p.h_out_ld, i, t, s.width);
+                store_unit<T, kF32, kRagged>(out, static_cast<uint8_t*>(p.h_out) + static_cast<uint64_t>(p.h_out_ld) * static_cast<uint32_t>(row), i, t, s.width);
             }
             if (p.h8.codes) {
                 Unit<false> u;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
             for (int k = 0; k < 4; ++k) f[k] = mul(mul(h[i][k], both(r)), kKept ? fw[kKept ? i : 0][k] : f[k]);
             Unit<false> x;
             x.put(f);
-            if (p.x) store_unit<T, false, kRagged>(x, reinterpret_cast<uint8_t*>(p.x) + row * p.x_ld, i, t, s.width);
+            if (p.x) store_unit<T, false, kRagged>(x, reinterpret_cast<uint8_t*>(p.x) + static_cast<uint64_t>(p.x_ld) * static_cast<uint32_t>(row), i, t, s.width);
             if (p.x8.codes) store_act8<T>(x, p.x8, s, row, i, t);
         }
     };

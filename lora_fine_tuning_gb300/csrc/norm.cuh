@@ -110,12 +110,12 @@ struct Mat {
             p += t * 8 * kSize;
         }
     }
-    __device__ __forceinline__ void fetch(uint8_t* to_stage, int64_t row, int t, int width) const {
+    __device__ __forceinline__ void fetch(uint8_t* to_stage, uint32_t row, int t, int width) const {
         if (!p) return;
         const uint32_t stage = smem_u32(to_stage) + at;
-        const uint8_t* x = p + row * ld;
+        const uint8_t* x = p + static_cast<uint64_t>(ld) * row;
         if (kCodes && scales) {
-            const uint8_t* y = scales + row * scales_ld;
+            const uint8_t* y = scales + static_cast<uint64_t>(scales_ld) * row;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (left > i * T * 8) {
@@ -165,7 +165,7 @@ struct Mat {
         }
     }
     // All lanes of a warp take part.
-    __device__ __forceinline__ void read(F2 (&v)[4], const uint8_t* stage, int64_t row, int i, int t) const {
+    __device__ __forceinline__ void read(F2 (&v)[4], const uint8_t* stage, uint32_t row, int i, int t) const {
         stage += at;
         if (kCodes && scales) {
             const uint2 c = *reinterpret_cast<const uint2*>(stage + i * T * 8);
@@ -184,7 +184,7 @@ struct Mat {
         uint4 a = *reinterpret_cast<const uint4*>(stage + (kF32 ? 2 * i : i) * T * 16);
         uint4 b = kF32 ? *reinterpret_cast<const uint4*>(stage + (2 * i + 1) * T * 16) : a;
         if (kRagged) {
-            const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p + row * ld)) & 15u;
+            const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p + static_cast<uint64_t>(ld) * row)) & 15u;
             if (shift) {
                 uint4 next = shuffle_down(a);
                 if ((t & 31) == 31) next = *reinterpret_cast<const uint4*>(stage - t * 16 + kMore + (i * (T / 32) + t / 32) * 16);
@@ -291,9 +291,9 @@ __device__ __forceinline__ void block_factors(F2 (&f)[4], const NormShape& s, in
 
 // A row's values in 8 bits.  Whole warps take part; the row's padding up to whole blocks is zero, its scale one.
 template <int T>
-__device__ __forceinline__ void store_act8(Unit<false> u, const NormAct8& a, const NormShape& s, int64_t row, int i, int t) {
-    uint8_t* codes = a.codes + row * s.codes_ld;
-    uint8_t* scales = a.scales + row * s.scales_ld;
+__device__ __forceinline__ void store_act8(Unit<false> u, const NormAct8& a, const NormShape& s, uint32_t row, int i, int t) {
+    uint8_t* codes = a.codes + static_cast<uint64_t>(s.codes_ld) * row;
+    uint8_t* scales = a.scales + static_cast<uint64_t>(s.scales_ld) * row;
     const int c = (i * T + t) * 8;
     if (c + 8 > s.width) {   // a row of NaN leaves its padding zero, too
 #pragma unroll

@@ -102,17 +102,17 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             float f[4] = {0.f, 0.f, 0.f, 0.f};
             if (s.w.p) {
                 const bool codes = kCodes && p.h8.codes;
-                const RowAt<kF32> at{codes ? p.h8.codes + row * s.codes_ld : static_cast<const uint8_t*>(p.h) + row * p.h_ld,
-                                     codes ? p.h8.scales + row * s.scales_ld : nullptr};
-                const uint16_t* dx = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(p.dx) + row * p.dx_ld);
+                const RowAt<kF32> at{codes ? p.h8.codes + static_cast<uint64_t>(s.codes_ld) * static_cast<uint32_t>(row) : static_cast<const uint8_t*>(p.h) + static_cast<uint64_t>(p.h_ld) * static_cast<uint32_t>(row),
+                                     codes ? p.h8.scales + static_cast<uint64_t>(s.scales_ld) * static_cast<uint32_t>(row) : nullptr};
+                const uint16_t* dx = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(p.dx) + static_cast<uint64_t>(p.dx_ld) * static_cast<uint32_t>(row));
                 const float2 a = small_sums(at, dx, s.w, s.offset, t, T, s.width);
                 f[1] = a.x;
                 f[2] = a.y;
             }
             if (s.post.p) {
                 const bool codes = kCodes && p.y8.codes;
-                const RowAt<false> at{codes ? p.y8.codes + row * s.codes_ld : reinterpret_cast<const uint8_t*>(p.y) + row * p.y_ld,
-                                      codes ? p.y8.scales + row * s.scales_ld : nullptr};
+                const RowAt<false> at{codes ? p.y8.codes + static_cast<uint64_t>(s.codes_ld) * static_cast<uint32_t>(row) : reinterpret_cast<const uint8_t*>(p.y) + static_cast<uint64_t>(p.y_ld) * static_cast<uint32_t>(row),
+                                      codes ? p.y8.scales + static_cast<uint64_t>(s.scales_ld) * static_cast<uint32_t>(row) : nullptr};
                 f[3] = small_sums(at, nullptr, s.w, 0.f, t, T, s.width).x;
             }
             sums.add(f);
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             }
             Unit<kF32> out;
             out.put(d[i]);
-            store_unit<T, kF32, kRagged>(out, static_cast<uint8_t*>(p.dh_out) + row * p.dh_out_ld, i, t, s.width);
+            store_unit<T, kF32, kRagged>(out, static_cast<uint8_t*>(p.dh_out) + static_cast<uint64_t>(p.dh_out_ld) * static_cast<uint32_t>(row), i, t, s.width);
             if (!has_y) continue;
             F2 y[4], f[4];
             Y.read(y, stage, row, i, t);
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             }
             Unit<false> out;
             out.put(f);
-            store_unit<T, false, kRagged>(out, reinterpret_cast<uint8_t*>(p.dy) + row * p.dy_ld, i, t, s.width);
+            store_unit<T, false, kRagged>(out, reinterpret_cast<uint8_t*>(p.dy) + static_cast<uint64_t>(p.dy_ld) * static_cast<uint32_t>(row), i, t, s.width);
         }
     };
     const bool second = s.post.p || p.drow;   // the sum of z v is needed
