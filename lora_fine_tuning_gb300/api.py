@@ -736,9 +736,6 @@ class Act8:
     def device(self):
         return self.codes.device
 
-    def get_device(self) -> int:
-        return self.codes.get_device()
-
 
 def act8(rows: int, width: int, *, stream=None) -> Act8:
     """Room for a rows x width matrix in 8 bits, on the current device."""

@@ -90,13 +90,6 @@ __device__ __forceinline__ uint2 act8_encode8(uint4 x, uint32_t& exponent) {
     return out;
 }
 
-// One bf16 value (its 16 bits) of each lane -> its code; the whole warp is one block.
-__device__ __forceinline__ uint32_t act8_encode1(uint32_t x16, uint32_t& exponent) {
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, finite_bits(x16));
-    exponent = act8_exponent(top);
-    return (x16 & 0x7F80u) == 0x7F80u ? 0x80u : act8_code(x16 << 16, act8_inverse(exponent)) & 0xFFu;
-}
-
 // Four codes -> four values, exact.  `scale` is the block's.
 __device__ __forceinline__ void act8_decode4(uint32_t codes, float scale, float (&v)[4]) {
     const uint32_t u = codes ^ 0x80808080u;   // code + 128

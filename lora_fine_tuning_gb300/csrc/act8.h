@@ -14,7 +14,7 @@ struct Act8Params {
     uint16_t* x;           // rows x width, row stride ld elements (store: read only)
     uint8_t *codes, *scales;
     int64_t ld;
-    int32_t rows, width;
+    int32_t width;
     uint32_t per_row;      // units of eight codes in a row of codes
     uint32_t units;        // rows * per_row
     int32_t vector;        // whole units of x are 16-byte aligned

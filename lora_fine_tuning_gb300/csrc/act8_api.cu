@@ -14,7 +14,7 @@ lora_status check(const void* x, int64_t rows, int64_t width, int64_t ld, const 
     if (rows > 0 && (!x || !a->codes || !a->scales)) return LORA_EINVAL;
     if (reinterpret_cast<uintptr_t>(x) % 2 || !aligned16(a->codes) || reinterpret_cast<uintptr_t>(a->scales) % 4) return LORA_EALIGN;
     p = Act8Params{const_cast<uint16_t*>(static_cast<const uint16_t*>(x)), reinterpret_cast<uint8_t*>(a->codes), a->scales,
-                   ld, static_cast<int32_t>(rows), static_cast<int32_t>(width), static_cast<uint32_t>(per_row),
+                   ld, static_cast<int32_t>(width), static_cast<uint32_t>(per_row),
                    static_cast<uint32_t>(rows * per_row), aligned16(x) && ld % 8 == 0, 0, 0};
     // 2^shift < per_row <= 2^(shift + 1): magic = ceil(2^(32 + shift) / per_row) is below 2^32 and exceeds that quotient by less than one,
     // so u magic exceeds u 2^(32 + shift) / per_row by less than 2^31, and the quotient's fraction is at most 1 - 1 / per_row

@@ -81,7 +81,7 @@ __device__ __forceinline__ void copies_wait(int left) {
 // One matrix that is read: where its rows are, and where a stage has a row's copies (both from thread t's first unit on).
 // kRagged: its rows need not start on 16 bytes or be whole units.  A row is then copied by the aligned 16 bytes that it lies in, its first ones
 // from before the row (inside the same 16); a warp's last lane also copies the 16 bytes after its unit, the other lanes get them
-// from their neighbour.  The forms without it have none of the arithmetic for that (1112 instead of 750 instructions a row of 16 warps of the backward).
+// from their neighbour.  The forms without it have none of the arithmetic for that (1112 instead of 715 instructions a row and warp of the backward).
 // kCodes: it may be in 8 bits.
 template <int T, int V, bool kF32, bool kRagged, bool kCodes>
 struct Mat {

@@ -15,7 +15,7 @@ constexpr int kMaxSms = 160;   // workspaces are sized without a device; a launc
 bool aligned(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // One matrix of the call: `p` may be null where it is not `needed`.
-struct Checker {
+struct Arguments {
     int64_t rows, width;
     lora_status st = LORA_OK;
     bool vectors = true, ragged = false;
@@ -46,7 +46,7 @@ struct Checker {
     }
 };
 
-lora_status check_shape(const lora_norm* n, Checker& c, NormShape& s) {
+lora_status check_shape(const lora_norm* n, Arguments& c, NormShape& s) {
     if (!n) return LORA_EINVAL;
     if (n->rows < 0 || n->rows > LORA_MAX_ROWS || n->width < 1 || n->width > LORA_MAX_NORM_WIDTH) return LORA_ESHAPE;
     if (n->stream_dtype != LORA_BF16 && n->stream_dtype != LORA_F32) return LORA_EINVAL;
@@ -89,7 +89,7 @@ lora_status norm_fwd(const lora_norm* norm, const void* h, const lora_bf16* y, v
                      const lora_act8* x8, const lora_act8* h8, const lora_act8* y8, void* stream) {
     NormFwd p;
     std::memset(&p, 0, sizeof(p));
-    Checker c{};
+    Arguments c{};
     lora_status st = check_shape(norm, c, p.s);
     if (st) return st;
     const int size = p.s.f32 ? 4 : 2;
@@ -125,7 +125,7 @@ lora_status norm_bwd(const lora_norm* norm, const lora_bf16* dx, const void* dh,
                      float* dgate, float* drow_gate, void* workspace, size_t workspace_bytes, void* stream) {
     NormBwd p;
     std::memset(&p, 0, sizeof(p));
-    Checker c{};
+    Arguments c{};
     lora_status st = check_shape(norm, c, p.s);
     if (st) return st;
     const int size = p.s.f32 ? 4 : 2;

@@ -322,6 +322,32 @@ def test_two_graphs_and_calls_between():
             assert all(torch.equal(a, b) for a, b in zip(want[i], outs[i]))
 
 
+def test_two_threads_on_one_stream():
+    """The launches of two threads' calls may interleave on the stream: each thread's calls have a workspace of their own."""
+    import threading
+    calls = []
+    for seed, rows in ((0, 900), (1, 700)):
+        st, dx, dh = inputs(rows, 768, post=True, gate=True, seed=seed)
+        h = api.norm_fwd(**st)[1]
+        calls.append(lambda dx=dx, h=h, dh=dh, rest={k: t for k, t in st.items() if k != "h"}: api.norm_bwd(dx, h, dh=dh, **rest))
+    want, wrong = [f() for f in calls], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(200):
+            got = calls[i]()
+            torch.cuda.current_stream().synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i]) if b is not None):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_no_rows():
     st, dx, dh = inputs(0, 256, post=True, gate=True, row_gate=True)
     x, h = api.norm_fwd(**st)
