@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) act8_load_kernel(const Act8Params p)
         const bool first = lane == 0 || at[i] == 0, last = lane == 31 || at[i] + 1 == p.per_row;
         uint8_t* to = reinterpret_cast<uint8_t*>(p.x + row[i] * p.ld);
         const int from = static_cast<int>(at[i]) * 16, left = p.width * 2 - from;
-        if (!kVec) store16<2>(to, from, p.width * 2, x, before, first, last);
+        if (!kVec) store16<2, false>(to, from, p.width * 2, x, before, first, last);
         else if (left >= 16) __stcs(reinterpret_cast<uint4*>(to + from), x);
         else if (left > 0) store_parts<2>(to + from, x, 0, left / 2);
     }

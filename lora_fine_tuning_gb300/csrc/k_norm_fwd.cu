@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
             for (int i = 0; i < V; ++i) {
                 if (kRagged && i >= mine) break;
                 F2 y[4];
-                Y.read(y, stage, row, i, t);
+                Y.template read<kKeep>(y, stage, row, i, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) q = fma2(y[k], y[k], q);
             }
@@ -80,10 +80,11 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_f
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (kRagged && i >= mine) break;
-            H.read(h[i], stage, row, i, t);
+            H.template read<kOnce>(h[i], stage, row, i, t);
             if (p.y) {
                 F2 y[4], f[4];
-                Y.read(y, stage, row, i, t);
+                if (kRagged && !s.post.p) Y.template read<kOnce>(y, stage, row, i, t);
+                else Y.template read<kPlain>(y, stage, row, i, t);
                 if (!kKept) block_factors<T>(f, s, i, t);
                 if (p.y8.codes) {
                     Unit<false> u;

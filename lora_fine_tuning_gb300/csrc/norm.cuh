@@ -78,6 +78,9 @@ __device__ __forceinline__ void copies_wait(int left) {
     else asm volatile("cp.async.wait_group 2;" ::: "memory");
 }
 
+// How a row's unit is taken from its stage: once, first of several times, or again.
+enum Take { kOnce, kKeep, kPlain };
+
 // One matrix that is read: where its rows are, and where a stage has a row's copies (both from thread t's first unit on).
 // kRagged: its rows need not start on 16 bytes or be whole units.  A row is then copied by the aligned 16 bytes that it lies in, its first ones
 // from before the row (inside the same 16); a warp's last lane also copies the 16 bytes after its unit, the other lanes get them
@@ -165,7 +168,9 @@ struct Mat {
         }
     }
     // All lanes of a warp take part.
-    __device__ __forceinline__ void read(F2 (&v)[4], const uint8_t* stage, uint32_t row, int i, int t) const {
+    // kKeep: a later read of the row may take the values as kPlain, aligned as this one leaves them.
+    template <Take kTake>
+    __device__ __forceinline__ void read(F2 (&v)[4], uint8_t* stage, uint32_t row, int i, int t) const {
         stage += at;
         if (kCodes && scales) {
             const uint2 c = *reinterpret_cast<const uint2*>(stage + i * T * 8);
@@ -183,16 +188,20 @@ struct Mat {
         Unit<kF32> u;
         uint4 a = *reinterpret_cast<const uint4*>(stage + (kF32 ? 2 * i : i) * T * 16);
         uint4 b = kF32 ? *reinterpret_cast<const uint4*>(stage + (2 * i + 1) * T * 16) : a;
-        if (kRagged) {
+        if (kRagged && kTake != kPlain) {
             const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p + static_cast<uint64_t>(ld) * row)) & 15u;
             if (shift) {
                 uint4 next = shuffle_down(a);
                 if ((t & 31) == 31) next = *reinterpret_cast<const uint4*>(stage - t * 16 + kMore + (i * (T / 32) + t / 32) * 16);
                 if (kF32) {
-                    a = shifted(a, b, shift);
-                    b = shifted(b, next, shift);
+                    a = shifted_alike(a, b, shift);
+                    b = shifted_alike(b, next, shift);
                 } else {
-                    a = shifted(a, next, shift);
+                    a = shifted_alike(a, next, shift);
+                }
+                if (kTake == kKeep) {
+                    *reinterpret_cast<uint4*>(stage + (kF32 ? 2 * i : i) * T * 16) = a;
+                    if (kF32) *reinterpret_cast<uint4*>(stage + (2 * i + 1) * T * 16) = b;
                 }
             }
         }
@@ -220,10 +229,10 @@ __device__ __forceinline__ void store_unit(const Unit<kF32>& u, void* row, int i
     if (reinterpret_cast<uintptr_t>(x) & 15u) before = shuffle_up(b);
     const bool first = (t & 31) == 0, last = (t & 31) == 31;
     if (kF32) {
-        store16<4>(x, (i * T + t) * 32, width * 4, a, before, first, false);
-        store16<4>(x, (i * T + t) * 32 + 16, width * 4, b, a, false, last);
+        store16<4, true>(x, (i * T + t) * 32, width * 4, a, before, first, false);
+        store16<4, true>(x, (i * T + t) * 32 + 16, width * 4, b, a, false, last);
     } else {
-        store16<2>(x, (i * T + t) * 16, width * 2, a, before, first, last);
+        store16<2, true>(x, (i * T + t) * 16, width * 2, a, before, first, last);
     }
 }
 

@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             if (kRagged && i >= mine) break;
             if (s.w.p) {
                 F2 h[4], dx[4], f[4];
-                H.read(h, stage, row, i, t);
-                Dx.read(dx, stage, row, i, t);
+                H.template read<kKeep>(h, stage, row, i, t);
+                Dx.template read<kKeep>(dx, stage, row, i, t);
                 if (!kKept) main_factors<T>(f, s, i, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             }
             if (s.post.p) {
                 F2 y[4];
-                Y.read(y, stage, row, i, t);
+                Y.template read<kKeep>(y, stage, row, i, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) yy = fma2(y[k], y[k], yy);
             }
@@ -130,11 +130,11 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (kRagged && i >= mine) break;
-            Dh.read(d[i], stage, row, i, t);
+            Dh.template read<kOnce>(d[i], stage, row, i, t);
             if (s.w.p) {
                 F2 h[4], dx[4], f[4];
-                H.read(h, stage, row, i, t);
-                Dx.read(dx, stage, row, i, t);
+                H.template read<kPlain>(h, stage, row, i, t);
+                Dx.template read<kPlain>(dx, stage, row, i, t);
                 if (!kKept) main_factors<T>(f, s, i, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             store_unit<T, kF32, kRagged>(out, static_cast<uint8_t*>(p.dh_out) + static_cast<uint64_t>(p.dh_out_ld) * static_cast<uint32_t>(row), i, t, s.width);
             if (!has_y) continue;
             F2 y[4], f[4];
-            Y.read(y, stage, row, i, t);
+            if (kRagged && !s.post.p) Y.template read<kOnce>(y, stage, row, i, t);
+            else Y.template read<kPlain>(y, stage, row, i, t);
             if (!kKept) block_factors<T>(f, s, i, t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : 
             F2 f[4];
             if (s.post.p) {
                 F2 y[4];
-                Y.read(y, stage, row, i, t);
+                Y.template read<kPlain>(y, stage, row, i, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     f[k] = mul(fma2(mul(y[k], both(inverse_y)), both(-m), mul(d[i][k], both(rg))), both(inverse_y));

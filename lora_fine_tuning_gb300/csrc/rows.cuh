@@ -15,6 +15,19 @@ __device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, uint32_t s) {
     return make_uint4(__funnelshift_r(w[0], w[1], r), __funnelshift_r(w[1], w[2], r), __funnelshift_r(w[2], w[3], r),
                       __funnelshift_r(w[3], w[4], r));
 }
+// The same where `s` is a multiple of two and the same in the whole warp: a branch instead of selections.
+__device__ __forceinline__ uint4 shifted_alike(uint4 a, uint4 b, uint32_t s) {
+    const uint32_t r = (s & 3) * 8;
+    const auto words = [r](uint32_t p, uint32_t q, uint32_t u, uint32_t v, uint32_t w) {
+        return make_uint4(__funnelshift_r(p, q, r), __funnelshift_r(q, u, r), __funnelshift_r(u, v, r), __funnelshift_r(v, w, r));
+    };
+    switch (s >> 2) {
+        case 0: return words(a.x, a.y, a.z, a.w, b.x);
+        case 1: return words(a.y, a.z, a.w, b.x, b.y);
+        case 2: return words(a.z, a.w, b.x, b.y, b.z);
+        default: return words(a.w, b.x, b.y, b.z, b.w);
+    }
+}
 __device__ __forceinline__ uint4 shuffle_down(uint4 v) {
     return make_uint4(__shfl_down_sync(0xFFFFFFFFu, v.x, 1), __shfl_down_sync(0xFFFFFFFFu, v.y, 1),
                       __shfl_down_sync(0xFFFFFFFFu, v.z, 1), __shfl_down_sync(0xFFFFFFFFu, v.w, 1));
@@ -54,7 +67,8 @@ __device__ __forceinline__ void store_parts(uint8_t* x, uint4 v, int from, int t
 // Sixteen bytes to byte `at` of a row of `bytes`, whose 16 bytes before have another owner's `before` (none for the first of a warp's
 // share).  Where the row does not start on 16 bytes, the aligned 16 that begin in `before` are stored; the `last` of the share also
 // stores the rest of its own.
-template <int kSize>
+// kAlike: the warp's lanes are in one row.
+template <int kSize, bool kAlike>
 __device__ __forceinline__ void store16(uint8_t* row, int at, int bytes, uint4 v, uint4 before, bool first, bool last) {
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u), left = bytes - at;
     if (shift == 0) {
@@ -63,7 +77,7 @@ __device__ __forceinline__ void store16(uint8_t* row, int at, int bytes, uint4 v
         return;
     }
     if (!first && left + shift >= 16) {
-        *reinterpret_cast<uint4*>(row + at - shift) = shifted(before, v, 16 - shift);
+        *reinterpret_cast<uint4*>(row + at - shift) = kAlike ? shifted_alike(before, v, 16 - shift) : shifted(before, v, 16 - shift);
     } else {
         if (!first && left + shift > 0) store_parts<kSize>(row + at - 16, before, (16 - shift) / kSize, min(16, 16 + left) / kSize);
         if (left > 0) store_parts<kSize>(row + at, v, 0, min(16 - shift, left) / kSize);
