@@ -316,7 +316,11 @@ __device__ __forceinline__ void store_act8(Unit<false> u, const NormAct8& a, con
 
 // Rows that a CTA works on at once, and the CTAs of an SM that a kernel's registers are meant for: 80 (768 threads) or 128 (512) a thread.
 constexpr int rows_of(int T) { return T >= 256 ? 1 : 256 / T; }
-constexpr int per_sm(int threads, int T) { return T * rows_of(T) >= threads ? 1 : threads / (T * rows_of(T)); }
+// Ten warps for rows up to 5120 values go with two CTAs at 96 registers: 8192 x 5120, all gradients, 136 us where one CTA of
+// sixteen warps (a quarter of them with two units, the others with one) takes 146.
+constexpr int per_sm(int threads, int T) {
+    if (T == 320) return 2;
+    return T * rows_of(T) >= threads ? 1 : threads / (T * rows_of(T)); }
 constexpr int kFwdThreads = 512, kBwdThreads = 512, kSumsThreads = 512;
 
 // Sums of M values over the T threads of a row, the same in each of them.  Two buffers in turn: a buffer is written again only
@@ -419,6 +423,7 @@ auto by_width(int width, bool ragged, F&& f) {
     if (width <= 2048) return f(integral_constant<int, 128>(), integral_constant<int, 2>(), No());
     if (width <= 2560) return f(integral_constant<int, 160>(), integral_constant<int, 2>(), No());
     if (width <= 4096) return f(integral_constant<int, 256>(), integral_constant<int, 2>(), No());
+    if (width <= 5120) return f(integral_constant<int, 320>(), integral_constant<int, 2>(), No());
     if (width <= 8192) return f(integral_constant<int, 512>(), integral_constant<int, 2>(), No());
     return f(integral_constant<int, 512>(), integral_constant<int, 4>(), No());
 }
@@ -448,7 +453,7 @@ cudaError_t configure(F&& kernels) {
     const auto set = [&e](auto* k) {
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBudget);
     };
-    for (const int width : {256, 512, 1024, 2048, 2560, 4096, 8192, kNormMaxWidth})
+    for (const int width : {256, 512, 1024, 2048, 2560, 4096, 5120, 8192, kNormMaxWidth})
         for (const bool ragged : {false, true})
             by_width(width, ragged, [&](auto t, auto v, auto r) {
                 kernels(t, v, r, set);
