@@ -44,7 +44,7 @@ int norm_bwd_groups(int rows, int width, int sms) {
     const auto groups = [&](bool ragged) {
         return by_width(width, ragged, [&](auto t, auto, auto) {
             constexpr int T = decltype(t)::value, R = rows_of(T);
-            return std::min((rows + R - 1) / R, sms * per_sm(kSumsThreads, T));
+            return std::min((rows + R - 1) / R, sms * per_sm(T));
         });
     };
     return std::max(groups(false), groups(true));

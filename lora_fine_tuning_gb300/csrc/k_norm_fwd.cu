@@ -6,7 +6,7 @@ namespace lora {
 namespace {
 
 template <int T, int V, bool kF32, bool kRagged>
-__global__ void __launch_bounds__(T * rows_of(T), per_sm(kFwdThreads, T)) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+__global__ void __launch_bounds__(T * rows_of(T), per_sm(T)) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
     constexpr int R = rows_of(T);
     constexpr bool kKept = kept<T, V>();
     extern __shared__ __align__(16) uint8_t ring_memory[];
@@ -186,7 +186,7 @@ cudaError_t launch_norm_fwd(const NormFwd& given, int sms, cudaStream_t stream) 
         NormFwd p = given;
         p.at_y = stage_bytes_of(T, V, p.s.f32 ? 4 : 2, K);
         p.stage_bytes = p.at_y + (p.y ? stage_bytes_of(T, V, 2, K) : 0);
-        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(kFwdThreads, T), kept<T, V>());
+        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(T), kept<T, V>());
         p.stages = plan.stages;
         const int grid = std::min((p.s.rows + R - 1) / R, sms * plan.per_sm);
         return launch_pdl(p.s.f32 ? norm_fwd_kernel<T, V, true, K> : norm_fwd_kernel<T, V, false, K>, dim3(grid), dim3(T * R),

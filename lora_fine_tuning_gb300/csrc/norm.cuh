@@ -314,14 +314,11 @@ __device__ __forceinline__ void store_act8(Unit<false> u, const NormAct8& a, con
     if (c % kAct8Block == 0 && c / kAct8Block < s.scales_ld) scales[c / kAct8Block] = static_cast<uint8_t>(c < s.codes_ld ? e : 127u);
 }
 
-// Rows that a CTA works on at once, and the CTAs of an SM that a kernel's registers are meant for: 80 (768 threads) or 128 (512) a thread.
+// Rows that a CTA works on at once, and the CTAs of an SM: 512 threads at 128 registers.  (1024 threads of one
+// unit at 64 registers spill: the backward of 16384 x 8192 takes 405 us instead of 276.)  Ten warps for rows up to 5120 values go with
+// two CTAs at 96 registers: 8192 x 5120, all gradients, 136 us, where one CTA of sixteen warps takes 146.
 constexpr int rows_of(int T) { return T >= 256 ? 1 : 256 / T; }
-// Ten warps for rows up to 5120 values go with two CTAs at 96 registers: 8192 x 5120, all gradients, 136 us where one CTA of
-// sixteen warps (a quarter of them with two units, the others with one) takes 146.
-constexpr int per_sm(int threads, int T) {
-    if (T == 320) return 2;
-    return T * rows_of(T) >= threads ? 1 : threads / (T * rows_of(T)); }
-constexpr int kFwdThreads = 512, kBwdThreads = 512, kSumsThreads = 512;
+constexpr int per_sm(int T) { return T == 320 ? 2 : T * rows_of(T) >= 512 ? 1 : 512 / (T * rows_of(T)); }
 
 // Sums of M values over the T threads of a row, the same in each of them.  Two buffers in turn: a buffer is written again only
 // after the barrier of the sum in between, which every thread passes after it has read the first.

@@ -8,7 +8,7 @@ namespace lora {
 namespace {
 
 template <int T, int V, bool kF32, bool kSums, bool kRagged, bool kCodes>
-__global__ void __launch_bounds__(T * rows_of(T), per_sm(kSums ? kSumsThreads : kBwdThreads, T)) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
+__global__ void __launch_bounds__(T * rows_of(T), per_sm(T)) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
     constexpr int R = rows_of(T);
     constexpr bool kKept = kept<T, V>();
     extern __shared__ __align__(16) uint8_t ring_memory[];
@@ -290,7 +290,7 @@ cudaError_t launch_norm_bwd_form(NormBwd& p, int sms, cudaStream_t stream) {
         p.at_dh = place(true, wide);
         p.at_y = place(p.y || p.y8.codes, p.y8.codes ? codes : half);
         p.stage_bytes = at;
-        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(kSums ? kSumsThreads : kBwdThreads, T), kept<T, V>());
+        const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(T), kept<T, V>());
         p.stages = plan.stages;
         const int grid = std::min((p.s.rows + R - 1) / R, sms * plan.per_sm);
         p.groups = grid;
