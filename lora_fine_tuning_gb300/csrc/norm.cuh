@@ -155,7 +155,8 @@ struct Mat {
             if (shift && (t & 31) == 31) copy(stage - t * 16 + kMore + (i * (T / 32) + t / 32) * 16, kF32 ? 2 * u + 2 : u + 1);
         }
     }
-    // What no copy writes of a stage is zero from the start: the thread's units past the row's end, and all of a matrix that is not given.
+    // What no copy writes of a stage is zero from the start: the thread's units past the row's end, and all of a matrix that is not given,
+    // the last lanes' further bytes among it.
     __device__ __forceinline__ void clear(uint8_t* stage) const {
         const int size = kCodes && scales ? 8 : 8 * kSize;
 #pragma unroll
@@ -165,6 +166,8 @@ struct Mat {
             if (!(kCodes && scales)) x[1] = make_uint2(0u, 0u);
             if (kF32 && !(kCodes && scales)) x[2 * T] = x[2 * T + 1] = make_uint2(0u, 0u);
             if (kCodes && scales) *reinterpret_cast<uint32_t*>(stage + at + V * T * 8 - threadIdx.x % T * 4 + i * T * 4) = 0u;
+            if (kRagged && !p && (threadIdx.x & 31) == 31)
+                *reinterpret_cast<uint4*>(stage + at - threadIdx.x % T * 16 + kMore + (i * (T / 32) + threadIdx.x % T / 32) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
     // All lanes of a warp take part.

@@ -155,7 +155,10 @@ lora_status norm_bwd(const lora_norm* norm, const lora_bf16* dx, const void* dh,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     p.dx = dx, p.dh = dh, p.h = h, p.y = y, p.dh_out = dh_out, p.dy = dy;
     p.s.ragged = c.ragged;
-    p.dx_ld = norm->dx * 2, p.dh_ld = norm->dh * size, p.h_ld = norm->h * size, p.y_ld = norm->y * 2, p.dh_out_ld = norm->dh_out * size, p.dy_ld = norm->dy * 2;
+    // (a matrix that is not given has no stride: nothing of its rows is shifted)
+    const auto bytes = [](const void* q, int64_t ld, int of) { return q ? ld * of : int64_t{0}; };
+    p.dx_ld = bytes(dx, norm->dx, 2), p.dh_ld = bytes(dh, norm->dh, size), p.h_ld = bytes(h, norm->h, size), p.y_ld = bytes(y, norm->y, 2);
+    p.dh_out_ld = norm->dh_out * size, p.dy_ld = bytes(dy, norm->dy, 2);
     p.dw = dw, p.dpost = dpost_w, p.dgate = dgate, p.drow = drow_gate;
     p.part = sums ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256) : nullptr;
     auto* launch = h8 || y8 ? (sums ? launch_norm_bwd8_sums : launch_norm_bwd8) : (sums ? launch_norm_bwd_sums : launch_norm_bwd);
