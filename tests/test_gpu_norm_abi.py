@@ -83,3 +83,36 @@ def test_no_gradient_of_the_stream_is_one_of_zeros(width, stream, eight):
     got = backward(st, stream, None, eight=eight)
     for k in OUTPUTS:
         assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("stream", [BF, F32])
+@pytest.mark.parametrize("width", [97, 2050, 4096, 9001])
+def test_outputs_left_out(width, stream):
+    st = inputs(9, width, stream)
+    dh = torch.ones_like(st["h"])
+    want = backward(st, stream, dh)
+    for leave in (("dy",), ("dy", "drow_gate"), ("dw", "dgate"), ("dpost_w",), OUTPUTS[1:], OUTPUTS[2:]):
+        got = backward(st, stream, dh, leave)
+        assert len(got) == len(OUTPUTS) - len(leave)
+        for k, t in got.items():
+            assert torch.equal(t, want[k]), (k, leave)
+
+
+@pytest.mark.parametrize("stream", [BF, F32])
+@pytest.mark.parametrize("width", [97, 200, 2050, 4096, 9001])
+def test_the_norm_in_8_bits_alone(width, stream):
+    """x NULL beside x8: the codes and scales of the call that also writes x."""
+    st = inputs(9, width, stream)
+
+    def forward(x):
+        h_out, x8 = torch.empty_like(st["h"]), api.act8(9, width)
+        x8.codes.fill_(77), x8.scales.fill_(77)
+        native.check("norm_fwd", native.lib().norm_fwd(norm(st, stream), ptr(st["h"]), ptr(st["y"]), ptr(h_out), ptr(x), kept(x8), None, None,
+                                                       torch.cuda.current_stream().cuda_stream))
+        return h_out, x8.codes, x8.scales
+
+    x = torch.empty(9, width, dtype=BF, device="cuda")
+    want = forward(x)
+    assert all(torch.equal(a, b) for a, b in zip(forward(None), want))
+    of_x = api.act8_store(x)
+    assert torch.equal(want[1], of_x.codes) and torch.equal(want[2], of_x.scales)
