@@ -15,7 +15,6 @@
 #include "host.h"
 #include "kernels.h"
 #include "lora.h"
-#include "norm.h"
 #include "plan.h"
 
 namespace lora {
@@ -124,9 +123,7 @@ lora_status device_setup(int* sms_out) {
             if (!cuda_ok(down_configure()) || !cuda_ok(gemm2_configure()) ||
                 !cuda_ok(dsdb_configure()) ||
                 !cuda_ok(da_configure()) || !cuda_ok(dora_configure()) || !cuda_ok(attn_fwd_configure()) ||
-                !cuda_ok(attn_bwd_configure()) || !cuda_ok(norm_fwd_configure()) ||
-                !cuda_ok(norm_bwd_configure()) || !cuda_ok(norm_bwd_sums_configure()) ||
-                !cuda_ok(norm_bwd8_configure()) || !cuda_ok(norm_bwd8_sums_configure()))
+                !cuda_ok(attn_bwd_configure()))
                 d.status = LORA_ECUDA;
         }
         if (d.status == LORA_OK && g_encode == nullptr) {

@@ -18,7 +18,8 @@ bool cuda_ok(cudaError_t e);
         if (!cuda_ok(expr)) return LORA_ECUDA;   \
     } while (0)
 
-// First use of the current device: checks its architecture and configures every kernel.  *sms: its SM count.
+// First use of the current device: checks its architecture and configures every kernel but the norms', which their first launches do.
+// *sms: its SM count.
 lora_status device_setup(int* sms);
 
 // Limit of the kernels' bounded waits (lora_set_wait_limit_ns).

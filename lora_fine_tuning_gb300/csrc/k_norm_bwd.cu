@@ -3,8 +3,6 @@
 
 namespace lora {
 
-cudaError_t norm_bwd_configure() { return configure_form<false, false>(); }
-
 cudaError_t launch_norm_bwd(NormBwd& p, int sms, cudaStream_t stream) { return launch_norm_bwd_form<false, false>(p, sms, stream); }
 
 }  // namespace lora

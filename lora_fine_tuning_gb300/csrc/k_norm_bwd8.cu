@@ -3,8 +3,6 @@
 
 namespace lora {
 
-cudaError_t norm_bwd8_configure() { return configure_form<false, true>(); }
-
 cudaError_t launch_norm_bwd8(NormBwd& p, int sms, cudaStream_t stream) { return launch_norm_bwd_form<false, true>(p, sms, stream); }
 
 }  // namespace lora

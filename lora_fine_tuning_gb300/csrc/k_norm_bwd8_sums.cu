@@ -3,8 +3,6 @@
 
 namespace lora {
 
-cudaError_t norm_bwd8_sums_configure() { return configure_form<true, true>(); }
-
 cudaError_t launch_norm_bwd8_sums(NormBwd& p, int sms, cudaStream_t stream) { return launch_norm_bwd_form<true, true>(p, sms, stream); }
 
 }  // namespace lora

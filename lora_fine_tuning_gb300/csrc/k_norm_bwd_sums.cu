@@ -50,8 +50,6 @@ int norm_bwd_groups(int rows, int width, int sms) {
     return std::max(groups(false), groups(true));
 }
 
-cudaError_t norm_bwd_sums_configure() { return configure_form<true, false>(); }
-
 cudaError_t launch_norm_bwd_sums(NormBwd& p, int sms, cudaStream_t stream) {
     return launch_norm_bwd_form<true, false>(p, sms, stream);
 }

@@ -170,15 +170,6 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(T)) norm_fwd_kernel(con
 
 }  // namespace
 
-cudaError_t norm_fwd_configure() {
-    return configure([](auto t, auto v, auto r, auto set) {
-        constexpr int T = decltype(t)::value, V = decltype(v)::value;
-        constexpr bool K = decltype(r)::value;
-        set(norm_fwd_kernel<T, V, false, K>);
-        set(norm_fwd_kernel<T, V, true, K>);
-    });
-}
-
 cudaError_t launch_norm_fwd(const NormFwd& given, int sms, cudaStream_t stream) {
     return by_width(given.s.width, given.s.ragged, [&](auto t, auto v, auto r) {
         constexpr int T = decltype(t)::value, V = decltype(v)::value, R = rows_of(T);
@@ -189,8 +180,10 @@ cudaError_t launch_norm_fwd(const NormFwd& given, int sms, cudaStream_t stream) 
         const RingPlan plan = ring_plan(R * p.stage_bytes, per_sm(T), kept<T, V>());
         p.stages = plan.stages;
         const int grid = std::min((p.s.rows + R - 1) / R, sms * plan.per_sm);
-        return launch_pdl(p.s.f32 ? norm_fwd_kernel<T, V, true, K> : norm_fwd_kernel<T, V, false, K>, dim3(grid), dim3(T * R),
-                          R * p.stages * p.stage_bytes, stream, p);
+        auto* k = p.s.f32 ? norm_fwd_kernel<T, V, true, K> : norm_fwd_kernel<T, V, false, K>;
+        static std::atomic<uint64_t> ready[2];   // of this form, by the stream's type
+        const cudaError_t e = let_rings(k, ready[p.s.f32 ? 1 : 0]);
+        return e != cudaSuccess ? e : launch_pdl(k, dim3(grid), dim3(T * R), R * p.stages * p.stage_bytes, stream, p);
     });
 }
 

@@ -28,6 +28,7 @@
 #include "norm.h"
 #include "rows.cuh"
 
+#include <atomic>
 #include <type_traits>
 
 namespace lora {
@@ -446,19 +447,16 @@ RingPlan ring_plan(int cta_bytes, int most, bool kept) {
 // Bytes of a stage that a matrix takes: its units and, for ragged rows, 16 for each warp's last lane.
 int stage_bytes_of(int T, int V, int size, bool ragged) { return V * T * 8 * size + (ragged ? V * (T / 32) * 16 : 0); }
 
-// Lets every form of a kernel use the rings' shared memory.
-template <class F>
-cudaError_t configure(F&& kernels) {
-    cudaError_t e = cudaSuccess;
-    const auto set = [&e](auto* k) {
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBudget);
-    };
-    for (const int width : {256, 512, 1024, 2048, 2560, 4096, 5120, 8192, kNormMaxWidth})
-        for (const bool ragged : {false, true})
-            by_width(width, ragged, [&](auto t, auto v, auto r) {
-                kernels(t, v, r, set);
-                return 0;
-            });
+// Lets a form of a kernel use the rings' shared memory, on its first launch on a device (below 64, as device_setup has it); ready: the devices that
+// had one.  All 140 forms at once take 26 ms, which the first call of any operator would wait for.
+template <class K>
+cudaError_t let_rings(K* kernel, std::atomic<uint64_t>& ready) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    const uint64_t bit = uint64_t{1} << (device & 63);
+    if (e != cudaSuccess || (ready.load(std::memory_order_acquire) & bit)) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBudget);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
     return e;
 }
 

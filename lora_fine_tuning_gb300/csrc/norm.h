@@ -61,11 +61,6 @@ struct NormBwd {
 // The most groups of rows that the backward sums over: the partial sums' first extent.
 int norm_bwd_groups(int rows, int width, int sms);
 
-cudaError_t norm_fwd_configure();
-cudaError_t norm_bwd_configure();
-cudaError_t norm_bwd_sums_configure();
-cudaError_t norm_bwd8_configure();
-cudaError_t norm_bwd8_sums_configure();
 cudaError_t launch_norm_fwd(const NormFwd& p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_bwd(NormBwd& p, int sms, cudaStream_t stream);        // without the weights' gradients
 cudaError_t launch_norm_bwd_sums(NormBwd& p, int sms, cudaStream_t stream);   // with their sums over each CTA's rows

@@ -264,16 +264,6 @@ __global__ void __launch_bounds__(T * rows_of(T), per_sm(T)) norm_bwd_kernel(con
 }
 
 template <bool kSums, bool kCodes>
-cudaError_t configure_form() {
-    return configure([](auto t, auto v, auto r, auto set) {
-        constexpr int T = decltype(t)::value, V = decltype(v)::value;
-        constexpr bool K = decltype(r)::value;
-        set(norm_bwd_kernel<T, V, false, kSums, K, kCodes>);
-        set(norm_bwd_kernel<T, V, true, kSums, K, kCodes>);
-    });
-}
-
-template <bool kSums, bool kCodes>
 cudaError_t launch_norm_bwd_form(NormBwd& p, int sms, cudaStream_t stream) {
     return by_width(p.s.width, p.s.ragged, [&](auto t, auto v, auto r) {
         constexpr int T = decltype(t)::value, V = decltype(v)::value, R = rows_of(T);
@@ -297,7 +287,9 @@ cudaError_t launch_norm_bwd_form(NormBwd& p, int sms, cudaStream_t stream) {
         auto* k = p.s.f32 ? norm_bwd_kernel<T, V, true, kSums, K, kCodes> : norm_bwd_kernel<T, V, false, kSums, K, kCodes>;
         // the rows' rings, in whose place the CTA's sums are gathered at the end
         const int memory = std::max<int>(R * p.stages * p.stage_bytes, kSums ? (R - 1) * 2 * T * V * 8 * 4 : 0);
-        return launch_pdl(k, dim3(grid), dim3(T * R), memory, stream, p);
+        static std::atomic<uint64_t> ready[2];   // of this form, by the stream's type
+        const cudaError_t e = let_rings(k, ready[p.s.f32 ? 1 : 0]);
+        return e != cudaSuccess ? e : launch_pdl(k, dim3(grid), dim3(T * R), memory, stream, p);
     });
 }
 
