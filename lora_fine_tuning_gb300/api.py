@@ -1009,7 +1009,7 @@ def _turned(on: _On, name: str, t: torch.Tensor, rows: int, heads: int, d: int):
 
 
 def _positions(on: _On, positions, rows: int) -> int:
-    dtype = positions.dtype
+    dtype = None if positions is None else positions.dtype
     if (dtype is not torch.int64 and dtype is not torch.int32) or not positions.is_contiguous() or positions.shape != (rows,):
         raise ValueError(f"positions must be a contiguous CUDA int64 or int32 vector of {rows}")
     on.check("positions", positions)
@@ -1018,8 +1018,10 @@ def _positions(on: _On, positions, rows: int) -> int:
 
 def _rope(name, Q, K, positions, rope, Q_out, K_out, stream):
     ref = Q if Q is not None else K
+    if ref is None:
+        raise ValueError("Q or K is needed")
     on = _On(ref, stream)
-    if ref.dim() != 3:
+    if ref.dim() != 3 or (K is not None and K.dim() != 3):
         raise ValueError("Q and K are rows x heads x head_dim")
     rows, _, d = ref.shape
     bits = _positions(on, positions, rows)
@@ -1062,8 +1064,10 @@ def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_ou
     """rope_fwd on the way into a cache: each row's turned K and its V go to row slots[row] (int64, on the device) of K_cache and
     V_cache (cache rows x kv_heads x head_dim, what attn_fwd reads; pages are runs of such rows).  A row whose slot is outside
     the cache, -1 for example, is not stored; slots inside it must differ.  Returns the turned Q."""
+    if Q is None or K is None or V is None or slots is None or K_cache is None or V_cache is None:
+        raise ValueError("Q, K, V, slots, K_cache and V_cache are needed")
     on = _On(Q, stream)
-    if Q.dim() != 3 or K.dim() != 3:
+    if Q.dim() != 3 or K.dim() != 3 or K_cache.dim() != 3:
         raise ValueError("Q, K, V and the caches are rows x heads x head_dim")
     rows, hq, d = Q.shape
     hk, cache_rows = K.shape[1], K_cache.shape[0]
