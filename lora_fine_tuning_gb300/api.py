@@ -895,14 +895,15 @@ def norm_bwd(dx, h, w=None, *, dh=None, y=None, post_w=None, gate=None, row_gate
              dgate=None, drow_gate=None, ws=None, stream=None) -> NormGrads:
     """Gradients of norm_fwd from dx and dh, those of x and h' (dh None: zero; dx and h None without w).  h: the forward's h', y its
     y, each a tensor or what act8_store or the forward kept of it in 8 bits (Act8).  Returns NormGrads: dh (of h, like
-    dh or h), dy, and with want_weights the gradients of w, post_w, gate and row_gate that were given, fp32."""
+    dh or h; bf16 where there are only 8 bits, unless dh_out is fp32), dy, and with want_weights the gradients of w, post_w, gate and row_gate that were given, fp32."""
     ref = h if h is not None else dh
     if ref is None:
         raise ValueError("the gradient of x or of the stream is needed")
     on = _On(ref.codes if isinstance(ref, Act8) else ref, stream)
     rows, width = ref.shape
-    # the stream's type: that of its gradient or of itself, bf16 where only 8 bits are given
-    stream_dtype = dh.dtype if dh is not None else torch.bfloat16 if isinstance(ref, Act8) else ref.dtype
+    # the stream's type: that of its gradient or of itself; where only 8 bits are given that of dh_out, or bf16
+    typed = dh if dh is not None else dh_out if isinstance(ref, Act8) else ref
+    stream_dtype = torch.bfloat16 if typed is None else typed.dtype
     if stream_dtype not in _DTYPES:
         raise TypeError("the stream is bfloat16 or float32")
     dx_ld = dh_ld = h_ld = y_ld = dy_ld = 0

@@ -391,3 +391,16 @@ def test_refusals():
                    dict(ws=torch.zeros(512, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(native.LoraError):
             api.norm_bwd(dx, h, **{**rest, **change})
+
+
+@pytest.mark.parametrize("width", [96, 97, 4096])
+@pytest.mark.parametrize("stream", [BF, F32])
+def test_stream_type_from_8_bits_alone(width, stream):
+    """A stream kept in 8 bits without a gradient of its own, as the last norm of a decoder has it: dh_out gives the stream's type."""
+    st, dx, dh = inputs(12, width, stream=stream, post=True)
+    h8 = api.act8_store(st["h"].bfloat16())
+    rest = {k: t for k, t in st.items() if k != "h"}
+    want = api.norm_bwd(dx, h8, dh=torch.zeros_like(dh), **rest)
+    got = api.norm_bwd(dx, h8, dh_out=torch.empty_like(dh), **rest)
+    assert got.dh.dtype == stream and all(torch.equal(a, b) for a, b in zip(got, want) if b is not None)
+    assert api.norm_bwd(dx, h8, **rest).dh.dtype == BF

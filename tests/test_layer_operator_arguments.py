@@ -1,10 +1,10 @@
-"""Calls of the rotary positions that lack an operand end in an error that names it, without a GPU: tensors are stand-ins, and a library that is
+"""Arguments of rotary positions and norms that are missing or decide a type, without a GPU: tensors are stand-ins, and where a call is refused a library that is
 reached fails the test."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from lora_fine_tuning_gb300 import api  # noqa: E402
+from lora_fine_tuning_gb300 import api, native  # noqa: E402
 from tests.test_layer_operator_devices import BF16, C, KV, Q, ROPE, ROWS, Tensor, lib  # noqa: E402, F401
 
 OUT = {api.rope_fwd: ("Q_out", "K_out"), api.rope_bwd: ("dQ_out", "dK_out")}
@@ -41,3 +41,15 @@ def test_no_positions(lib):  # noqa: F811
     with pytest.raises(ValueError, match="positions"):
         api.rope_fwd(Tensor(*Q), Tensor(*KV), None, ROPE, Q_out=Tensor(*Q), K_out=Tensor(*KV))
     assert not lib.called
+
+
+@pytest.mark.parametrize("dtype,code", [(torch.bfloat16, 0), (torch.float32, 1)])
+def test_stream_type_where_only_8_bits_are_given(lib, monkeypatch, dtype, code):  # noqa: F811
+    """Without the stream's gradient, dh_out alone says what type the stream has."""
+    seen = []
+    monkeypatch.setattr(lib, "norm_bwd", lambda norm, *rest: seen.append(native.Norm.from_buffer_copy(norm).stream_dtype) or 0)
+    h8, dh = api.Act8(Tensor((6, 64), torch.int8), Tensor((6, 4), torch.uint8), 64), Tensor((6, 64), dtype)
+    g = api.norm_bwd(Tensor((6, 64), BF16), h8, Tensor((64,), BF16), want_weights=False, dh_out=dh)
+    assert seen == [code] and g.dh is dh
+    with pytest.raises(TypeError):
+        api.norm_bwd(Tensor((6, 64), BF16), h8, Tensor((64,), BF16), want_weights=False, dh_out=Tensor((6, 64), torch.float16))
