@@ -1,8 +1,8 @@
-"""Adapters on a small decoder, from the library's operators alone: trained with what the backward needs kept in 8 bits, then generating
-into a paged cache.
+"""Adapters on a small decoder, from the library's operators alone: trained with the inputs of norms and Q/K/V projections kept in 8 bits, then
+generating into a cache of pages.
 
-    python examples/decoder_layers.py                 # inputs of layers and norms kept in 8 bits
-    python examples/decoder_layers.py --keep bf16     # kept as they are
+    python examples/decoder_layers.py                 # these inputs kept in 8 bits; Q, K, V and the attention's output in bf16
+    python examples/decoder_layers.py --keep bf16     # all of them in bf16
 
 Each layer: the stream's norm, a frozen fused Q/K/V projection with an adapter, rotary positions in place, causal attention over the packed
 samples, a frozen output projection with an adapter, whose output joins the stream normed, gated and scaled, in one call with the
@@ -57,7 +57,7 @@ class Decoder:
 
     def forward(self, tokens, positions, seqs, seed, dropout, keep):
         """Logits, and what the backward needs: of each layer its input x, the stream h that x is the norm of, and its output y (in 8 bits with
-        keep="8 bits"), and of its attention Q, K, V, O and their statistics."""
+        keep="8 bits"), and as they are Q, K, V, O (the output projection's input), the attention's statistics and the adapters' S."""
         rows, eight = len(tokens), keep == "8 bits"
 
         def room():

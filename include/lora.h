@@ -439,7 +439,7 @@ lora_status act8_load(const lora_act8* in, int64_t rows, int64_t width, lora_bf1
 
 /* The layer's backward from an input in 8 bits: multi_lora_bwd and lora_bwd with X8 (m x k) in the place of X.  Of X the backward
  * needs dA = (X .* D)^T dS only, and code * scale is a bf16 value: the results are those of the bf16 call on
- * what act8_load gives. */
+ * what act8_load gives, dS rounded to bf16 for that product as there. */
 lora_status multi_lora_bwd_act8(const lora_bf16* dY, const lora_act8* X8, const lora_bf16* W,
                                 const lora_adapter* adapters, int32_t n_adapters, const lora_segment* segments,
                                 int32_t n_segments, uint64_t seed, int64_t m, int64_t k, int64_t n,
@@ -541,8 +541,9 @@ lora_status rope_bwd(const lora_bf16* dQ, const lora_bf16* dK, const void* posit
                      const lora_rope* rope, lora_bf16* dQ_out, lora_bf16* dK_out, void* stream);
 
 /* rope_fwd on the way into a cache: the row's turned K and its V go to row slots[row] (device, int64) of K_cache and V_cache
- * (cache_rows x kv_heads x head_dim, strides k_out and v_out), the rows that attn_fwd reads.  A cache of pages is such
- * a matrix, with slot = page * page rows + row of the page.  A row whose slot is outside [0, cache_rows) is not stored (its Q_out
+ * (cache_rows x kv_heads x head_dim, strides k_out and v_out).  A cache of pages is such a matrix, with slot = page * page rows +
+ * row of the page; attn_fwd reads one run of its rows a sequence (k_start, k_rows), so those of requests whose pages follow each
+ * other.  A row whose slot is outside [0, cache_rows) is not stored (its Q_out
  * is written).  Slots inside it must differ from each other: of two rows with one slot, either may be left there, or parts
  * of both. */
 lora_status rope_append(const lora_bf16* Q, const lora_bf16* K, const lora_bf16* V, const void* positions,

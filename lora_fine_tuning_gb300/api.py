@@ -1063,8 +1063,9 @@ def rope_bwd(dQ, dK, positions, rope: Rope, *, dQ_out=None, dK_out=None, stream=
 
 def rope_append(Q, K, V, positions, slots, K_cache, V_cache, rope: Rope, *, Q_out=None, stream=None):
     """rope_fwd on the way into a cache: each row's turned K and its V go to row slots[row] (int64, on the device) of K_cache and
-    V_cache (cache rows x kv_heads x head_dim, what attn_fwd reads; pages are runs of such rows).  A row whose slot is outside
-    the cache, -1 for example, is not stored; slots inside it must differ.  Returns the turned Q."""
+    V_cache (cache rows x kv_heads x head_dim; pages are runs of such rows, and attn_fwd reads one run a sequence: requests whose
+    pages follow each other).  A row whose slot is outside the cache, -1 for example, is not stored; slots inside it
+    must differ.  Returns the turned Q."""
     if Q is None or K is None or V is None or slots is None or K_cache is None or V_cache is None:
         raise ValueError("Q, K, V, slots, K_cache and V_cache are needed")
     on = _On(Q, stream)

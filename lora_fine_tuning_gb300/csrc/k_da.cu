@@ -5,9 +5,9 @@
 // it: dA = X_hat^T dS = (X .* D)^T (q dS) = (X .* D)^T dSq.
 // Each unit is (adapter a, 128-feature block, one of a's 128-row tiles): two
 // TMA boxes of X (128 tokens x 64 features, 128B swizzle) plus the tile's dSq
-// rows.  Warps 2..9 zero the dropped X elements in shared memory (Philox,
-// exactly as the forward) in two groups of four warps that take alternate
-// stages, a thread one token row of its stage (sixteen independent Philox
+// rows.  Warps from 2 on zero the dropped X elements in shared memory (Philox,
+// exactly as the forward) in two to four groups of four warps that take the
+// stages in turn, a thread one token row of its stage (sixteen independent Philox
 // calls, eight at a time), warp 1 issues tcgen05.mma with both operands
 // MN-major (M = 128 features, N = rank, K = 128 tokens) accumulating over a
 // CTA's run of tiles of one (adapter, feature block), and the run's partial is
@@ -16,6 +16,8 @@
 // them into the two bf16 boxes, masked on the way: code * scale is a bf16 value, so the product is that of the bf16 X.  Their arithmetic
 // (some 600 instructions a row of a stage) is what bounds that form: 8192 x 14336 at rank 16 64 us, 57 from bf16; four groups
 // of warps where four stages fit.
+// dSq is dS rounded once to bf16, from its fp32 sums: the tensor core takes both operands in X's type.  It is the rounding of a value
+// among thousands that dA adds up, at most 2^-8 of each, and measures 0.0015 to 0.0017 of dA's norm, as much as dA's own rounding (0.0016).
 // finalize_da then writes dA in bf16 and clears the accumulators and dSq
 // (dA is dSq's last reader), so the workspace ends the call all zeros.
 #include "act8.cuh"

@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kQHeads = kRopeQHeads, kKHeads = kRopeKHeads;   // of a lane, at most
-// CTAs of an SM: 128 registers a thread, 168 with V.  Fewer spill: 8192 rows of 40 heads 38 us with five CTAs, 33 with four;
+// CTAs of an SM: 128 registers a thread (the widest form spills 16 bytes), 168 with V.  Fewer spill more: 8192 rows of 40 heads 38 us with five CTAs, 33 with four;
 // 5000 rows into a cache 20 us with four, 18 with three.
 constexpr int ctas_of(bool append) { return append ? 3 : 4; }
 

@@ -9,9 +9,9 @@
 //   dw = sum_t dx n,  K = sum_t row_gate dh' v,  dgate = res P K,  dpost_w = res gate K,  drow_gate = sum_j z v
 //
 // Bound by memory.  T threads share a row (a warp up to 512 values, 512 threads up to 16384), each with V units of eight
-// consecutive values.  A row comes into shared memory by asynchronous copies two or three rows ahead, a thread's own units by its own
-// copies, so that nothing but these is waited for and a CTA's 128 registers hold the factors W and res gate P and the backward's
-// sums over rows instead of loads under way.  Rows are worked on in turn with one exchange over the row's threads each: what is summed
+// consecutive values.  A row comes into shared memory by asynchronous copies up to three rows ahead (one where two stages fit,
+// none above 8192 values: ring_plan), a thread's own units by its own copies, so that nothing but these is waited for and a CTA's 128
+// registers hold the factors W and res gate P and the backward's sums over rows instead of loads under way.  Rows are worked on in turn with one exchange over the row's threads each: what is summed
 // over a row (its squares, t h, q v) is added up together with the first sums of the next row.
 // Sums over a row are fp32, by pairs; the sum of squares is formed anew on values 2^-80 their size where it leaves fp32's range.
 // The CTAs' sums over rows are added by a second kernel in a fixed order.
@@ -85,7 +85,8 @@ enum Take { kOnce, kKeep, kPlain };
 // One matrix that is read: where its rows are, and where a stage has a row's copies (both from thread t's first unit on).
 // kRagged: its rows need not start on 16 bytes or be whole units.  A row is then copied by the aligned 16 bytes that it lies in, its first ones
 // from before the row (inside the same 16); a warp's last lane also copies the 16 bytes after its unit, the other lanes get them
-// from their neighbour.  The forms without it have none of the arithmetic for that (1112 instead of 715 instructions a row and warp of the backward).
+// from their neighbour.  The forms without it have none of the arithmetic for that (715 instructions a row and warp
+// of the backward of 4864 x 8192, 1544 of 4864 x 8191).
 // kCodes: it may be in 8 bits.
 template <int T, int V, bool kF32, bool kRagged, bool kCodes>
 struct Mat {
@@ -320,7 +321,8 @@ __device__ __forceinline__ void store_act8(Unit<false> u, const NormAct8& a, con
 
 // Rows that a CTA works on at once, and the CTAs of an SM: 512 threads at 128 registers.  (1024 threads of one
 // unit at 64 registers spill: the backward of 16384 x 8192 takes 405 us instead of 276.)  Ten warps for rows up to 5120 values go with
-// two CTAs at 96 registers: 8192 x 5120, all gradients, 136 us, where one CTA of sixteen warps takes 146.
+// two CTAs at 96 registers: 8192 x 5120, all gradients, 136 us, where one CTA of sixteen warps takes 146, although
+// the forms with sums then spill 172 to 244 bytes a thread.
 constexpr int rows_of(int T) { return T >= 256 ? 1 : 256 / T; }
 constexpr int per_sm(int T) { return T == 320 ? 2 : T * rows_of(T) >= 512 ? 1 : 512 / (T * rows_of(T)); }
 

@@ -1,4 +1,4 @@
-// Launch plans of the norms around a block (k_norm.cu), filled by norm_api.cu.
+// Launch plans of the norms around a block (norm.cuh, k_norm_fwd.cu, norm_bwd.cuh), filled by norm_api.cu.
 #pragma once
 
 #include <cstdint>

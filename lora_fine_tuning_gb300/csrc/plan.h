@@ -265,7 +265,7 @@ struct DaParams {
     const uint8_t* scales;             // X in 8 bits: its blocks' scales (rows of scales_ld bytes); null: X is bf16
     int64_t scales_ld;
     uint32_t off_codes;                // and where a stage has its codes (a multiple of 1024: the swizzle's period)
-    int32_t groups;                    // mask groups of four warps (2 or 3); stages % groups == 0
+    int32_t groups;                    // mask groups of four warps (2 or 3; 4 too in 8 bits); stages % groups == 0
     Slots sl;                          // deterministic mode: dA partials per (adapter * nfb + feature block, CTA) slot
 };
 
